@@ -63,6 +63,7 @@ typedef enum pa_dtype { PA_FP16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_FP8_E5M2 =
 #define PA_DEVERR_GROUP     32u  /* prefix group malformed, or a member does not share the prefix */
 #define PA_DEVERR_Q_RANGE   64u  /* a bf16 query element beyond fp16's finite range (8-bit and 4-bit
                                     caches, which compute in fp16); its rows are not finite */
+#define PA_DEVERR_PATH      128u /* accepted path not ascending, or past its tree */
 
 typedef struct pa_shape {
     int32_t num_seqs;            /* N: sequences in the batch (>= 0) */
@@ -201,6 +202,87 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
                           void* stream);
 
 /*
+ * Tree attention over the cache: pa_decode_multi for drafted tokens that form a
+ * tree instead of a chain (speculative verification of several continuations
+ * in one pass -- letsbuildsolutions "How LLM Inference Engines Work",
+ * speculative decoding).
+ *
+ * Sequence b brings n_b = q_start[b + 1] - q_start[b] nodes, its last n_b
+ * cached tokens.  With base = context_lens[b] - n_b, node i (row q_start[b] + i)
+ * sees every key t < base, and the key base + j of node j exactly when bit j of
+ * tree_masks[q_start[b] + i] is set (j < n_b; higher bits are ignored).  A node
+ * sees itself only when its own bit is set, and node order is free, so any
+ * visibility among the new tokens can be expressed.
+ *     s_t  = scale * <q[q_start[b] + i, h, :], K(b, t, h / g)>,  t visible
+ *     out[q_start[b] + i, h, :] = sum_t softmax(s)_t * V(b, t, h / g)
+ * accumulated in fp32; a node that sees no key gives a zero row.  A K or V of a
+ * node that holds infinities or NaN leaves the rows that do not see that node
+ * untouched; a row that sees a V of a node with an infinity or NaN is NaN.
+ *
+ *   max_nodes     largest n_b of the call, 1..64
+ *   total_q       T: rows of q, out and tree_masks (q_start[N] should equal it)
+ *   tree_masks    device uint64 [T]
+ *   others        as pa_decode_multi; workspace: pa_decode_tree_workspace_bytes
+ *
+ * Malformed sizes set PA_DEVERR_CONTEXT and NaN rows as in pa_decode_multi.
+ * Supported shapes as pa_decode (16-bit).  Results are deterministic and
+ * independent of block placement.  Three launches on `stream`.
+ */
+size_t pa_decode_tree_workspace_bytes(const pa_shape* shape, int32_t max_nodes);
+
+pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total_q, const void* q,
+                         const int32_t* q_start, const uint64_t* tree_masks, const void* k_pool,
+                         const void* v_pool, const int32_t* block_tables, const int32_t* context_lens,
+                         float scale, void* out, void* workspace, size_t workspace_bytes,
+                         uint32_t* err_word, void* stream);
+
+/*
+ * The drafted path that the target model agrees with.  Node 0 of a tree is the
+ * sequence's newest token (always accepted); the parent of node i > 0 is the
+ * highest node below i in its tree_masks entry.  draft_tokens[i] is node i's
+ * token, target_tokens[i] the token that the target model chose after node i.
+ * A node matches when its token is its parent's target token; of a parent's
+ * matching children the lowest counts; a node is accepted when it and every
+ * node below it on its way (its mask) is node 0 or such a child.
+ *
+ *   path              int32 [N][max_nodes]  accepted nodes in ascending order, then -1
+ *   num_accepted      int32 [N]             how many (0 for a sequence without nodes)
+ *   next_tokens       int64 [N]             the target token after the last accepted node
+ *                                           (-1 for a sequence without nodes)
+ *   new_context_lens  int32 [N]             context_lens - n_b + num_accepted
+ *   q_start, tree_masks, context_lens       as pa_decode_tree; tokens int64 [T]
+ *
+ * A malformed sequence (sizes as in pa_decode_multi) sets PA_DEVERR_CONTEXT and
+ * answers as one without nodes.  new_context_lens may be context_lens itself.
+ * One launch.
+ */
+pa_status pa_tree_verify(int32_t num_seqs, int32_t max_nodes, int32_t total_q, const int32_t* q_start,
+                         const uint64_t* tree_masks, const int64_t* draft_tokens,
+                         const int64_t* target_tokens, const int32_t* context_lens, int32_t* path,
+                         int32_t* num_accepted, int64_t* next_tokens, int32_t* new_context_lens,
+                         uint32_t* err_word, void* stream);
+
+/*
+ * Keep the accepted tokens' keys and values: with base = context_lens[b] - n_b
+ * (context_lens as they were for the tree), the K and V rows of position
+ * base + path[b][d] move to position base + d, for every KV head and every d
+ * before the path's first -1.  Rows are read as they were before the call.
+ * Positions behind the kept ones are left as they are.  Bit-exact.  Paths
+ * ascend strictly and stay inside the tree; a path that does not sets
+ * PA_DEVERR_PATH, a bad block id PA_DEVERR_BLOCK_ID, malformed sizes
+ * PA_DEVERR_CONTEXT, and nothing of that sequence moves.  The blocks that the
+ * trees' tokens lie in belong to one sequence each (copy-on-write has run
+ * before the append).  Call it once per layer's pools with the same path.
+ *
+ *   path          int32 [N][max_nodes] (pa_tree_verify), max_nodes 1..64
+ * Uses shape->num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+ * max_blocks_per_seq, dtype (16-bit).  One launch.
+ */
+pa_status pa_keep_kv(const pa_shape* shape, int32_t max_nodes, const int32_t* path,
+                     const int32_t* q_start, const int32_t* block_tables, const int32_t* context_lens,
+                     void* k_pool, void* v_pool, uint32_t* err_word, void* stream);
+
+/*
  * 8-bit (FP8) KV cache.  Storing keys and values in 8 bits halves the cache
  * (ontq "AI Inference Serving at Scale", section 6; the vLLM deployment
  * script on thewebvale, section 5, names fp8_e5m2 as a cache dtype).
@@ -289,6 +371,48 @@ pa_status pa_decode_shared_prefix(const pa_shape* shape, const void* q, const vo
 pa_status pa_append_kv(const pa_shape* shape, int32_t num_tokens, const void* k_new,
                        const void* v_new, const int64_t* slot_mapping, void* k_pool,
                        void* v_pool, uint32_t* err_word, void* stream);
+
+/*
+ * Norms and rotary positions of new tokens' queries and keys, and pa_append_kv,
+ * in one pass.  For token t at position p = positions[t], each query and key
+ * head x (d values), in fp32 and rounded once:
+ *     y = x / sqrt(mean(x^2) + eps) * weight            (weight NULL: y = x)
+ *     (a, b) -> (a c - b s, b c + a s),  c = scale cos(p f_j), s = scale sin(p f_j)
+ * for the pairs j < rotary_dim / 2: (y_j, y_{j + rotary_dim / 2}), or
+ * (y_{2j}, y_{2j + 1}) when interleaved; values from rotary_dim on pass through.
+ * Angles are exact to 2^-32 of a turn at any int32 position.  Queries go to
+ * q_out, keys and (untouched) values to the pools at slot_mapping[t] as in
+ * pa_append_kv (a negative slot skips them; a slot past the pool sets
+ * PA_DEVERR_SLOT and skips them; the token's queries are written all the same).
+ *
+ *   q, k_new, v_new  [num_tokens] rows of [Hq][d], [Hkv][d], [Hkv][d], consecutive
+ *                    tokens q_stride, k_stride, v_stride elements apart (multiples
+ *                    of 8): the parts of one projection's output need no copy
+ *   positions        int32 [num_tokens], any sign
+ *   q_out            [num_tokens][Hq][d]; may be q itself when q is contiguous, must
+ *                    not overlap it otherwise
+ *   rope->inv_freq   fp32 [rotary_dim / 2] radians per position (device); long-context
+ *                    scalings are frequencies and a scale
+ *   rope->q_weight, k_weight  16-bit [d] (device) or NULL
+ *
+ * Supported: fp16 or bf16; d a multiple of 16 up to 256; rotary_dim a multiple
+ * of 16 up to d (0: no rotation).  One launch.
+ */
+typedef struct pa_rope {
+    const float* inv_freq;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float scale;                 /* multiplies cos and sin (1: plain rotation) */
+    float eps;
+    const void* q_weight;
+    const void* k_weight;
+} pa_rope;
+
+pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t num_tokens,
+                            const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, const int32_t* positions,
+                            const int64_t* slot_mapping, void* q_out, void* k_pool, void* v_pool,
+                            uint32_t* err_word, void* stream);
 
 /*
  * Copy-on-write block copies (ontq section 3, "Copy-on-Write Memory

@@ -21,7 +21,7 @@ STATUS_NAMES = {
 }
 PA_FP16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2 = 0, 1, 2, 3
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_SLOT, DEVERR_COPY_PAIR, DEVERR_TIMEOUT, DEVERR_GROUP = 1, 2, 4, 8, 16, 32
-DEVERR_Q_RANGE = 64
+DEVERR_Q_RANGE, DEVERR_PATH = 64, 128
 
 # Every symbol include/pa.h declares.
 EXPORTS = ("pa_decode_workspace_bytes", "pa_decode", "pa_append_kv", "pa_copy_blocks", "pa_read_error",
@@ -29,7 +29,8 @@ EXPORTS = ("pa_decode_workspace_bytes", "pa_decode", "pa_append_kv", "pa_copy_bl
            "pa_decode_shared_prefix", "pa_decode_fp8_workspace_bytes", "pa_decode_fp8", "pa_append_kv_fp8",
            "pa_copy_blocks_fp8", "pa_decode_multi_workspace_bytes", "pa_decode_multi",
            "pa_decode_int4_workspace_bytes", "pa_decode_int4", "pa_append_kv_int4", "pa_copy_blocks_int4",
-           "pa_set_decode_stall_ns")
+           "pa_set_decode_stall_ns", "pa_decode_tree_workspace_bytes", "pa_decode_tree", "pa_tree_verify",
+           "pa_keep_kv", "pa_rope_append_kv")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -43,6 +44,18 @@ class PaShape(ctypes.Structure):
         ("num_blocks", ctypes.c_int32),
         ("max_blocks_per_seq", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
+    ]
+
+
+class PaRope(ctypes.Structure):
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
     ]
 
 
@@ -118,6 +131,17 @@ def load() -> ctypes.CDLL:
         lib.pa_copy_blocks_int4.restype = I32
         lib.pa_set_decode_stall_ns.argtypes = [ctypes.c_uint64]
         lib.pa_set_decode_stall_ns.restype = I32
+        lib.pa_decode_tree_workspace_bytes.argtypes = [SP, I32]
+        lib.pa_decode_tree_workspace_bytes.restype = SZ
+        lib.pa_decode_tree.argtypes = [SP, I32, I32, P, P, P, P, P, P, P, F, P, P, SZ, P, P]
+        lib.pa_decode_tree.restype = I32
+        lib.pa_tree_verify.argtypes = [I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P]
+        lib.pa_tree_verify.restype = I32
+        lib.pa_keep_kv.argtypes = [SP, I32, P, P, P, P, P, P, P, P]
+        lib.pa_keep_kv.restype = I32
+        I64 = ctypes.c_int64
+        lib.pa_rope_append_kv.argtypes = [SP, ctypes.POINTER(PaRope), I32, P, I64, P, I64, P, I64, P, P, P, P, P, P, P]
+        lib.pa_rope_append_kv.restype = I32
         _lib = lib
         return lib
 

@@ -256,6 +256,28 @@ class BlockManager:
                 self._free.append(b)
         del self._len[seq]
 
+    def truncate(self, seq, length: int) -> None:
+        """Cut a sequence back to its first ``length`` tokens (drafted tokens
+        that were not accepted): whole blocks past them drop one reference and
+        go back to the free list at 0.  Queued copies into those blocks must
+        have been taken before."""
+        if seq not in self._blocks:
+            raise KeyError(f"unknown sequence {seq!r}")
+        length = int(length)
+        if not 0 <= length <= self._len[seq]:
+            raise ValueError(f"length must be between 0 and {self._len[seq]}")
+        blocks = self._blocks[seq]
+        keep = -(-length // self.block_size)
+        dropped = blocks[keep:]
+        if any(dst in dropped for _, dst in self._copies):
+            raise RuntimeError("take_copies() first: a queued copy writes a block to be dropped")
+        del blocks[keep:]
+        for b in dropped:
+            self._ref[b] -= 1
+            if self._ref[b] == 0:
+                self._free.append(b)
+        self._len[seq] = length
+
     def take_copies(self) -> np.ndarray:
         """Queued (src, dst) copy-on-write pairs as int32 [n, 2]; clears the queue."""
         c = np.asarray(self._copies, dtype=np.int32).reshape(-1, 2)

@@ -40,7 +40,7 @@
 
 namespace pa {
 
-template <int D_, int BS_, int NW_, bool BF16_>
+template <int D_, int BS_, int NW_, bool BF16_, bool TREE_ = false>
 struct MultiTraits {
     using Gm = Geom<D_, BS_>;
     static constexpr int D = D_;
@@ -48,6 +48,7 @@ struct MultiTraits {
     static constexpr int NW = NW_;                          // warps = 16-row tiles per CTA
     static constexpr int ROWS = 16 * NW;
     static constexpr bool BF16 = BF16_;
+    static constexpr bool TREE = TREE_;                     // drafted trees: visible keys by ancestor masks
     static constexpr int THREADS = 32 * NW;
     // about 8 warps per SM: 6 / 4 / 2 / 1 CTAs of 1 / 2 / 4 / 8 warps, sharing
     // ~190 KiB of stages
@@ -68,11 +69,39 @@ struct MultiTraits {
     static_assert(NW == 1 || NW == 2 || NW == 4 || NW == 8, "warps");
 };
 
+// The keys of a run starting at position t0 that a drafted node sees, as bits:
+// every key cached before the tree (off = base - t0 of them) and, from bit off
+// on, the nodes on its way (mask).
+__device__ __forceinline__ uint64_t tree_visible(uint64_t mask, int off) {
+    if (off >= 64) return ~0ull;
+    if (off >= 0) return (mask << off) | ((1ull << off) - 1);
+    return off > -64 ? mask >> -off : 0ull;
+}
+
+// The low n bits of a mask of at most 64 nodes.
+__device__ __forceinline__ uint64_t node_bits(uint64_t mask, int n) {
+    return n >= 64 ? mask : mask & ((1ull << n) - 1);
+}
+
+// Does a 32-bit word hold an infinite or NaN 16-bit value?
+template <bool BF16>
+__device__ __forceinline__ bool pair_not_finite(uint32_t w) {
+    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+    return (w & E) == E || ((w >> 16) & E) == E;
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool vec_not_finite(const uint4& v) {
+    return pair_not_finite<BF16>(v.x) || pair_not_finite<BF16>(v.y) || pair_not_finite<BF16>(v.z) ||
+           pair_not_finite<BF16>(v.w);
+}
+
 // consume_block for query rows with their own key limits: valid[r] keys of
 // this block are visible to the lane's row group r (rows g and g + 8 of the
 // warp's tile), vvalid slots of the block hold cached tokens (the rest of the
-// V rows are zeroed in registers).
-template <class Gm, bool BF16>
+// V rows are zeroed in registers).  TREE: valid[r] and vvalid are sets of the
+// block's keys, one bit each, instead of counts.
+template <class Gm, bool BF16, bool TREE = false>
 __device__ __forceinline__ void consume_block_rows(uint32_t kb, uint32_t vb, const int (&valid)[2], int vvalid,
                                                    const uint32_t (&qa)[Gm::KD][4], WarpAcc<Gm::D, 2>& acc,
                                                    float scale_log2, int lane) {
@@ -100,7 +129,8 @@ __device__ __forceinline__ void consume_block_rows(uint32_t kb, uint32_t vb, con
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int tok = nt * 8 + 2 * t4 + (e & 1);
-            const float v = tok < valid[e >> 1] ? sacc[nt][e] * scale_log2 : -INFINITY;
+            const bool seen = TREE ? ((uint32_t)valid[e >> 1] >> tok) & 1u : tok < valid[e >> 1];
+            const float v = seen ? sacc[nt][e] * scale_log2 : -INFINITY;
             sacc[nt][e] = v;
             mx[e >> 1] = fmaxf(mx[e >> 1], v);
         }
@@ -151,6 +181,10 @@ __device__ __forceinline__ void consume_block_rows(uint32_t kb, uint32_t vb, con
     // V^T operand registers: a0 / a1 hold the tokens 16 kt + 2 t4 + {0, 1},
     // a2 / a3 the tokens 16 kt + 8 + 2 t4 + {0, 1} (low half = the first)
     auto keep = [&](int tok) -> uint32_t {
+        if constexpr (TREE) {
+            const uint32_t two = (uint32_t)vvalid >> tok;
+            return (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+        }
         return (tok < vvalid ? 0x0000ffffu : 0u) | (tok + 1 < vvalid ? 0xffff0000u : 0u);
     };
 #pragma unroll
@@ -161,7 +195,7 @@ __device__ __forceinline__ void consume_block_rows(uint32_t kb, uint32_t vb, con
             const int row = kt * 16 + ((lane >> 4) << 3) + (lane & 7);
             const int chunk = 2 * mt + ((lane >> 3) & 1);
             ldsm_x4_t(vb + swz<Gm::BOX_BYTES>(row, chunk), a0, a1, a2, a3);
-            if (vvalid < Gm::BS) {
+            if (TREE ? (uint32_t)vvalid != (Gm::BS == 32 ? ~0u : (1u << (Gm::BS & 31)) - 1) : vvalid < Gm::BS) {
                 const uint32_t k0 = keep(16 * kt + 2 * t4), k1 = keep(16 * kt + 8 + 2 * t4);
                 a0 &= k0;
                 a1 &= k0;
@@ -182,6 +216,9 @@ struct MultiParams {
     int32_t max_q;                // the launch's largest chunk (q_len above it is an error)
     int32_t total_q;              // T: rows of q and out
     int32_t q_box;                // tokens per Q tile copy (tensor-core kernel: min(max_q, T))
+    // drafted trees (TREE kernels)
+    const uint64_t* tree_masks;   // [T] the nodes of its own tree that a node sees
+    int32_t tiles;                // 128-row tiles of a tree; d.Hkv counts (KV head, tile) pairs
 };
 
 template <class Tr>
@@ -358,6 +395,13 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             n_next = max(0, chunk_len(nx.s));
             load_q(qn, nx, n_next);
         }
+        // trees: the nodes that the lane's two rows see, and the first position of the tree
+        uint64_t see[2] = {0, 0};
+        const int base = ctx - n;
+        if constexpr (Tr::TREE) {
+            if (rw0 < n * G) see[0] = node_bits(__ldg(mp.tree_masks + qst[it.s] + rw0 / G), n);
+            if (rw1 < n * G) see[1] = node_bits(__ldg(mp.tree_masks + qst[it.s] + rw1 / G), n);
+        }
         // key limits of the lane's two rows (-1: no such row)
         const int lim0 = rw0 < n * G ? ctx - n + rw0 / G : -1;
         const int lim1 = rw1 < n * G ? ctx - n + rw1 / G : -1;
@@ -385,10 +429,38 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             }
             poisoned |= stage_poison[st];
             const int t0 = (it.b0 + b) * BS;
-            const int valid[2] = {min(BS, max(0, lim0 - t0 + 1)), min(BS, max(0, lim1 - t0 + 1))};
-            const int vvalid = min(BS, ctx - t0);
             const uint32_t kb = ring + st * Gm::STAGE_BYTES;
-            consume_block_rows<Gm, Tr::BF16>(kb, kb + Gm::CHUNK_BYTES, valid, vvalid, qa, acc, p.scale_log2, lane);
+            if constexpr (Tr::TREE) {
+                constexpr uint32_t FULL = BS == 32 ? ~0u : (1u << (BS & 31)) - 1;
+                const int held = min(BS, ctx - t0);              // cached tokens in the block
+                uint32_t vkeep = held >= 32 ? ~0u : (1u << held) - 1;
+                const int valid[2] = {lim0 < 0 ? 0 : (int)((uint32_t)tree_visible(see[0], base - t0) & FULL),
+                                      lim1 < 0 ? 0 : (int)((uint32_t)tree_visible(see[1], base - t0) & FULL)};
+                uint32_t spoilt = 0;
+                if (t0 + BS > base) {
+                    // Nodes whose V holds an infinity or NaN: a weight of 0 would still
+                    // spoil the rows that do not see them, so their V leaves the
+                    // product, and the rows that do see them become NaN.
+                    const uint8_t* vt = smem + st * Gm::STAGE_BYTES + Gm::CHUNK_BYTES;
+                    const int first = max(0, base - t0);
+                    for (int i = first * (D / 8) + lane; i < held * (D / 8); i += 32) {
+                        const int key = i / (D / 8);
+                        const uint4 v = *reinterpret_cast<const uint4*>(vt + swz<Gm::BOX_BYTES>(key, i % (D / 8)));
+                        if (vec_not_finite<Tr::BF16>(v)) spoilt |= 1u << key;
+                    }
+                    spoilt = __reduce_or_sync(0xffffffffu, spoilt);
+                    vkeep &= ~spoilt;
+                }
+                consume_block_rows<Gm, Tr::BF16, true>(kb, kb + Gm::CHUNK_BYTES, valid, (int)vkeep, qa, acc,
+                                                       p.scale_log2, lane);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (spoilt & (uint32_t)valid[r]) acc.l[r] = qnan;
+            } else {
+                const int valid[2] = {min(BS, max(0, lim0 - t0 + 1)), min(BS, max(0, lim1 - t0 + 1))};
+                const int vvalid = min(BS, ctx - t0);
+                consume_block_rows<Gm, Tr::BF16>(kb, kb + Gm::CHUNK_BYTES, valid, vvalid, qa, acc, p.scale_log2, lane);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
             if (warp == 0 && !idone) {
@@ -427,7 +499,7 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
                 if (rr < n * G) {
                     if (complete) {
                         uint16_t* orow = p.out + ((size_t)(qst[it.s] + rr / G) * p.Hq + (size_t)it.kvh * G + rr % G) * D;
-                        const float inv = 1.f / L;
+                        const float inv = Tr::TREE && L == 0.f ? 0.f : 1.f / L;   // a node that sees no key: zero
 #pragma unroll
                         for (int mt = 0; mt < Gm::KD; ++mt)
 #pragma unroll
@@ -483,12 +555,14 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 constexpr int MERGE_THREADS = 512;
 constexpr int MERGE_PIECES = 4;
 
-template <int D>
+// TREE: Hkv counts (KV head, tile) pairs of `tiles` tiles; a tile holds
+// rows_per_chunk rows.
+template <int D, bool TREE = false>
 __global__ void __launch_bounds__(MERGE_THREADS)
 pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_start,
                const int32_t* __restrict__ context_lens, const float* __restrict__ partials,
                uint16_t* __restrict__ out, int N, int Hkv, int G, int rows_per_chunk, int nchunks_hint,
-               int max_q, int total_q, int bf16) {
+               int max_q, int total_q, int bf16, int tiles) {
     griddep_wait();   // the attention grid is complete and its writes visible
     constexpr int PSTRIDE = D + 4;
     constexpr int LPR = D / 4;                    // lanes per row
@@ -516,18 +590,22 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
     const int s = a;
     const int nb = (int)(cum[s + 1] - cum[s]);
     if (nb == 0) return;
-    const int kvh = (int)((x - cum[s] * Hkv) / nb);
-    const long long P0 = cum[s] * Hkv + (long long)kvh * nb;
+    const int pair = (int)((x - cum[s] * Hkv) / nb);
+    const long long P0 = cum[s] * Hkv + (long long)pair * nb;
     if (P0 == x || sc.lo(c - 1) > P0) return;     // not cut here, or cut first by an earlier boundary
-    const int qa = q_start[s], qb = q_start[s + 1];
-    const int n = qb - qa;
+    const int q0 = q_start[s], qb = q_start[s + 1];
+    const int n_all = qb - q0;
     const int ctx = context_lens[s];
-    if (qa < 0 || qb > total_q || n < 0 || n > max_q || n > ctx) return;    // reported by the kernel
+    if (q0 < 0 || qb > total_q || n_all < 0 || n_all > max_q || n_all > ctx) return;    // reported by the kernel
+    const int kvh = TREE ? pair / tiles : pair;
+    const int heads = TREE ? Hkv / tiles : Hkv;
+    const int skip = TREE ? (pair % tiles) * (rows_per_chunk / G) : 0;     // the tile's first node
+    const int qa = q0 + skip, n = TREE ? min(rows_per_chunk / G, n_all - skip) : n_all;
     const long long cfirst = sc.of(P0), clast = sc.of(P0 + nb - 1);
     const size_t cstride = (size_t)2 * rows_per_chunk * PSTRIDE;
     const int np = (int)(clast - cfirst) + 1;
     const int d0 = sub * 4;
-    const int Hq = Hkv * G;
+    const int Hq = heads * G;
     for (int base = warp * RPW; base < n * G; base += nwarps * RPW) {
         const int rr = base + lane / LPR;
         const bool writer = rr < n * G;
@@ -582,7 +660,7 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
             }
         }
         if (!writer) continue;
-        const float inv = 1.f / L;
+        const float inv = TREE && L == 0.f ? 0.f : 1.f / L;
         const float xv[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
         uint32_t w[2];
 #pragma unroll
@@ -629,5 +707,8 @@ void multi_table_bf16_d128(MultiKernelInfo (&t)[2]);
 void multi_table_bf16_d64(MultiKernelInfo (&t)[2]);
 void multi_table_fp16_d128(MultiKernelInfo (&t)[2]);
 void multi_table_fp16_d64(MultiKernelInfo (&t)[2]);
+// Drafted trees: [d == 128][bs == 32], defined in tree_*.cu.
+void tree_table_bf16(MultiKernelInfo (&t)[2][2]);
+void tree_table_fp16(MultiKernelInfo (&t)[2][2]);
 
 }  // namespace pa

@@ -53,11 +53,12 @@
 
 namespace pa {
 
-template <int D_, int BS_, bool BF16_>
+template <int D_, int BS_, bool BF16_, bool TREE_ = false>
 struct TcTraits {
     static constexpr int D = D_;
     static constexpr int BS = BS_;
     static constexpr bool BF16 = BF16_;
+    static constexpr bool TREE = TREE_;                      // drafted trees: visible keys by ancestor masks
     static constexpr int ROWS = 128;                         // M of every MMA
     static constexpr int KEYS = 64;                          // keys per stage (N of the score MMA)
     static constexpr int SB = KEYS / BS;                     // blocks per stage
@@ -83,7 +84,8 @@ struct TcTraits {
     static constexpr int SMEM_BYTES = SMEM_CAP;              // all of it, 1024 of it alignment slack
     static constexpr int R_CAP = 12;
     static constexpr int REC_BYTES = 48;
-    static constexpr int NBAR_FIXED = 12;    // s_full[2] s_free[2] p_full[2] pv_done[2] q_full q_empty fin o_free
+    // s_full[2] s_free[2] p_full[2] pv_done[2] q_full q_empty fin o_free; trees: scanned[2]
+    static constexpr int NBAR_FIXED = TREE ? 14 : 12;
     // tagged cells per row: softmax references along a segment's stages [4],
     // and the partial row sums handed to a segment's last stage [4] (value, reference)
     static constexpr int XCH_BYTES = (4 + 2 * 4) * ROWS * 8;
@@ -115,11 +117,14 @@ struct TcTraits {
     static_assert(O_COL + D <= P_COL && P_COL + 128 <= TMEM_COLS, "tensor memory");
 };
 
-// One ring stage as the copy warp describes it to the consumers.
+// One ring stage as the copy warp describes it to the consumers.  Trees: n
+// counts the nodes of the segment's tile and q0 is the tile's first row; the
+// tree's own n follows from ctx and base.
 struct alignas(16) TcStage {
-    int s, kvh, t0, nkeys;       // sequence, KV head, first key, keys copied (blocks x B)
+    int base, kvh, t0, nkeys;    // first position of the chunk, KV head, first key, keys copied (blocks x B)
     int n, ctx, q0, flags;       // chunk length, context, first query row of the sequence
-    int poison, seg, pad1, pad2;  // bad block id seen; segment number within the CTA
+    int poison, seg;             // bad block id seen; segment number within the CTA
+    uint32_t spoilt[2];          // trees: stage keys (bits) whose V is not finite
 };
 static_assert(sizeof(TcStage) == 48, "stage record");
 
@@ -160,7 +165,8 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int G = p.Hq / p.Hkv;
+    const int HKV = Tr::TREE ? p.Hkv / mp.tiles : p.Hkv;      // KV heads of the pool
+    const int G = p.Hq / HKV;
     const uint32_t sbase = smem_u32(smem);
     const int qrows = Tr::q_rows(mp.q_box, G);
     const uint32_t q_half = (uint32_t)qrows * 128;            // between the Q tile's column halves
@@ -173,6 +179,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     auto empty = [&](int st) -> uint32_t { return bars + 8 * (R + st); };
     const uint32_t s_full = bars + 16 * R, s_free = s_full + 16, p_full = s_free + 16, pv_done = p_full + 16;
     const uint32_t q_full = pv_done + 16, q_empty = q_full + 8, fin = q_empty + 8, o_free = fin + 8;
+    const uint32_t scanned = o_free + 8;                      // trees only
     TcStage* recs = reinterpret_cast<TcStage*>(smem + Tr::REC_OFF);
     volatile unsigned long long* xch = reinterpret_cast<volatile unsigned long long*>(smem + Tr::XCH_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Tr::MISC_OFF);
@@ -194,6 +201,10 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         mbar_init(q_empty, 1);
         mbar_init(fin, 2);                      // the score thread and the PV thread
         mbar_init(o_free, SW / 2);              // a segment's output read: the four warps of its last stage
+        if constexpr (Tr::TREE) {               // a stream's four warps have looked at the tree's V rows
+            mbar_init(scanned, SW / 2);
+            mbar_init(scanned + 8, SW / 2);
+        }
         *abort_flag = 0;
         *n_stages = 0x7fffffff;
         fence_mbar_init();
@@ -261,10 +272,14 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             SegIter it = locate(p, tab, lo, lane);
             while (ok && it.gi < hi) {
                 const int len = seg_len(it, hi);
-                const int n = chunk_len(it.s);
+                const int n_all = chunk_len(it.s);
+                // a tree's nodes come in tiles of ROWS / G; p.Hkv counts (KV head, tile) pairs
+                const int kvh = Tr::TREE ? it.kvh / mp.tiles : it.kvh;
+                const int skip = Tr::TREE ? (it.kvh - kvh * mp.tiles) * (Tr::ROWS / G) : 0;
+                const int n = Tr::TREE ? min(Tr::ROWS / G, n_all - skip) : n_all;
                 if (n > 0) {
                     const int ctx = __ldg(p.context_lens + it.s);
-                    const int q0 = __ldg(qst + it.s);
+                    const int q0 = __ldg(qst + it.s) + skip;
                     const long long P0 = it.gi - it.b0;
                     const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
                     const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
@@ -275,7 +290,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             mbar_arrive_expect_tx(q_full, (uint32_t)(HALVES * 128 * G * mp.q_box));
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
-                                tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, it.kvh * G, q0, q_full);
+                                tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, kvh * G, q0, q_full);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -307,8 +322,9 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     }
                                 if (poison) set_err(p.err, PA_DEVERR_BLOCK_ID);
                                 TcStage& rc = recs[st];
-                                rc.s = it.s;
-                                rc.kvh = it.kvh;
+                                rc.base = ctx - n_all;
+                                rc.kvh = kvh;
+                                if constexpr (Tr::TREE) rc.spoilt[0] = rc.spoilt[1] = 0u;
                                 rc.t0 = (it.b0 + bb) * BS;
                                 rc.nkeys = nbs * BS;
                                 rc.n = n;
@@ -331,7 +347,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             const int ci = kl ? lane : lane - SB;
                             int cid = __shfl_sync(0xffffffffu, ids, (bb + (ci & (SB - 1))) & 31);
                             if ((unsigned)cid >= (unsigned)p.NB) cid = 0;   // flagged and poisoned above
-                            const int y = (cid * p.Hkv + it.kvh) * BS;
+                            const int y = (cid * HKV + kvh) * BS;
                             const uint32_t dst = ring + st * Tr::STAGE_BYTES + (kl ? 0 : Tr::KV_BYTES) + ci * Tr::BLK_BYTES;
                             if (ok && lane < 2 * SB && ci < nbs) {
                                 // each block is read once: L2 evict-first
@@ -522,6 +538,11 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         float m_mine = -INFINITY, l = 0.f;                      // reference of this stream's sum, the sum
         int pois = 0, lim = -1, cur_seg = -1, seg_kvh = 0, seg_q0 = 0;
         bool wact = false, ok = true;
+        // trees: the nodes this row sees (a row of no node looks at every key, so that
+        // it never takes its warp off the unmasked path; its results go nowhere)
+        uint64_t sees = 0;
+        bool alive = false;
+        uint32_t scan_ph = 0;
         while (true) {
             if (*abort_flag) break;
             if (!wait_all(full(st), ph)) {
@@ -540,6 +561,11 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 l = 0.f;
                 pois = 0;
                 lim = r < n * G ? ctx - n + r / G : -1;
+                if constexpr (Tr::TREE) {
+                    alive = r < n * G;
+                    lim = alive ? 0 : -1;
+                    sees = alive ? node_bits(__ldg(mp.tree_masks + seg_q0 + r / G), ctx - recs[st].base) : 0;
+                }
                 wact = __any_sync(0xffffffffu, lim >= 0);
             }
             pois |= recs[st].poison;
@@ -553,6 +579,44 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (!p_free) p_free = wait_all(pv_done + 8 * b, (uint32_t)(((j - 2) >> 1) & 1));
                 return p_free;
             };
+            uint64_t spoilt = 0;
+            if constexpr (Tr::TREE) {
+                // Nodes whose V holds an infinity or NaN: a weight of 0 would still spoil
+                // the rows that do not see them, so their V leaves the product, and the
+                // rows that do see them become NaN.  The stream's warps share the look
+                // (while the scores are computed) and meet at a barrier before acting.
+                const int from = max(0, recs[st].base - t0), held = min(nkeys, ctx - t0);
+                if (from < held) {
+                    uint8_t* vt = smem + ring_off + st * Tr::STAGE_BYTES + Tr::KV_BYTES;
+                    auto part_of = [&](int i) -> uint4* {
+                        const int key = i / (HALVES * 8), part = i % (HALVES * 8);
+                        return reinterpret_cast<uint4*>(vt + (key / BS) * Tr::BLK_BYTES + (part / 8) * Tr::HALF_STRIDE +
+                                                        (key % BS) * 128 + (part % 8) * 16);
+                    };
+                    uint64_t mine = 0;
+                    for (int i = from * HALVES * 8 + stid; i < held * HALVES * 8; i += 128)
+                        if (vec_not_finite<Tr::BF16>(*part_of(i))) mine |= 1ull << (i / (HALVES * 8));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t bits = __reduce_or_sync(0xffffffffu, (uint32_t)(mine >> (32 * h)));
+                        if (lane == 0 && bits) atomicOr(&recs[st].spoilt[h], bits);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(scanned + 8 * stream);
+                    if (!wait_all(scanned + 8 * stream, scan_ph)) {
+                        ok = false;
+                        break;
+                    }
+                    scan_ph ^= 1u;
+                    const volatile uint32_t* words = recs[st].spoilt;
+                    spoilt = (uint64_t)words[0] | ((uint64_t)words[1] << 32);
+                    if (spoilt) {                            // uniform over the stream
+                        for (int i = from * HALVES * 8 + stid; i < held * HALVES * 8; i += 128)
+                            if ((spoilt >> (i / (HALVES * 8))) & 1) *part_of(i) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
+                }
+            }
             if (!wait_all(s_full + 8 * b, (uint32_t)((j >> 1) & 1))) {
                 ok = false;
                 break;
@@ -574,9 +638,13 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free + 8 * b);
             if (wact) {
-                const int kv = min(nkeys, max(0, lim - t0 + 1));   // keys this row sees here
+                const int kv = Tr::TREE ? 0 : min(nkeys, max(0, lim - t0 + 1));   // keys this row sees here
+                // trees: the same as a set (t0 < ctx <= base + 64, so the offset is in range)
+                uint64_t set = ~0ull;
+                if constexpr (Tr::TREE)
+                    if (alive) set = tree_visible(sees, recs[st].base - t0) & (nkeys < KEYS ? (1ull << nkeys) - 1 : ~0ull);
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (__all_sync(0xffffffffu, kv >= KEYS)) {
+                if (__all_sync(0xffffffffu, Tr::TREE ? set == ~0ull : kv >= KEYS)) {
 #pragma unroll
                     for (int k = 0; k < KEYS; ++k) {
                         x[k] *= p.scale_log2;
@@ -585,7 +653,9 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 } else {
 #pragma unroll
                     for (int k = 0; k < KEYS; ++k) {
-                        x[k] = k < kv ? x[k] * p.scale_log2 : -INFINITY;
+                        const bool seen = Tr::TREE ? ((k < 32 ? (uint32_t)set : (uint32_t)(set >> 32)) >> (k & 31)) & 1u
+                                                   : k < kv;
+                        x[k] = seen ? x[k] * p.scale_log2 : -INFINITY;
                         m4[k & 3] = fmaxf(m4[k & 3], x[k]);
                     }
                 }
@@ -601,7 +671,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     m_mine = m_prev;
                 }
                 const float m_new = fmaxf(m_prev, mx);
-                const bool need = m_new > m_prev + Tr::TAU;
+                const bool need = m_new > m_prev + Tr::TAU && (!Tr::TREE || alive);
                 if (need) m_mine = m_new;
                 if (!(flags & TC_LAST)) xch_put(ref_cell + ((j + 1) & 3) * Tr::ROWS + r, m_mine, (uint32_t)(j + 1));
                 const float alpha = need ? ex2(m_prev - m_new) : 1.f;      // m_prev = -inf: 0
@@ -655,6 +725,8 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     tmem_st16(lane_addr + Tr::P_COL + 64 * b + 32 + 16 * c, lw);
                 }
                 l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                if constexpr (Tr::TREE)
+                    if (spoilt & set) l = qnan;
             }
             // V rows past the context or past the blocks copied are zero for the PV product
             const int vvalid = max(0, min(nkeys, ctx - t0));
@@ -701,7 +773,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const bool live = lim >= 0;
                     if (flags & TC_COMPLETE) {
                         uint16_t* orow = p.out + ((size_t)(seg_q0 + r / G) * p.Hq + (size_t)seg_kvh * G + r % G) * D;
-                        const float inv = 1.f / L;
+                        const float inv = Tr::TREE && L == 0.f ? 0.f : 1.f / L;   // a node that sees no key: zero
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t u[32];
@@ -792,5 +864,8 @@ void multi_tc_table_bf16_d128(MultiKernelInfo (&t)[2]);
 void multi_tc_table_bf16_d64(MultiKernelInfo (&t)[2]);
 void multi_tc_table_fp16_d128(MultiKernelInfo (&t)[2]);
 void multi_tc_table_fp16_d64(MultiKernelInfo (&t)[2]);
+// Drafted trees: [d == 128][bs == 32], defined in tree_*.cu.
+void tree_tc_table_bf16(MultiKernelInfo (&t)[2][2]);
+void tree_tc_table_fp16(MultiKernelInfo (&t)[2][2]);
 
 }  // namespace pa

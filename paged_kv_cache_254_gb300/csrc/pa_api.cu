@@ -15,6 +15,8 @@
 #include "multi_kernel.cuh"
 #include "multi_tc_kernel.cuh"
 #include "prefix_kernel.cuh"
+#include "rope_ops.cuh"
+#include "tree_ops.cuh"
 
 namespace {
 
@@ -398,6 +400,37 @@ const MultiKernelInfo* pick_multi_tc(const pa_shape* s) {
 // partial states per tile row per CTA.
 size_t multi_region_bytes(const pa_shape* s, int ctas, int rows) {
     return counters_bytes(s) + cum_bytes(s) + (size_t)ctas * 2 * rows * (s->head_dim + 4) * sizeof(float);
+}
+
+// ---------------------------------------------------------------- drafted trees
+// A tree launch: up to 16 query rows per (sequence, KV head) pair on the
+// mma.sync kernel, more on the tcgen05 kernel in tiles of 128 rows (the
+// measurements at kTcMinRows; a tree's masks change neither side).
+struct TreePlan {
+    const MultiKernelInfo* k;
+    int tiles;                   // row tiles per tree
+    int nodes_per_tile;
+};
+
+pa_status plan_tree(const pa_shape* s, int max_nodes, TreePlan* out) {
+    const DecodeKernelInfo* k16 = nullptr;
+    const pa_status st = pick_decode(s, &k16);            // the same shape rules as decode
+    if (st != PA_OK) return st;
+    if (max_nodes < 1 || max_nodes > 64) return PA_ERR_INVALID_ARG;
+    static const auto tab = [] {
+        struct T { MultiKernelInfo mma[2][2][2], tc[2][2][2]; } x;   // [bf16][d == 128][bs == 32]
+        tree_table_fp16(x.mma[0]);
+        tree_table_bf16(x.mma[1]);
+        tree_tc_table_fp16(x.tc[0]);
+        tree_tc_table_bf16(x.tc[1]);
+        return x;
+    }();
+    const int g = s->num_q_heads / s->num_kv_heads, rows = max_nodes * g;
+    const int t = s->dtype == PA_BF16, d = s->head_dim == 128, b = s->block_size == 32;
+    out->k = rows >= kTcMinRows ? &tab.tc[t][d][b] : &tab.mma[t][d][b];
+    out->tiles = (rows + out->k->rows - 1) / out->k->rows;
+    out->nodes_per_tile = out->k->rows / g;
+    return (long long)s->num_kv_heads * out->tiles < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 // Workspace of prefix-aware decode (offsets in off[]): [0] prefix counters,
@@ -871,14 +904,232 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
         const cudaError_t e =
             shape->head_dim == 128
                 ? cudaLaunchKernelEx(&cfg, pa_multi_merge<128>, d.cum, q_start, context_lens, parts, d.out, d.N,
-                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf)
+                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf, 1)
                 : cudaLaunchKernelEx(&cfg, pa_multi_merge<64>, d.cum, q_start, context_lens, parts, d.out, d.N, d.Hkv,
-                                     g, k->rows, ctas, max_q_len, total_q, bf);
+                                     g, k->rows, ctas, max_q_len, total_q, bf, 1);
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+
+size_t pa_decode_tree_workspace_bytes(const pa_shape* shape, int32_t max_nodes) {
+    TreePlan plan;
+    if (plan_tree(shape, max_nodes, &plan) != PA_OK) return 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int ctas = plan.k->max_ctas(dev);
+    return ctas > 0 ? multi_region_bytes(shape, ctas, plan.k->rows) : 0;
+}
+
+pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total_q, const void* q,
+                         const int32_t* q_start, const uint64_t* tree_masks, const void* k_pool,
+                         const void* v_pool, const int32_t* block_tables, const int32_t* context_lens,
+                         float scale, void* out, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                         void* stream) {
+    TreePlan plan;
+    const pa_status st = plan_tree(shape, max_nodes, &plan);
+    if (st != PA_OK) return st;
+    if (total_q < 0) return PA_ERR_INVALID_ARG;
+    if (!q_start || !k_pool || !v_pool || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    if (total_q > 0 && (!q || !out || !tree_masks)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_start, 4) || !aligned(tree_masks, 8))
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    // with no query rows at all the mma.sync kernel only checks the trees' sizes
+    if (total_q == 0 && plan_tree(shape, 1, &plan) != PA_OK) return PA_ERR_UNSUPPORTED;
+    const bool tc = plan.k->rows > 16 && total_q > 0;
+    const int ctas = plan.k->max_ctas(dev);
+    if (ctas <= 0) return PA_ERR_CUDA;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < multi_region_bytes(shape, ctas, plan.k->rows))
+        return PA_ERR_WORKSPACE;
+    CUtensorMap mk, mv, mq;
+    if (!(tc ? pool_map_groups(&mk, k_pool, shape) : pool_map_chunk(&mk, k_pool, shape)) ||
+        !pool_map_chunk(&mv, v_pool, shape))
+        return PA_ERR_CUDA;
+    const int q_box = std::min({(int)max_nodes, plan.nodes_per_tile, (int)total_q});
+    if (tc && !q_map(&mq, q, shape, total_q, q_box)) return PA_ERR_CUDA;
+
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    MultiLaunch L{};
+    L.tmap_q = tc ? &mq : nullptr;
+    L.tmap_k = &mk;
+    L.tmap_v = &mv;
+    DecodeParams& d = L.p.d;
+    d.q = static_cast<const uint16_t*>(q);
+    d.block_tables = block_tables;
+    d.context_lens = context_lens;
+    d.out = static_cast<uint16_t*>(out);
+    d.err = err_word;
+    d.chunk_ctr = reinterpret_cast<int32_t*>(base);
+    d.cum = reinterpret_cast<const long long*>(base + counters_bytes(shape));
+    d.partials = reinterpret_cast<float*>(base + counters_bytes(shape) + cum_bytes(shape));
+    d.N = shape->num_seqs;
+    d.Hq = shape->num_q_heads;
+    d.Hkv = shape->num_kv_heads * plan.tiles;
+    d.NB = shape->num_blocks;
+    d.MB = shape->max_blocks_per_seq;
+    d.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
+    d.timeout_ns = kTimeoutNs;
+    d.v_scale = 1.0f;
+    L.p.q_start = q_start;
+    L.p.max_q = max_nodes;
+    L.p.total_q = total_q;
+    L.p.q_box = q_box;
+    L.p.tree_masks = tree_masks;
+    L.p.tiles = plan.tiles;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.grid = ctas;
+    pa_decode_prepass<<<1, 1024, 0, L.stream>>>(context_lens, nullptr, shape->num_seqs,
+                                                shape->max_blocks_per_seq, shape->block_size, d.chunk_ctr, 1,
+                                                const_cast<long long*>(d.cum));
+    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    if (plan.k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
+    if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
+        const int g = shape->num_q_heads / shape->num_kv_heads;
+        cudaLaunchAttribute attr[1];
+        const cudaLaunchConfig_t cfg = pdl_config(ctas - 1, MERGE_THREADS, 0, L.stream, attr);
+        const float* parts = d.partials;
+        const auto merge = shape->head_dim == 128 ? pa_multi_merge<128, true> : pa_multi_merge<64, true>;
+        if (cudaLaunchKernelEx(&cfg, merge, d.cum, q_start, context_lens, parts, d.out, d.N, d.Hkv, g, plan.k->rows,
+                               ctas, (int)max_nodes, (int)total_q, (int)(shape->dtype == PA_BF16), plan.tiles) !=
+            cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_tree_verify(int32_t num_seqs, int32_t max_nodes, int32_t total_q, const int32_t* q_start,
+                         const uint64_t* tree_masks, const int64_t* draft_tokens, const int64_t* target_tokens,
+                         const int32_t* context_lens, int32_t* path, int32_t* num_accepted, int64_t* next_tokens,
+                         int32_t* new_context_lens, uint32_t* err_word, void* stream) {
+    if (num_seqs < 0 || max_nodes < 1 || max_nodes > 64 || total_q < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!q_start || !context_lens || !path || !num_accepted || !next_tokens || !new_context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (total_q > 0 && (!tree_masks || !draft_tokens || !target_tokens)) return PA_ERR_INVALID_ARG;
+    if (!aligned(tree_masks, 8) || !aligned(draft_tokens, 8) || !aligned(target_tokens, 8) ||
+        !aligned(next_tokens, 8) || !aligned(q_start, 4) || !aligned(context_lens, 4) || !aligned(path, 4) ||
+        !aligned(num_accepted, 4) || !aligned(new_context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    VerifyArgs a{};
+    a.q_start = q_start;
+    a.masks = tree_masks;
+    a.draft = draft_tokens;
+    a.target = target_tokens;
+    a.context_lens = context_lens;
+    a.path = path;
+    a.accepted = num_accepted;
+    a.next = next_tokens;
+    a.new_lens = new_context_lens;
+    a.err = err_word;
+    a.N = num_seqs;
+    a.P = max_nodes;
+    a.total_q = total_q;
+    return tree_verify_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_keep_kv(const pa_shape* shape, int32_t max_nodes, const int32_t* path, const int32_t* q_start,
+                     const int32_t* block_tables, const int32_t* context_lens, void* k_pool, void* v_pool,
+                     uint32_t* err_word, void* stream) {
+    const pa_status st = check_common(shape);
+    if (st != PA_OK) return st;
+    if (elem_bytes(shape->dtype) != 2 || shape->num_seqs < 0 || shape->max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (max_nodes < 1 || max_nodes > 64) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;
+    if (!path || !q_start || !block_tables || !context_lens || !k_pool || !v_pool) return PA_ERR_INVALID_ARG;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(path, 4) || !aligned(q_start, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if ((long long)shape->max_blocks_per_seq * shape->block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    KeepArgs a{};
+    a.path = path;
+    a.q_start = q_start;
+    a.context_lens = context_lens;
+    a.block_tables = block_tables;
+    a.k_pool = static_cast<uint4*>(k_pool);
+    a.v_pool = static_cast<uint4*>(v_pool);
+    a.err = err_word;
+    a.N = shape->num_seqs;
+    a.P = max_nodes;
+    a.Hkv = shape->num_kv_heads;
+    a.BS = shape->block_size;
+    a.NB = shape->num_blocks;
+    a.MB = shape->max_blocks_per_seq;
+    a.vec_per_row = shape->head_dim * 2 / 16;
+    if ((long long)a.Hkv * a.vec_per_row * 2 > 0x7fffffffll - 256 ||
+        (2ll * a.Hkv * a.vec_per_row + 255) / 256 * a.N > 0x7fffffffll)
+        return PA_ERR_UNSUPPORTED;
+    return keep_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t num_tokens, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                            int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, void* q_out,
+                            void* k_pool, void* v_pool, uint32_t* err_word, void* stream) {
+    const pa_status st = check_common(shape);
+    if (st != PA_OK) return st;
+    if (!rope || elem_bytes(shape->dtype) != 2 || num_tokens < 0 || shape->num_q_heads <= 0)
+        return PA_ERR_INVALID_ARG;
+    const int D = shape->head_dim;
+    if (D % 16 != 0 || D > 256) return PA_ERR_UNSUPPORTED;
+    if (rope->rotary_dim < 0 || rope->rotary_dim > D) return PA_ERR_INVALID_ARG;
+    if (rope->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (!std::isfinite(rope->scale) || !(rope->eps >= 0.f) || !std::isfinite(rope->eps)) return PA_ERR_INVALID_ARG;
+    if ((long long)shape->num_q_heads + 2ll * shape->num_kv_heads > (1ll << 30)) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    if (!q || !k_new || !v_new || !positions || !slot_mapping || !q_out || !k_pool || !v_pool ||
+        (rope->rotary_dim > 0 && !rope->inv_freq))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q_out, 16) ||
+        !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
+        !aligned(rope->inv_freq, 4) || !aligned(rope->q_weight, 16) || !aligned(rope->k_weight, 16))
+        return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)shape->num_q_heads * D, kv_row = (int64_t)shape->num_kv_heads * D;
+    if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return PA_ERR_INVALID_ARG;
+    // q_out may be q itself (a row is read before it is written), not a shifted part of it
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(q_out);
+    const uintptr_t q1 = q0 + 2 * (uintptr_t)((num_tokens - 1) * q_stride + q_row),
+                    o1 = o0 + 2 * (uintptr_t)(num_tokens * q_row);
+    if (q0 < o1 && o0 < q1 && !(q0 == o0 && q_stride == q_row)) return PA_ERR_INVALID_ARG;
+    const int sms = current_sms();
+    if (sms <= 0) return PA_ERR_CUDA;
+    RopeArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k_new);
+    a.v = static_cast<const uint16_t*>(v_new);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.inv_freq = rope->inv_freq;
+    a.q_weight = static_cast<const uint16_t*>(rope->q_weight);
+    a.k_weight = static_cast<const uint16_t*>(rope->k_weight);
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_pool = static_cast<uint16_t*>(k_pool);
+    a.v_pool = static_cast<uint16_t*>(v_pool);
+    a.err = err_word;
+    a.num_slots = (long long)shape->num_blocks * shape->block_size;
+    a.T = num_tokens;
+    a.Hq = shape->num_q_heads;
+    a.Hkv = shape->num_kv_heads;
+    a.D = D;
+    a.BS = shape->block_size;
+    a.rot = rope->rotary_dim;
+    a.interleaved = rope->interleaved != 0;
+    a.scale = rope->scale;
+    a.eps = rope->eps;
+    return rope_append_launch(a, shape->dtype == PA_BF16, static_cast<cudaStream_t>(stream), sms) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
 
 size_t pa_decode_int4_workspace_bytes(const pa_shape* shape) {
     const DecodeKernelInfo* k16 = nullptr;

@@ -1,0 +1,13 @@
+// Instantiations of the tree attention kernels: fp16.
+#include "multi_kernel.cuh"
+
+namespace pa {
+
+void tree_table_fp16(MultiKernelInfo (&t)[2][2]) {
+    t[0][0] = multi_info<MultiTraits<64, 16, 1, false, true>>();
+    t[0][1] = multi_info<MultiTraits<64, 32, 1, false, true>>();
+    t[1][0] = multi_info<MultiTraits<128, 16, 1, false, true>>();
+    t[1][1] = multi_info<MultiTraits<128, 32, 1, false, true>>();
+}
+
+}  // namespace pa

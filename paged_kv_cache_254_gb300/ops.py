@@ -8,6 +8,7 @@ calls the matching ``pa_*`` function of libpa.so on the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -257,6 +258,267 @@ def pa_decode_multi(q, k_pool, v_pool, block_tables, context_lens, q_start, scal
                                  ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
                                  _stream(q.device, stream))
     _lib.check(st, "pa_decode_multi")
+    return out
+
+
+# --------------------------------------------------------------------------- drafted trees, rotary positions
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _call(fn, device, *args):
+    """Call a library function with ``device`` current."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on_stream(fn):
+    """Give ``fn`` a ``stream`` argument: the call runs with that stream
+    current, so what it allocates belongs to the stream, and its arguments'
+    memory is not reused before the stream has passed the call."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            result = fn(*args, **kwargs)
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return result
+    return call
+
+
+def _check_err(err):
+    if err is not None:
+        _need_cuda("err", err, torch.int32)
+
+
+_tree_bytes = {}
+
+
+def _tree_workspace_bytes(device, shape, max_nodes) -> int:
+    # the size depends on the shape and the device's SM count alone
+    key = (device.index, max_nodes, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim,
+           shape.block_size, shape.dtype)
+    need = _tree_bytes.get(key)
+    if need is None:
+        need = int(_call(_lib.load().pa_decode_tree_workspace_bytes, device, shape, max_nodes))
+        if need:
+            _tree_bytes[key] = need
+    return need
+
+
+@_on_stream
+def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_masks, scale, max_nodes=None,
+                   out=None, workspace=None, err=None):
+    """Attention of drafted trees over the cache (see include/pa.h): q
+    [T, Hq, d] holds each sequence's nodes at rows q_start[b] .. q_start[b + 1]
+    - 1 (q_start: int32 [N + 1]); bit j of tree_masks [T] (int64, see
+    ``tree_masks()``) lets a row see node j of its own tree, next to every key
+    cached before the tree.  max_nodes (1..64) defaults to the largest tree
+    (read from q_start on the host)."""
+    _need_cuda("q", q)
+    _need_cuda("k_pool", k_pool, q.dtype)
+    _need_cuda("v_pool", v_pool, q.dtype)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    _need_cuda("q_start", q_start, torch.int32)
+    _need_cuda("tree_masks", tree_masks, torch.int64)
+    if q.dtype not in _DTYPES:
+        raise TypeError("q must be float16 or bfloat16")
+    if q.dim() != 3 or k_pool.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q [T, Hq, d], k_pool and v_pool [NB, Hkv, B, d], block_tables [N, MB]")
+    T, Hq, d = q.shape
+    N = block_tables.shape[0]
+    if q_start.shape != (N + 1,) or context_lens.shape != (N,) or tree_masks.shape != (T,):
+        raise ValueError("q_start must have N + 1 entries, context_lens N and tree_masks T")
+    if k_pool.shape != v_pool.shape or k_pool.shape[3] != d:
+        raise ValueError("shape mismatch between q and the pools")
+    if max_nodes is None:
+        qs = q_start.cpu()
+        max_nodes = max(1, int((qs[1:] - qs[:-1]).max().item())) if N > 0 else 1
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need_cuda("out", out, q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    _check_err(err)
+    dev = q.device
+    _same_device(dev, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables, context_lens=context_lens,
+                 q_start=q_start, tree_masks=tree_masks, out=out, workspace=workspace, err=err)
+    shape = _pool_shape(k_pool, N, Hq, block_tables.shape[1])
+    if workspace is None:
+        # 0 bytes: an invalid shape or tree size, which the call reports
+        need = _tree_workspace_bytes(dev, shape, max_nodes)
+        if need and not torch.cuda.is_current_stream_capturing():
+            workspace = _shared_workspace(dev, need)
+        else:
+            # a captured call keeps a workspace of its graph's own: the shared one may be
+            # replaced by a larger one, and another graph may run beside this one
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda("workspace", workspace)
+    st = _call(_lib.load().pa_decode_tree, dev, shape, max_nodes, T, q.data_ptr(), q_start.data_ptr(),
+               tree_masks.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+               context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), _addr(err), _raw_stream(dev))
+    _lib.check(st, "pa_decode_tree")
+    return out
+
+
+@_on_stream
+def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_lens, max_nodes=None, path=None,
+                   err=None):
+    """The drafted path that the target model's tokens agree with (see
+    include/pa.h).  Returns (path int32 [N, max_nodes], num_accepted int32 [N],
+    next_tokens int64 [N], new_context_lens int32 [N])."""
+    _need_cuda("tree_masks", tree_masks, torch.int64)
+    _need_cuda("draft_tokens", draft_tokens, torch.int64)
+    _need_cuda("target_tokens", target_tokens, torch.int64)
+    _need_cuda("q_start", q_start, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    if tree_masks.dim() != 1 or context_lens.dim() != 1:
+        raise ValueError("tree_masks [T], context_lens [N]")
+    T, N = tree_masks.shape[0], context_lens.shape[0]
+    if draft_tokens.shape != (T,) or target_tokens.shape != (T,) or q_start.shape != (N + 1,):
+        raise ValueError("draft_tokens and target_tokens must have tree_masks' shape, q_start N + 1 entries")
+    if max_nodes is None:
+        qs = q_start.cpu()
+        max_nodes = max(1, int((qs[1:] - qs[:-1]).max().item())) if N > 0 else 1
+    dev = tree_masks.device
+    if path is None:
+        path = torch.empty((N, max(0, max_nodes)), dtype=torch.int32, device=dev)
+    else:
+        _need_cuda("path", path, torch.int32)
+        if path.shape != (N, max_nodes):
+            raise ValueError("path must be [N, max_nodes]")
+    _check_err(err)
+    _same_device(dev, draft_tokens=draft_tokens, target_tokens=target_tokens, q_start=q_start,
+                 context_lens=context_lens, path=path, err=err)
+    counts = torch.empty((2, N), dtype=torch.int32, device=dev)
+    accepted, lens = counts[0], counts[1]
+    following = torch.empty(N, dtype=torch.int64, device=dev)
+    st = _call(_lib.load().pa_tree_verify, dev, N, max_nodes, T, q_start.data_ptr(), tree_masks.data_ptr(),
+               draft_tokens.data_ptr(), target_tokens.data_ptr(), context_lens.data_ptr(), path.data_ptr(),
+               accepted.data_ptr(), following.data_ptr(), lens.data_ptr(), _addr(err), _raw_stream(dev))
+    _lib.check(st, "pa_tree_verify")
+    return path, accepted, following, lens
+
+
+@_on_stream
+def pa_keep_kv(path, q_start, context_lens, block_tables, k_pool, v_pool, err=None):
+    """Move the accepted tokens' K and V rows to consecutive positions behind
+    each sequence's context (see include/pa.h); path int32 [N, max_nodes] and
+    the context lengths are those of the tree."""
+    _need_cuda("k_pool", k_pool)
+    _need_cuda("v_pool", v_pool, k_pool.dtype)
+    _need_cuda("path", path, torch.int32)
+    _need_cuda("q_start", q_start, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    if k_pool.dtype not in _DTYPES:
+        raise TypeError("the pools must be float16 or bfloat16")
+    if path.dim() != 2 or block_tables.dim() != 2 or k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("path [N, max_nodes], block_tables [N, MB], k_pool and v_pool [NB, Hkv, B, d]")
+    N, P = path.shape
+    if q_start.shape != (N + 1,) or context_lens.shape != (N,) or block_tables.shape[0] != N:
+        raise ValueError("q_start must have N + 1 entries, context_lens and block_tables N")
+    _check_err(err)
+    dev = k_pool.device
+    _same_device(dev, v_pool=v_pool, path=path, q_start=q_start, context_lens=context_lens,
+                 block_tables=block_tables, err=err)
+    shape = _pool_shape(k_pool, N, 1, block_tables.shape[1])
+    st = _call(_lib.load().pa_keep_kv, dev, shape, P, path.data_ptr(), q_start.data_ptr(), block_tables.data_ptr(),
+               context_lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _addr(err), _raw_stream(dev))
+    _lib.check(st, "pa_keep_kv")
+
+
+def _token_rows(name, t, dtype):
+    """[T, H, d] with contiguous heads, tokens any (16-byte) stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, d]")
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if T <= 1:
+        st = H * d if st < H * d or st % 8 else st      # a single token: its stride is never used
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if T > 1 and st < H * d:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return st
+
+
+@_on_stream
+def pa_rope_append_kv(q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, inv_freq, interleaved=False,
+                      rope_scale=1.0, q_weight=None, k_weight=None, eps=1e-6, out=None, err=None):
+    """Norm (with q_weight / k_weight) and rotate queries and keys, write keys
+    and values into the pools at slot_mapping, and return the queries
+    [T, Hq, d] (see include/pa.h).  q, k_new, v_new [T, heads, d] may be views
+    of one projection's output; inv_freq [rotary_dim / 2] fp32 as from
+    ``rope_inv_freq()``, or None for no rotation; out may be q."""
+    _need_cuda("k_pool", k_pool)
+    dt = k_pool.dtype
+    if dt not in _DTYPES:
+        raise TypeError("the pools must be float16 or bfloat16")
+    _need_cuda("v_pool", v_pool, dt)
+    qs, ks, vs = _token_rows("q", q, dt), _token_rows("k_new", k_new, dt), _token_rows("v_new", v_new, dt)
+    _need_cuda("positions", positions, torch.int32)
+    _need_cuda("slot_mapping", slot_mapping, torch.int64)
+    T, Hq, d = q.shape
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.shape[3] != d:
+        raise ValueError("k_pool and v_pool must be [NB, Hkv, B, d] with q's d")
+    if k_new.shape != (T, k_pool.shape[1], d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new, v_new must be [T, Hkv, d]")
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("positions and slot_mapping must be [T]")
+    rotary = 0
+    if inv_freq is not None:
+        _need_cuda("inv_freq", inv_freq, torch.float32)
+        if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
+            raise ValueError("inv_freq must be [rotary_dim / 2] with rotary_dim <= d")
+        rotary = 2 * inv_freq.shape[0]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need_cuda(name, w, dt)
+            if w.shape != (d,):
+                raise ValueError(f"{name} must be [d]")
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+    else:
+        _need_cuda("out", out, dt)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    _check_err(err)
+    dev = k_pool.device
+    _same_device(dev, q=q, k_new=k_new, v_new=v_new, v_pool=v_pool, positions=positions, slot_mapping=slot_mapping,
+                 inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, out=out, err=err)
+    shape = _pool_shape(k_pool, 0, Hq)
+    rope = _lib.PaRope(_addr(inv_freq) if rotary else None, rotary, int(bool(interleaved)), rope_scale, eps,
+                       _addr(q_weight), _addr(k_weight))
+    st = _call(_lib.load().pa_rope_append_kv, dev, shape, rope, T, q.data_ptr(), qs, k_new.data_ptr(), ks,
+               v_new.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), out.data_ptr(),
+               k_pool.data_ptr(), v_pool.data_ptr(), _addr(err), _raw_stream(dev))
+    _lib.check(st, "pa_rope_append_kv")
     return out
 
 
