@@ -289,9 +289,12 @@ bool q_map(CUtensorMap* m, const void* q, const pa_shape* s, int total_q, int q_
 }
 
 int current_sms() {
+    static std::atomic<int> cached[64];                  // SM counts do not change
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    if (dev < 64 && (sms = cached[dev].load(std::memory_order_relaxed)) > 0) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    if (dev < 64) cached[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
@@ -1081,7 +1084,7 @@ pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t 
     if (rope->rotary_dim < 0 || rope->rotary_dim > D) return PA_ERR_INVALID_ARG;
     if (rope->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
     if (!std::isfinite(rope->scale) || !(rope->eps >= 0.f) || !std::isfinite(rope->eps)) return PA_ERR_INVALID_ARG;
-    if ((long long)shape->num_q_heads + 2ll * shape->num_kv_heads > (1ll << 30)) return PA_ERR_UNSUPPORTED;
+    if (((long long)shape->num_q_heads + 2ll * shape->num_kv_heads) * D >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if (!q || !k_new || !v_new || !positions || !slot_mapping || !q_out || !k_pool || !v_pool ||
         (rope->rotary_dim > 0 && !rope->inv_freq))

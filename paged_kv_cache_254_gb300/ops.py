@@ -262,15 +262,32 @@ def pa_decode_multi(q, k_pool, v_pool, block_tables, context_lens, q_start, scal
 
 
 # --------------------------------------------------------------------------- drafted trees, rotary positions
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+# These calls run beside kernels of a few microseconds, so their host side is
+# kept short: one check per argument, the raw stream handle, no context manager
+# unless another device is current.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _arg(name, t, dtype, device):
+    """``t`` is a contiguous tensor of ``dtype`` on CUDA device ``device``."""
+    if isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.is_contiguous():
+        return
+    _need_cuda(name, t, dtype)
+    raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+
+
+def _index(name, t) -> int:
+    """The CUDA device of the argument that the others have to share."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.get_device()
 
 
 def _call(fn, device, *args):
-    """Call a library function with ``device`` current."""
-    if torch.cuda.current_device() == device.index:
+    """Call a library function with CUDA device ``device`` current."""
+    if torch.cuda.current_device() == device:
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -278,10 +295,6 @@ def _call(fn, device, *args):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on_stream(fn):
@@ -301,24 +314,27 @@ def _on_stream(fn):
     return call
 
 
-def _check_err(err):
-    if err is not None:
-        _need_cuda("err", err, torch.int32)
+def _largest_chunk(q_start, n):
+    qs = q_start.cpu()
+    return max(1, int((qs[1:] - qs[:-1]).max().item())) if n > 0 else 1
 
 
 _tree_bytes = {}
 
 
-def _tree_workspace_bytes(device, shape, max_nodes) -> int:
-    # the size depends on the shape and the device's SM count alone
-    key = (device.index, max_nodes, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim,
-           shape.block_size, shape.dtype)
+def _tree_workspace(dev, shape, max_nodes):
+    # the size depends on these and the device's SM count alone
+    key = (dev, max_nodes, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim, shape.block_size,
+           shape.dtype)
     need = _tree_bytes.get(key)
     if need is None:
-        need = int(_call(_lib.load().pa_decode_tree_workspace_bytes, device, shape, max_nodes))
-        if need:
-            _tree_bytes[key] = need
-    return need
+        need = int(_call(_lib.load().pa_decode_tree_workspace_bytes, dev, shape, max_nodes))
+        _tree_bytes[key] = need          # 0: an invalid shape or tree size, which the call reports
+    if need == 0 or torch.cuda.is_current_stream_capturing():
+        # a captured call keeps a workspace of its graph's own: the shared one may be
+        # replaced by a larger one, and another graph may run beside this one
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+    return _kept_workspace(dev, _raw_stream(dev), need)
 
 
 @_on_stream
@@ -330,53 +346,47 @@ def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_
     ``tree_masks()``) lets a row see node j of its own tree, next to every key
     cached before the tree.  max_nodes (1..64) defaults to the largest tree
     (read from q_start on the host)."""
-    _need_cuda("q", q)
-    _need_cuda("k_pool", k_pool, q.dtype)
-    _need_cuda("v_pool", v_pool, q.dtype)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
-    _need_cuda("q_start", q_start, torch.int32)
-    _need_cuda("tree_masks", tree_masks, torch.int64)
-    if q.dtype not in _DTYPES:
+    dev = _index("q", q)
+    dt = q.dtype
+    if dt not in _DTYPES:
         raise TypeError("q must be float16 or bfloat16")
+    _arg("q", q, dt, dev)
+    _arg("k_pool", k_pool, dt, dev)
+    _arg("v_pool", v_pool, dt, dev)
+    _arg("block_tables", block_tables, torch.int32, dev)
+    _arg("context_lens", context_lens, torch.int32, dev)
+    _arg("q_start", q_start, torch.int32, dev)
+    _arg("tree_masks", tree_masks, torch.int64, dev)
     if q.dim() != 3 or k_pool.dim() != 4 or block_tables.dim() != 2:
         raise ValueError("q [T, Hq, d], k_pool and v_pool [NB, Hkv, B, d], block_tables [N, MB]")
     T, Hq, d = q.shape
-    N = block_tables.shape[0]
+    N, MB = block_tables.shape
+    pool = k_pool.shape
     if q_start.shape != (N + 1,) or context_lens.shape != (N,) or tree_masks.shape != (T,):
         raise ValueError("q_start must have N + 1 entries, context_lens N and tree_masks T")
-    if k_pool.shape != v_pool.shape or k_pool.shape[3] != d:
+    if pool != v_pool.shape or pool[3] != d:
         raise ValueError("shape mismatch between q and the pools")
     if max_nodes is None:
-        qs = q_start.cpu()
-        max_nodes = max(1, int((qs[1:] - qs[:-1]).max().item())) if N > 0 else 1
+        max_nodes = _largest_chunk(q_start, N)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need_cuda("out", out, q.dtype)
+        _arg("out", out, dt, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    _check_err(err)
-    dev = q.device
-    _same_device(dev, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables, context_lens=context_lens,
-                 q_start=q_start, tree_masks=tree_masks, out=out, workspace=workspace, err=err)
-    shape = _pool_shape(k_pool, N, Hq, block_tables.shape[1])
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    shape = _lib.PaShape(N, Hq, pool[1], d, pool[2], pool[0], MB, _DTYPES[dt])
     if workspace is None:
-        # 0 bytes: an invalid shape or tree size, which the call reports
-        need = _tree_workspace_bytes(dev, shape, max_nodes)
-        if need and not torch.cuda.is_current_stream_capturing():
-            workspace = _shared_workspace(dev, need)
-        else:
-            # a captured call keeps a workspace of its graph's own: the shared one may be
-            # replaced by a larger one, and another graph may run beside this one
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _tree_workspace(dev, shape, max_nodes)
     else:
-        _need_cuda("workspace", workspace)
+        _arg("workspace", workspace, workspace.dtype, dev)
     st = _call(_lib.load().pa_decode_tree, dev, shape, max_nodes, T, q.data_ptr(), q_start.data_ptr(),
                tree_masks.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
-               context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), _addr(err), _raw_stream(dev))
-    _lib.check(st, "pa_decode_tree")
+               context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _addr(err),
+               _raw_stream(dev))
+    if st:
+        _lib.check(st, "pa_decode_tree")
     return out
 
 
@@ -386,36 +396,34 @@ def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_len
     """The drafted path that the target model's tokens agree with (see
     include/pa.h).  Returns (path int32 [N, max_nodes], num_accepted int32 [N],
     next_tokens int64 [N], new_context_lens int32 [N])."""
-    _need_cuda("tree_masks", tree_masks, torch.int64)
-    _need_cuda("draft_tokens", draft_tokens, torch.int64)
-    _need_cuda("target_tokens", target_tokens, torch.int64)
-    _need_cuda("q_start", q_start, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
+    dev = _index("tree_masks", tree_masks)
+    _arg("tree_masks", tree_masks, torch.int64, dev)
+    _arg("draft_tokens", draft_tokens, torch.int64, dev)
+    _arg("target_tokens", target_tokens, torch.int64, dev)
+    _arg("q_start", q_start, torch.int32, dev)
+    _arg("context_lens", context_lens, torch.int32, dev)
     if tree_masks.dim() != 1 or context_lens.dim() != 1:
         raise ValueError("tree_masks [T], context_lens [N]")
     T, N = tree_masks.shape[0], context_lens.shape[0]
     if draft_tokens.shape != (T,) or target_tokens.shape != (T,) or q_start.shape != (N + 1,):
         raise ValueError("draft_tokens and target_tokens must have tree_masks' shape, q_start N + 1 entries")
     if max_nodes is None:
-        qs = q_start.cpu()
-        max_nodes = max(1, int((qs[1:] - qs[:-1]).max().item())) if N > 0 else 1
-    dev = tree_masks.device
+        max_nodes = _largest_chunk(q_start, N)
     if path is None:
-        path = torch.empty((N, max(0, max_nodes)), dtype=torch.int32, device=dev)
+        path = torch.empty((N, max(0, max_nodes)), dtype=torch.int32, device=context_lens.device)
     else:
-        _need_cuda("path", path, torch.int32)
+        _arg("path", path, torch.int32, dev)
         if path.shape != (N, max_nodes):
             raise ValueError("path must be [N, max_nodes]")
-    _check_err(err)
-    _same_device(dev, draft_tokens=draft_tokens, target_tokens=target_tokens, q_start=q_start,
-                 context_lens=context_lens, path=path, err=err)
-    counts = torch.empty((2, N), dtype=torch.int32, device=dev)
-    accepted, lens = counts[0], counts[1]
-    following = torch.empty(N, dtype=torch.int64, device=dev)
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    accepted, lens = torch.empty_like(context_lens), torch.empty_like(context_lens)
+    following = torch.empty(N, dtype=torch.int64, device=context_lens.device)
     st = _call(_lib.load().pa_tree_verify, dev, N, max_nodes, T, q_start.data_ptr(), tree_masks.data_ptr(),
                draft_tokens.data_ptr(), target_tokens.data_ptr(), context_lens.data_ptr(), path.data_ptr(),
                accepted.data_ptr(), following.data_ptr(), lens.data_ptr(), _addr(err), _raw_stream(dev))
-    _lib.check(st, "pa_tree_verify")
+    if st:
+        _lib.check(st, "pa_tree_verify")
     return path, accepted, following, lens
 
 
@@ -424,46 +432,49 @@ def pa_keep_kv(path, q_start, context_lens, block_tables, k_pool, v_pool, err=No
     """Move the accepted tokens' K and V rows to consecutive positions behind
     each sequence's context (see include/pa.h); path int32 [N, max_nodes] and
     the context lengths are those of the tree."""
-    _need_cuda("k_pool", k_pool)
-    _need_cuda("v_pool", v_pool, k_pool.dtype)
-    _need_cuda("path", path, torch.int32)
-    _need_cuda("q_start", q_start, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    if k_pool.dtype not in _DTYPES:
+    dev = _index("k_pool", k_pool)
+    dt = k_pool.dtype
+    if dt not in _DTYPES:
         raise TypeError("the pools must be float16 or bfloat16")
-    if path.dim() != 2 or block_tables.dim() != 2 or k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+    _arg("k_pool", k_pool, dt, dev)
+    _arg("v_pool", v_pool, dt, dev)
+    _arg("path", path, torch.int32, dev)
+    _arg("q_start", q_start, torch.int32, dev)
+    _arg("context_lens", context_lens, torch.int32, dev)
+    _arg("block_tables", block_tables, torch.int32, dev)
+    pool = k_pool.shape
+    if path.dim() != 2 or block_tables.dim() != 2 or len(pool) != 4 or pool != v_pool.shape:
         raise ValueError("path [N, max_nodes], block_tables [N, MB], k_pool and v_pool [NB, Hkv, B, d]")
     N, P = path.shape
     if q_start.shape != (N + 1,) or context_lens.shape != (N,) or block_tables.shape[0] != N:
         raise ValueError("q_start must have N + 1 entries, context_lens and block_tables N")
-    _check_err(err)
-    dev = k_pool.device
-    _same_device(dev, v_pool=v_pool, path=path, q_start=q_start, context_lens=context_lens,
-                 block_tables=block_tables, err=err)
-    shape = _pool_shape(k_pool, N, 1, block_tables.shape[1])
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    shape = _lib.PaShape(N, 1, pool[1], pool[3], pool[2], pool[0], block_tables.shape[1], _DTYPES[dt])
     st = _call(_lib.load().pa_keep_kv, dev, shape, P, path.data_ptr(), q_start.data_ptr(), block_tables.data_ptr(),
                context_lens.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), _addr(err), _raw_stream(dev))
-    _lib.check(st, "pa_keep_kv")
+    if st:
+        _lib.check(st, "pa_keep_kv")
 
 
-def _token_rows(name, t, dtype):
-    """[T, H, d] with contiguous heads, tokens any (16-byte) stride apart."""
+def _token_rows(name, t, dtype, shape, device):
+    """Elements between the tokens of ``t`` [T, H, d], whose heads are
+    contiguous within a token."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dtype != dtype:
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, heads, d]")
-    T, H, d = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    T, H, d = shape
     st, sh, sd = t.stride()
     if T <= 1:
-        st = H * d if st < H * d or st % 8 else st      # a single token: its stride is never used
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        return H * d                                    # a single token's stride is never used
+    if sd != 1 or (sh != d and H > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if T > 1 and st < H * d:
+    if st < H * d:
         raise ValueError(f"{name}: tokens must not overlap")
     return st
 
@@ -476,49 +487,56 @@ def pa_rope_append_kv(q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, 
     [T, Hq, d] (see include/pa.h).  q, k_new, v_new [T, heads, d] may be views
     of one projection's output; inv_freq [rotary_dim / 2] fp32 as from
     ``rope_inv_freq()``, or None for no rotation; out may be q."""
-    _need_cuda("k_pool", k_pool)
+    dev = _index("k_pool", k_pool)
     dt = k_pool.dtype
     if dt not in _DTYPES:
         raise TypeError("the pools must be float16 or bfloat16")
-    _need_cuda("v_pool", v_pool, dt)
-    qs, ks, vs = _token_rows("q", q, dt), _token_rows("k_new", k_new, dt), _token_rows("v_new", v_new, dt)
-    _need_cuda("positions", positions, torch.int32)
-    _need_cuda("slot_mapping", slot_mapping, torch.int64)
-    T, Hq, d = q.shape
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.shape[3] != d:
-        raise ValueError("k_pool and v_pool must be [NB, Hkv, B, d] with q's d")
-    if k_new.shape != (T, k_pool.shape[1], d) or v_new.shape != k_new.shape:
-        raise ValueError("k_new, v_new must be [T, Hkv, d]")
+    _arg("k_pool", k_pool, dt, dev)
+    _arg("v_pool", v_pool, dt, dev)
+    pool = k_pool.shape
+    if len(pool) != 4 or pool != v_pool.shape:
+        raise ValueError("k_pool and v_pool must be [NB, Hkv, B, d]")
+    NB, Hkv, B, d = pool
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be a tensor [T, Hq, d] with the pools' d")
+    T, Hq, _ = q.shape
+    qs = _token_rows("q", q, dt, (T, Hq, d), dev)
+    ks = _token_rows("k_new", k_new, dt, (T, Hkv, d), dev)
+    vs = _token_rows("v_new", v_new, dt, (T, Hkv, d), dev)
+    _arg("positions", positions, torch.int32, dev)
+    _arg("slot_mapping", slot_mapping, torch.int64, dev)
     if positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("positions and slot_mapping must be [T]")
     rotary = 0
     if inv_freq is not None:
-        _need_cuda("inv_freq", inv_freq, torch.float32)
+        _arg("inv_freq", inv_freq, torch.float32, dev)
         if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
             raise ValueError("inv_freq must be [rotary_dim / 2] with rotary_dim <= d")
         rotary = 2 * inv_freq.shape[0]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need_cuda(name, w, dt)
-            if w.shape != (d,):
-                raise ValueError(f"{name} must be [d]")
+    if q_weight is not None:
+        _arg("q_weight", q_weight, dt, dev)
+        if q_weight.shape != (d,):
+            raise ValueError("q_weight must be [d]")
+    if k_weight is not None:
+        _arg("k_weight", k_weight, dt, dev)
+        if k_weight.shape != (d,):
+            raise ValueError("k_weight must be [d]")
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((T, Hq, d), dtype=dt, device=q.device)
     else:
-        _need_cuda("out", out, dt)
+        _arg("out", out, dt, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    _check_err(err)
-    dev = k_pool.device
-    _same_device(dev, q=q, k_new=k_new, v_new=v_new, v_pool=v_pool, positions=positions, slot_mapping=slot_mapping,
-                 inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight, out=out, err=err)
-    shape = _pool_shape(k_pool, 0, Hq)
-    rope = _lib.PaRope(_addr(inv_freq) if rotary else None, rotary, int(bool(interleaved)), rope_scale, eps,
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    shape = _lib.PaShape(0, Hq, Hkv, d, B, NB, 1, _DTYPES[dt])
+    rope = _lib.PaRope(_addr(inv_freq) if rotary else None, rotary, 1 if interleaved else 0, rope_scale, eps,
                        _addr(q_weight), _addr(k_weight))
     st = _call(_lib.load().pa_rope_append_kv, dev, shape, rope, T, q.data_ptr(), qs, k_new.data_ptr(), ks,
                v_new.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), out.data_ptr(),
                k_pool.data_ptr(), v_pool.data_ptr(), _addr(err), _raw_stream(dev))
-    _lib.check(st, "pa_rope_append_kv")
+    if st:
+        _lib.check(st, "pa_rope_append_kv")
     return out
 
 
@@ -527,11 +545,15 @@ _sp_cache = {}
 
 def _shared_workspace(device, need, stream=None):
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device.index, s.cuda_stream)
+    return _kept_workspace(device.index, s.cuda_stream, need)
+
+
+def _kept_workspace(index, stream_handle, need):
+    key = (index, stream_handle)
     with _ws_lock:
         ws = _sp_cache.get(key)
         if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{index}")
             _sp_cache[key] = ws
         return ws
 
