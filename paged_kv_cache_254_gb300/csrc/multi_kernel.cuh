@@ -218,7 +218,10 @@ struct MultiParams {
     int32_t q_box;                // tokens per Q tile copy (tensor-core kernel: min(max_q, T))
     // drafted trees (TREE kernels)
     const uint64_t* tree_masks;   // [T] the nodes of its own tree that a node sees
-    int32_t tiles;                // 128-row tiles of a tree; d.Hkv counts (KV head, tile) pairs
+    // Trees of more query rows than a kernel's tile holds come in `groups` groups of
+    // group_nodes nodes: the work list (d.cum) counts d.N * groups sequences, all of
+    // group 0 first, and a sequence has blocks only in the groups it has nodes in.
+    int32_t groups, group_nodes;
 };
 
 template <class Tr>
@@ -555,14 +558,14 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 constexpr int MERGE_THREADS = 512;
 constexpr int MERGE_PIECES = 4;
 
-// TREE: Hkv counts (KV head, tile) pairs of `tiles` tiles; a tile holds
-// rows_per_chunk rows.
+// TREE: the work list's sequences are (group, sequence) pairs, N / groups
+// sequences to a group of group_nodes nodes.
 template <int D, bool TREE = false>
 __global__ void __launch_bounds__(MERGE_THREADS)
 pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_start,
                const int32_t* __restrict__ context_lens, const float* __restrict__ partials,
                uint16_t* __restrict__ out, int N, int Hkv, int G, int rows_per_chunk, int nchunks_hint,
-               int max_q, int total_q, int bf16, int tiles) {
+               int max_q, int total_q, int bf16, int groups, int group_nodes) {
     griddep_wait();   // the attention grid is complete and its writes visible
     constexpr int PSTRIDE = D + 4;
     constexpr int LPR = D / 4;                    // lanes per row
@@ -590,22 +593,21 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
     const int s = a;
     const int nb = (int)(cum[s + 1] - cum[s]);
     if (nb == 0) return;
-    const int pair = (int)((x - cum[s] * Hkv) / nb);
-    const long long P0 = cum[s] * Hkv + (long long)pair * nb;
+    const int kvh = (int)((x - cum[s] * Hkv) / nb);
+    const long long P0 = cum[s] * Hkv + (long long)kvh * nb;
     if (P0 == x || sc.lo(c - 1) > P0) return;     // not cut here, or cut first by an earlier boundary
-    const int q0 = q_start[s], qb = q_start[s + 1];
+    const int seq = TREE ? s % (N / groups) : s;
+    const int skip = TREE ? s / (N / groups) * group_nodes : 0;    // the group's first node
+    const int q0 = q_start[seq], qb = q_start[seq + 1];
     const int n_all = qb - q0;
-    const int ctx = context_lens[s];
+    const int ctx = context_lens[seq];
     if (q0 < 0 || qb > total_q || n_all < 0 || n_all > max_q || n_all > ctx) return;    // reported by the kernel
-    const int kvh = TREE ? pair / tiles : pair;
-    const int heads = TREE ? Hkv / tiles : Hkv;
-    const int skip = TREE ? (pair % tiles) * (rows_per_chunk / G) : 0;     // the tile's first node
-    const int qa = q0 + skip, n = TREE ? min(rows_per_chunk / G, n_all - skip) : n_all;
+    const int qa = q0 + skip, n = TREE ? min(group_nodes, n_all - skip) : n_all;
     const long long cfirst = sc.of(P0), clast = sc.of(P0 + nb - 1);
     const size_t cstride = (size_t)2 * rows_per_chunk * PSTRIDE;
     const int np = (int)(clast - cfirst) + 1;
     const int d0 = sub * 4;
-    const int Hq = heads * G;
+    const int Hq = Hkv * G;
     for (int base = warp * RPW; base < n * G; base += nwarps * RPW) {
         const int rr = base + lane / LPR;
         const bool writer = rr < n * G;

@@ -117,9 +117,7 @@ struct TcTraits {
     static_assert(O_COL + D <= P_COL && P_COL + 128 <= TMEM_COLS, "tensor memory");
 };
 
-// One ring stage as the copy warp describes it to the consumers.  Trees: n
-// counts the nodes of the segment's tile and q0 is the tile's first row; the
-// tree's own n follows from ctx and base.
+// One ring stage as the copy warp describes it to the consumers.
 struct alignas(16) TcStage {
     int base, kvh, t0, nkeys;    // first position of the chunk, KV head, first key, keys copied (blocks x B)
     int n, ctx, q0, flags;       // chunk length, context, first query row of the sequence
@@ -165,8 +163,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int HKV = Tr::TREE ? p.Hkv / mp.tiles : p.Hkv;      // KV heads of the pool
-    const int G = p.Hq / HKV;
+    const int G = p.Hq / p.Hkv;
     const uint32_t sbase = smem_u32(smem);
     const int qrows = Tr::q_rows(mp.q_box, G);
     const uint32_t q_half = (uint32_t)qrows * 128;            // between the Q tile's column halves
@@ -272,14 +269,10 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             SegIter it = locate(p, tab, lo, lane);
             while (ok && it.gi < hi) {
                 const int len = seg_len(it, hi);
-                const int n_all = chunk_len(it.s);
-                // a tree's nodes come in tiles of ROWS / G; p.Hkv counts (KV head, tile) pairs
-                const int kvh = Tr::TREE ? it.kvh / mp.tiles : it.kvh;
-                const int skip = Tr::TREE ? (it.kvh - kvh * mp.tiles) * (Tr::ROWS / G) : 0;
-                const int n = Tr::TREE ? min(Tr::ROWS / G, n_all - skip) : n_all;
+                const int n = chunk_len(it.s);
                 if (n > 0) {
                     const int ctx = __ldg(p.context_lens + it.s);
-                    const int q0 = __ldg(qst + it.s) + skip;
+                    const int q0 = __ldg(qst + it.s);
                     const long long P0 = it.gi - it.b0;
                     const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
                     const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
@@ -290,7 +283,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             mbar_arrive_expect_tx(q_full, (uint32_t)(HALVES * 128 * G * mp.q_box));
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
-                                tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, kvh * G, q0, q_full);
+                                tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, it.kvh * G, q0, q_full);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -322,8 +315,8 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     }
                                 if (poison) set_err(p.err, PA_DEVERR_BLOCK_ID);
                                 TcStage& rc = recs[st];
-                                rc.base = ctx - n_all;
-                                rc.kvh = kvh;
+                                rc.base = ctx - n;
+                                rc.kvh = it.kvh;
                                 if constexpr (Tr::TREE) rc.spoilt[0] = rc.spoilt[1] = 0u;
                                 rc.t0 = (it.b0 + bb) * BS;
                                 rc.nkeys = nbs * BS;
@@ -347,7 +340,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             const int ci = kl ? lane : lane - SB;
                             int cid = __shfl_sync(0xffffffffu, ids, (bb + (ci & (SB - 1))) & 31);
                             if ((unsigned)cid >= (unsigned)p.NB) cid = 0;   // flagged and poisoned above
-                            const int y = (cid * HKV + kvh) * BS;
+                            const int y = (cid * p.Hkv + it.kvh) * BS;
                             const uint32_t dst = ring + st * Tr::STAGE_BYTES + (kl ? 0 : Tr::KV_BYTES) + ci * Tr::BLK_BYTES;
                             if (ok && lane < 2 * SB && ci < nbs) {
                                 // each block is read once: L2 evict-first

@@ -17,6 +17,7 @@
 #include "prefix_kernel.cuh"
 #include "rope_ops.cuh"
 #include "tree_ops.cuh"
+#include "tree_wide_kernel.cuh"
 
 namespace {
 
@@ -117,32 +118,21 @@ size_t decode_region_bytes(const pa_shape* s, long long workers, long long nd) {
     return counters_bytes(s) + cum_bytes(s) + (size_t)(workers + nd) * piece_bytes(s);
 }
 
-// Zero the chunk counter; cum[s] = blocks of the
-// sequences before s in the decode work list (with a shared-prefix pass,
-// blocks after each sequence's first_blocks).  One CTA.
-__global__ void __launch_bounds__(1024)
-pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ first_blocks, int N,
-                  int MB, int BS, int32_t* __restrict__ counters, long long n_counters,
-                  long long* __restrict__ cum) {
+// cum[0] = 0, cum[i + 1] = value(0) + .. + value(i) for i < n, by one CTA of
+// 1024 threads.
+template <class Value>
+__device__ __forceinline__ void prefix_sums(int n, long long* __restrict__ cum, Value value) {
     __shared__ long long wsum[32];
     __shared__ long long carry;
-    griddep_launch_dependents();   // the attention kernel may set up meanwhile; it waits for this grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (long long i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
     if (threadIdx.x == 0) {
         carry = 0;
         cum[0] = 0;
     }
     __syncthreads();
-    for (int base = 0; base < N; base += 1024) {
+    for (int base = 0; base < n; base += 1024) {
         const int s = base + (int)threadIdx.x;
-        long long v = 0;
-        if (s < N) {
-            const int c = context_lens[s];
-            const int nb = (c > 0 && c <= MB * BS) ? (c + BS - 1) / BS : 0;
-            const int f = first_blocks ? first_blocks[s] : 0;
-            v = nb - f > 0 ? nb - f : 0;
-        }
+        const long long v = s < n ? value(s) : 0;
         long long x = v;
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, x, o);
@@ -160,11 +150,42 @@ pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __res
         }
         __syncthreads();
         const long long incl = carry + (warp > 0 ? wsum[warp - 1] : 0) + x;
-        if (s < N) cum[s + 1] = incl;
+        if (s < n) cum[s + 1] = incl;
         __syncthreads();
         if (threadIdx.x == blockDim.x - 1) carry = incl;
         __syncthreads();
     }
+}
+
+// Zero the chunk counter; cum[s] = blocks of the
+// sequences before s in the decode work list (with a shared-prefix pass,
+// blocks after each sequence's first_blocks).  One CTA.
+__global__ void __launch_bounds__(1024)
+pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ first_blocks, int N,
+                  int MB, int BS, int32_t* __restrict__ counters, long long n_counters,
+                  long long* __restrict__ cum) {
+    griddep_launch_dependents();   // the attention kernel may set up meanwhile; it waits for this grid
+    for (long long i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
+    prefix_sums(N, cum, [&](int s) -> long long {
+        const int c = context_lens[s];
+        const int nb = (c > 0 && c <= MB * BS) ? (c + BS - 1) / BS : 0;
+        const int f = first_blocks ? first_blocks[s] : 0;
+        return nb - f > 0 ? nb - f : 0;
+    });
+}
+
+// The same for trees: (group, sequence) pairs, all sequences of group 0 first.  A
+// sequence has blocks in the groups that it has nodes in, a malformed one nowhere.
+__global__ void __launch_bounds__(1024)
+pa_tree_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ q_start, int N, int groups,
+                int group_nodes, int max_nodes, int total_q, int MB, int BS, long long* __restrict__ cum) {
+    griddep_launch_dependents();
+    prefix_sums(N * groups, cum, [&](int i) -> long long {
+        const int s = i % N, a = q_start[s], b = q_start[s + 1], c = context_lens[s];
+        const long long n = (long long)b - a;
+        const bool ok = a >= 0 && b <= total_q && n <= max_nodes && n <= c && c > 0 && c <= MB * BS;
+        return ok && n > (long long)(i / N) * group_nodes ? (c + BS - 1) / BS : 0;
+    });
 }
 
 template <int D>
@@ -407,12 +428,14 @@ size_t multi_region_bytes(const pa_shape* s, int ctas, int rows) {
 
 // ---------------------------------------------------------------- drafted trees
 // A tree launch: up to 16 query rows per (sequence, KV head) pair on the
-// mma.sync kernel, more on the tcgen05 kernel in tiles of 128 rows (the
-// measurements at kTcMinRows; a tree's masks change neither side).
+// mma.sync kernel, up to 128 on the tcgen05 kernel's tile (the measurements at
+// kTcMinRows; a tree's masks change neither side), more on the two-tile kernel
+// in groups of up to 256 rows.
 struct TreePlan {
     const MultiKernelInfo* k;
-    int tiles;                   // row tiles per tree
-    int nodes_per_tile;
+    int groups, group_nodes;     // row groups per tree, and the nodes of one
+    int tile_nodes;              // nodes of one 128-row tile
+    bool tc;
 };
 
 pa_status plan_tree(const pa_shape* s, int max_nodes, TreePlan* out) {
@@ -421,19 +444,33 @@ pa_status plan_tree(const pa_shape* s, int max_nodes, TreePlan* out) {
     if (st != PA_OK) return st;
     if (max_nodes < 1 || max_nodes > 64) return PA_ERR_INVALID_ARG;
     static const auto tab = [] {
-        struct T { MultiKernelInfo mma[2][2][2], tc[2][2][2]; } x;   // [bf16][d == 128][bs == 32]
+        struct T { MultiKernelInfo mma[2][2][2], tc[2][2][2], wide[2][2][2]; } x;   // [bf16][d == 128][bs == 32]
         tree_table_fp16(x.mma[0]);
         tree_table_bf16(x.mma[1]);
         tree_tc_table_fp16(x.tc[0]);
         tree_tc_table_bf16(x.tc[1]);
+        tree_wide_table_fp16(x.wide[0]);
+        tree_wide_table_bf16(x.wide[1]);
         return x;
     }();
     const int g = s->num_q_heads / s->num_kv_heads, rows = max_nodes * g;
     const int t = s->dtype == PA_BF16, d = s->head_dim == 128, b = s->block_size == 32;
-    out->k = rows >= kTcMinRows ? &tab.tc[t][d][b] : &tab.mma[t][d][b];
-    out->tiles = (rows + out->k->rows - 1) / out->k->rows;
-    out->nodes_per_tile = out->k->rows / g;
-    return (long long)s->num_kv_heads * out->tiles < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
+    out->tc = rows >= kTcMinRows;
+    out->k = rows > 128 ? &tab.wide[t][d][b] : out->tc ? &tab.tc[t][d][b] : &tab.mma[t][d][b];
+    out->group_nodes = out->k->rows / g;
+    out->groups = (max_nodes + out->group_nodes - 1) / out->group_nodes;
+    out->tile_nodes = 128 / g;
+    return (long long)s->num_seqs * out->groups < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
+size_t tree_cum_bytes(const pa_shape* s, int groups) {
+    return (((size_t)s->num_seqs * groups + 1) * sizeof(long long) + 255) & ~size_t(255);
+}
+
+// Scratch of a tree launch: block prefix sums over (group, sequence), two
+// partial states per tile row per CTA.
+size_t tree_region_bytes(const pa_shape* s, const TreePlan& plan, int ctas) {
+    return tree_cum_bytes(s, plan.groups) + (size_t)ctas * 2 * plan.k->rows * (s->head_dim + 4) * sizeof(float);
 }
 
 // Workspace of prefix-aware decode (offsets in off[]): [0] prefix counters,
@@ -907,9 +944,9 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
         const cudaError_t e =
             shape->head_dim == 128
                 ? cudaLaunchKernelEx(&cfg, pa_multi_merge<128>, d.cum, q_start, context_lens, parts, d.out, d.N,
-                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf, 1)
+                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf, 1, 0)
                 : cudaLaunchKernelEx(&cfg, pa_multi_merge<64>, d.cum, q_start, context_lens, parts, d.out, d.N, d.Hkv,
-                                     g, k->rows, ctas, max_q_len, total_q, bf, 1);
+                                     g, k->rows, ctas, max_q_len, total_q, bf, 1, 0);
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -922,7 +959,7 @@ size_t pa_decode_tree_workspace_bytes(const pa_shape* shape, int32_t max_nodes) 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     const int ctas = plan.k->max_ctas(dev);
-    return ctas > 0 ? multi_region_bytes(shape, ctas, plan.k->rows) : 0;
+    return ctas > 0 ? tree_region_bytes(shape, plan, ctas) : 0;
 }
 
 pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total_q, const void* q,
@@ -945,16 +982,16 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
     // with no query rows at all the mma.sync kernel only checks the trees' sizes
     if (total_q == 0 && plan_tree(shape, 1, &plan) != PA_OK) return PA_ERR_UNSUPPORTED;
-    const bool tc = plan.k->rows > 16 && total_q > 0;
+    const bool tc = plan.tc;
     const int ctas = plan.k->max_ctas(dev);
     if (ctas <= 0) return PA_ERR_CUDA;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < multi_region_bytes(shape, ctas, plan.k->rows))
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < tree_region_bytes(shape, plan, ctas))
         return PA_ERR_WORKSPACE;
     CUtensorMap mk, mv, mq;
     if (!(tc ? pool_map_groups(&mk, k_pool, shape) : pool_map_chunk(&mk, k_pool, shape)) ||
         !pool_map_chunk(&mv, v_pool, shape))
         return PA_ERR_CUDA;
-    const int q_box = std::min({(int)max_nodes, plan.nodes_per_tile, (int)total_q});
+    const int q_box = std::min({(int)max_nodes, plan.tile_nodes, (int)total_q});
     if (tc && !q_map(&mq, q, shape, total_q, q_box)) return PA_ERR_CUDA;
 
     uint8_t* base = static_cast<uint8_t*>(workspace);
@@ -968,12 +1005,11 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     d.context_lens = context_lens;
     d.out = static_cast<uint16_t*>(out);
     d.err = err_word;
-    d.chunk_ctr = reinterpret_cast<int32_t*>(base);
-    d.cum = reinterpret_cast<const long long*>(base + counters_bytes(shape));
-    d.partials = reinterpret_cast<float*>(base + counters_bytes(shape) + cum_bytes(shape));
+    d.cum = reinterpret_cast<const long long*>(base);
+    d.partials = reinterpret_cast<float*>(base + tree_cum_bytes(shape, plan.groups));
     d.N = shape->num_seqs;
     d.Hq = shape->num_q_heads;
-    d.Hkv = shape->num_kv_heads * plan.tiles;
+    d.Hkv = shape->num_kv_heads;
     d.NB = shape->num_blocks;
     d.MB = shape->max_blocks_per_seq;
     d.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
@@ -984,12 +1020,13 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     L.p.total_q = total_q;
     L.p.q_box = q_box;
     L.p.tree_masks = tree_masks;
-    L.p.tiles = plan.tiles;
+    L.p.groups = plan.groups;
+    L.p.group_nodes = plan.group_nodes;
     L.stream = static_cast<cudaStream_t>(stream);
     L.grid = ctas;
-    pa_decode_prepass<<<1, 1024, 0, L.stream>>>(context_lens, nullptr, shape->num_seqs,
-                                                shape->max_blocks_per_seq, shape->block_size, d.chunk_ctr, 1,
-                                                const_cast<long long*>(d.cum));
+    pa_tree_prepass<<<1, 1024, 0, L.stream>>>(context_lens, q_start, shape->num_seqs, plan.groups, plan.group_nodes,
+                                              max_nodes, total_q, shape->max_blocks_per_seq, shape->block_size,
+                                              const_cast<long long*>(d.cum));
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     if (plan.k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
     if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
@@ -998,9 +1035,9 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
         const cudaLaunchConfig_t cfg = pdl_config(ctas - 1, MERGE_THREADS, 0, L.stream, attr);
         const float* parts = d.partials;
         const auto merge = shape->head_dim == 128 ? pa_multi_merge<128, true> : pa_multi_merge<64, true>;
-        if (cudaLaunchKernelEx(&cfg, merge, d.cum, q_start, context_lens, parts, d.out, d.N, d.Hkv, g, plan.k->rows,
-                               ctas, (int)max_nodes, (int)total_q, (int)(shape->dtype == PA_BF16), plan.tiles) !=
-            cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, merge, d.cum, q_start, context_lens, parts, d.out, d.N * plan.groups, d.Hkv, g,
+                               plan.k->rows, ctas, (int)max_nodes, (int)total_q, (int)(shape->dtype == PA_BF16),
+                               plan.groups, plan.group_nodes) != cudaSuccess)
             return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
