@@ -83,17 +83,13 @@ __device__ __forceinline__ uint64_t node_bits(uint64_t mask, int n) {
     return n >= 64 ? mask : mask & ((1ull << n) - 1);
 }
 
-// Does a 32-bit word hold an infinite or NaN 16-bit value?
-template <bool BF16>
-__device__ __forceinline__ bool pair_not_finite(uint32_t w) {
-    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
-    return (w & E) == E || ((w >> 16) & E) == E;
-}
-
+// Does a vector of eight 16-bit values hold an infinity or NaN?  Adding one to the
+// exponent carries into the sign's place exactly when it is all ones.
 template <bool BF16>
 __device__ __forceinline__ bool vec_not_finite(const uint4& v) {
-    return pair_not_finite<BF16>(v.x) || pair_not_finite<BF16>(v.y) || pair_not_finite<BF16>(v.z) ||
-           pair_not_finite<BF16>(v.w);
+    constexpr uint32_t ONE = BF16 ? 0x00800080u : 0x04000400u;
+    auto carry = [](uint32_t w) -> uint32_t { return (w & 0x7fff7fffu) + ONE; };
+    return ((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) != 0;
 }
 
 // consume_block for query rows with their own key limits: valid[r] keys of

@@ -65,7 +65,9 @@ struct WideTraits {
     static constexpr int REC_OFF = (8 * NBAR + 15) / 16 * 16;
     static constexpr int MISC_OFF = REC_OFF + NREC * 48;
     static constexpr int Q_OFF = (MISC_OFF + 16 + 1023) / 1024 * 1024;
-    static constexpr int RING_OFF = Q_OFF + Q_BYTES;
+    static constexpr int OUT_OFF = Q_OFF + Q_BYTES;          // per softmax warp: 32 rows of 128 bytes on their way out
+    static constexpr int OUT_BYTES = 32 * 128;
+    static constexpr int RING_OFF = OUT_OFF + 8 * OUT_BYTES;
     static constexpr int R_FIT = (SMEM_BYTES - 1024 - RING_OFF) / SLOT_BYTES;
     static constexpr int R = R_FIT > R_CAP ? R_CAP : R_FIT;  // ring slots
     static constexpr int THREADS = 384;
@@ -106,7 +108,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int G = p.Hq / p.Hkv;
+    const int G = p.Hq / p.Hkv, gs = 31 - __clz(G);           // a power of two
     const uint32_t sbase = smem_u32(smem);
     const uint32_t q_base = sbase + Tr::Q_OFF, ring = sbase + Tr::RING_OFF;
     auto full = [&](int st) -> uint32_t { return sbase + 8 * st; };
@@ -183,7 +185,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     const long long lo = has_work ? sc.lo(blockIdx.x) : 0, hi = has_work ? sc.lo(blockIdx.x + 1) : 0;
 
     if (warp >= Tr::COPY_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == Tr::COPY_WARP) {
             // ============================================================ copies
             // with one group the keys are read once per call; with more, another CTA
@@ -216,7 +218,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                     const long long P0 = it.gi - it.b0;
                     const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
                     const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
-                    const int tile_nodes = Tr::TILE / G;
+                    const int tile_nodes = Tr::TILE >> gs;
                     if (lane == 0) {
                         if (nseg > 0 && !mbar_wait_bounded(q_empty, (uint32_t)((nseg - 1) & 1), p.timeout_ns)) {
                             ok = false;
@@ -376,7 +378,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
             // ============================================================ MMAs of one tile
             const int t = warp - Tr::MMA_WARP;
             const uint32_t s_col = tmem + 128 * t, o_col = tmem + Tr::O_COL + 128 * t;
-            const int tile_rows0 = t * (Tr::TILE / G);            // first node of the tile
+            const int tile_rows0 = t * (Tr::TILE >> gs);          // first node of the tile
             int st = 0, nseg = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -462,11 +464,11 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
         __syncwarp();
     } else {
         // ================================================================ softmax
-        // 256 x 200 + 128 x 104 registers: the 384 x 168 of the launch
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // 256 x 216 + 128 x 72 registers: the 384 x 168 of the launch
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int t = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;                        // row of the tile = TMEM lane
-        const int node = (t * Tr::TILE + r) / G;                  // node of the group
+        const int node = (t * Tr::TILE + r) >> gs;                // node of the group
         auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.timeout_ns));
         };
@@ -499,8 +501,8 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                 m = -INFINITY;
                 l = 0.f;
                 pois = 0;
-                alive = node < rc.n && r < Tr::TILE / G * G;
-                active = rc.n > t * (Tr::TILE / G);
+                alive = node < rc.n;
+                active = rc.n > t * (Tr::TILE >> gs);
                 sees = alive ? node_bits(__ldg(mp.tree_masks + seg_q0 + node), rc.ctx - base) : 0;
             }
             pois |= rc.poison;
@@ -633,56 +635,62 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                 }
                 if (busy) {
                     tc_fence_after();
-                    if (flags & TC_COMPLETE) {
-                        uint16_t* orow = p.out + ((size_t)(seg_q0 + node) * p.Hq + (size_t)seg_kvh * G + r % G) * D;
-                        const float inv = l == 0.f ? 0.f : 1.f / l;   // a node that sees no key: zero
+                    // 128 bytes of each row at a time (64 finished values, or 32 of a partial
+                    // state) go through shared memory, so that 8 lanes write a row's piece
+                    uint8_t* out = smem + Tr::OUT_OFF + warp * Tr::OUT_BYTES;
+                    const bool complete = flags & TC_COMPLETE;
+                    const float inv = pois ? qnan : complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;   // a node that sees no key: zero
+                    constexpr int PIECES = D / 32;
+                    const unsigned rows = __ballot_sync(0xffffffffu, alive);
+                    const int row0 = t * Tr::TILE + quarter * 32;                 // the warp's first row of the group
+#pragma unroll 1
+                    for (int c = 0; c < PIECES; ++c) {
+                        uint32_t u[32];
+                        tmem_ld32(o_addr + 32 * c, u);
+                        tmem_ld_wait();
+                        after_wait(u);
+                        const int half = complete ? c & 1 : 0;                    // which half of the 128 bytes
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t u[32];
-                            tmem_ld32(o_addr + 32 * c, u);
-                            tmem_ld_wait();
-                            after_wait(u);
-                            uint32_t w[16];
+                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * inv);
+                        if (complete) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float o0 = pois ? qnan : __uint_as_float(u[2 * k]) * inv;
-                                const float o1 = pois ? qnan : __uint_as_float(u[2 * k + 1]) * inv;
-                                w[k] = pack2<Tr::BF16>(o0, o1);
+                            for (int k = 0; k < 4; ++k) {
+                                auto two = [&](int i) -> uint32_t {
+                                    return pack2<Tr::BF16>(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+                                };
+                                *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * half + k) ^ (lane & 7)) << 4)) =
+                                    make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
                             }
-                            if (alive) {
-                                uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+                            if (half == 0) continue;
+                        } else {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                            for (int k = 0; k < 8; ++k)
+                                *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                    make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                        }
+                        __syncwarp();
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = 4 * i + lane / 8, part = lane & 7;
+                            const uint4 v = *reinterpret_cast<const uint4*>(out + rr * 128 + ((part ^ (rr & 7)) << 4));
+                            if (!((rows >> rr) & 1)) continue;
+                            const int row = row0 + rr;
+                            if (complete) {
+                                uint16_t* orow = p.out + ((size_t)(seg_q0 + (row >> gs)) * p.Hq + (size_t)seg_kvh * G + (row & (G - 1))) * D;
+                                *reinterpret_cast<uint4*>(orow + 64 * (c / 2) + 8 * part) = v;
+                            } else {
+                                float* prow = p.partials + (((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS +
+                                                            row) * Tr::PSTRIDE;
+                                *reinterpret_cast<uint4*>(prow + 32 * c + 4 * part) = v;
                             }
                         }
-                    } else {
-                        float* prow = p.partials +
-                                      (((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS + t * Tr::TILE + r) *
-                                          Tr::PSTRIDE;
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t u[32];
-                            tmem_ld32(o_addr + 32 * c, u);
-                            tmem_ld_wait();
-                            after_wait(u);
-                            if (alive) {
-                                float4* dst = reinterpret_cast<float4*>(prow + 32 * c);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    float4 v;
-                                    v.x = pois ? qnan : __uint_as_float(u[4 * k]);
-                                    v.y = pois ? qnan : __uint_as_float(u[4 * k + 1]);
-                                    v.z = pois ? qnan : __uint_as_float(u[4 * k + 2]);
-                                    v.w = pois ? qnan : __uint_as_float(u[4 * k + 3]);
-                                    dst[k] = v;
-                                }
-                            }
-                        }
-                        if (alive) {
-                            prow[D] = m;
-                            prow[D + 1] = l;
-                        }
+                        __syncwarp();
+                    }
+                    if (alive && !complete) {
+                        float* prow = p.partials + (((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS + row0 +
+                                                    lane) * Tr::PSTRIDE;
+                        prow[D] = m;
+                        prow[D + 1] = l;
                     }
                     tc_fence_before();
                 }
