@@ -49,6 +49,7 @@ struct MultiTraits {
     static constexpr int ROWS = 16 * NW;
     static constexpr bool BF16 = BF16_;
     static constexpr bool TREE = TREE_;                     // drafted trees: visible keys by ancestor masks
+    static constexpr int MIN_CHUNK = 64 / BS_;              // trees: blocks of a CTA's chunk at least
     static constexpr int THREADS = 32 * NW;
     // about 8 warps per SM: 6 / 4 / 2 / 1 CTAs of 1 / 2 / 4 / 8 warps, sharing
     // ~190 KiB of stages
@@ -64,7 +65,8 @@ struct MultiTraits {
     static constexpr int QS_OFF = CTX_OFF + CUM_SMEM * 4;
     static constexpr int PS_OFF = QS_OFF + (CUM_SMEM + 1) * 4;
     static constexpr int AB_OFF = PS_OFF + R * 4;
-    static constexpr int SMEM_BYTES = AB_OFF + 16 + 1024;  // + alignment slack
+    static constexpr int START_OFF = AB_OFF + 16;           // trees: NW words and a TreeStart
+    static constexpr int SMEM_BYTES = AB_OFF + 16 + (TREE ? 48 + 8 * NW : 0) + 1024;  // + alignment slack
     static_assert(R >= 2, "ring");
     static_assert(NW == 1 || NW == 2 || NW == 4 || NW == 8, "warps");
 };
@@ -206,6 +208,94 @@ __device__ __forceinline__ void consume_block_rows(uint32_t kb, uint32_t vb, con
         }
 }
 
+// The work list of trees.  Trees of more query rows than a kernel's tile holds come
+// in `groups` groups of group_nodes nodes: the list has N * groups sequences, all
+// of group 0 first.  A sequence has its blocks in the groups that it has nodes in,
+// a malformed one nowhere.
+struct TreeTab {
+    const int* ctx;
+    const int* qst;
+    int N, groups, group_nodes, max_nodes, total_q, MB, BS;
+    __device__ __forceinline__ int nb(int i) const {
+        const int g = groups == 1 ? 0 : i / N, s = i - g * N;
+        const int a = qst[s], b = qst[s + 1], c = ctx[s];
+        const long long n = (long long)b - a;
+        const bool ok = a >= 0 && b <= total_q && n <= max_nodes && n <= c && c > 0 && c <= MB * BS;
+        return ok && n > g * group_nodes ? (c + BS - 1) / BS : 0;
+    }
+    __device__ __forceinline__ int fst(int) const { return 0; }
+};
+
+// Where a CTA's chunk of the list begins, and the list's length in (KV head,
+// block) units; nb is 0 for a CTA without a chunk.
+struct alignas(16) TreeStart {
+    int s, kvh, b0, nb;
+    long long W, pad;
+};
+
+// W blocks in equal chunks, each of min_blocks at least while there are that many.
+__device__ __forceinline__ Sched tree_sched(long long W, int ctas, int min_blocks) {
+    const long long most = W < min_blocks ? (W > 0 ? 1 : 0) : W / min_blocks;
+    Sched sc;
+    sc.W = sc.Ws = W;
+    sc.NS = (int)(most < ctas ? most : ctas);
+    sc.ND = 0;
+    return sc;
+}
+
+// The CTA's own place in the list, found by all of its threads: each counts the
+// blocks of a run of sequences, a scan over the CTA places the runs, and the thread
+// whose run the chunk begins in walks it.  (A pre-pass kernel that writes prefix
+// sums for all, and a search in them, cost three dependent loads more and 3 us.)
+// wsum: THREADS / 32 words, box: one TreeStart, both in shared memory.
+template <int THREADS>
+__device__ __forceinline__ void tree_start(const TreeTab& tab, int Hkv, int min_blocks, long long* wsum,
+                                           TreeStart* box) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = tab.N * tab.groups, per = (n + THREADS - 1) / THREADS;
+    const int i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
+    long long sum = 0;
+    for (int i = i0; i < i1; ++i) sum += tab.nb(i);
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    if (threadIdx.x == 0) box->nb = 0;
+    __syncthreads();
+    long long before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const long long v = wsum[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    const long long W = total * Hkv;
+    if (threadIdx.x == 0) box->W = W;
+    const Sched sc = tree_sched(W, gridDim.x, min_blocks);
+    if ((int)blockIdx.x < sc.NS) {
+        const long long lo = sc.lo(blockIdx.x);
+        if (before * Hkv <= lo && lo < (before + sum) * Hkv) {
+            long long c = before;
+            for (int i = i0; i < i1; ++i) {
+                const int nb = tab.nb(i);
+                if (lo < (c + nb) * Hkv) {
+                    const long long off = lo - c * Hkv;
+                    box->s = i;
+                    box->kvh = (int)(off / nb);
+                    box->b0 = (int)(off % nb);
+                    box->nb = nb;
+                    break;
+                }
+                c += nb;
+            }
+        }
+    }
+    __syncthreads();
+}
+
 struct MultiParams {
     DecodeParams d;               // q / out hold T = q_start[N] token rows
     const int32_t* q_start;       // [N + 1] first query row of each sequence
@@ -214,10 +304,8 @@ struct MultiParams {
     int32_t q_box;                // tokens per Q tile copy (tensor-core kernel: min(max_q, T))
     // drafted trees (TREE kernels)
     const uint64_t* tree_masks;   // [T] the nodes of its own tree that a node sees
-    // Trees of more query rows than a kernel's tile holds come in `groups` groups of
-    // group_nodes nodes: the work list (d.cum) counts d.N * groups sequences, all of
-    // group 0 first, and a sequence has blocks only in the groups it has nodes in.
-    int32_t groups, group_nodes;
+    int32_t groups, group_nodes;  // (TreeTab)
+    struct TreeStart* starts;     // [CTAs] where each CTA's chunk begins
 };
 
 template <class Tr>
@@ -261,18 +349,28 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const bool in_smem = p.N <= Tr::CUM_SMEM;
     if (in_smem) {
         for (int i = threadIdx.x; i <= p.N; i += Tr::THREADS) {
-            scum[i] = __ldg(p.cum + i);
+            if constexpr (!Tr::TREE) scum[i] = __ldg(p.cum + i);
             sqs[i] = __ldg(mp.q_start + i);
             if (i < p.N) sctx[i] = __ldg(p.context_lens + i);
         }
     }
     __syncthreads();
-    SeqTab tab;
-    tab.cum = in_smem ? scum : p.cum;
-    tab.ctx = in_smem ? sctx : p.context_lens;
-    tab.first = nullptr;
     const int* qst = in_smem ? sqs : mp.q_start;
-    const long long* cum = tab.cum;
+    std::conditional_t<Tr::TREE, TreeTab, SeqTab> tab;
+    tab.ctx = in_smem ? sctx : p.context_lens;
+    if constexpr (Tr::TREE) {
+        tab.qst = qst;
+        tab.N = p.N;
+        tab.groups = 1;
+        tab.group_nodes = mp.group_nodes;
+        tab.max_nodes = mp.max_q;
+        tab.total_q = mp.total_q;
+        tab.MB = p.MB;
+        tab.BS = BS;
+    } else {
+        tab.cum = in_smem ? scum : p.cum;
+        tab.first = nullptr;
+    }
     const float qnan = __int_as_float(0x7fc00000);
     // a sequence's chunk length, or -1 when it is malformed
     auto chunk_len = [&](int s) -> int {
@@ -298,10 +396,28 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     }
 
     // ---- this CTA's chunk ----
-    const Sched sc = make_sched(cum[p.N] * p.Hkv, gridDim.x, 0);
-    if ((int)blockIdx.x >= sc.NS) return;
+    Sched sc;
+    SegIter it;
+    if constexpr (Tr::TREE) {
+        uint8_t* room = smem + (Tr::START_OFF + 15) / 16 * 16;
+        const TreeStart& at = *reinterpret_cast<TreeStart*>(room);
+        tree_start<Tr::THREADS>(tab, p.Hkv, Tr::MIN_CHUNK, reinterpret_cast<long long*>(room + 32),
+                                reinterpret_cast<TreeStart*>(room));
+        if (threadIdx.x == 0) mp.starts[blockIdx.x] = at;
+        sc = tree_sched(at.W, gridDim.x, Tr::MIN_CHUNK);
+        if ((int)blockIdx.x >= sc.NS) return;
+        it.gi = sc.lo(blockIdx.x);
+        it.s = at.s;
+        it.kvh = at.kvh;
+        it.b0 = at.b0;
+        it.nb = at.nb;
+        it.first = 0;
+    } else {
+        sc = make_sched(tab.cum[p.N] * p.Hkv, gridDim.x, 0);
+        if ((int)blockIdx.x >= sc.NS) return;
+        it = locate(p, tab, sc.lo(blockIdx.x), lane);
+    }
     const long long lo = sc.lo(blockIdx.x), hi = sc.lo(blockIdx.x + 1);
-    SegIter it = locate(p, tab, lo, lane);
 
     // ---- issue side (lane 0 of warp 0) ----
     SegIter is = it;
@@ -554,14 +670,12 @@ pa_multi_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 constexpr int MERGE_THREADS = 512;
 constexpr int MERGE_PIECES = 4;
 
-// TREE: the work list's sequences are (group, sequence) pairs, N / groups
-// sequences to a group of group_nodes nodes.
-template <int D, bool TREE = false>
+template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS)
 pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_start,
                const int32_t* __restrict__ context_lens, const float* __restrict__ partials,
                uint16_t* __restrict__ out, int N, int Hkv, int G, int rows_per_chunk, int nchunks_hint,
-               int max_q, int total_q, int bf16, int groups, int group_nodes) {
+               int max_q, int total_q, int bf16) {
     griddep_wait();   // the attention grid is complete and its writes visible
     constexpr int PSTRIDE = D + 4;
     constexpr int LPR = D / 4;                    // lanes per row
@@ -592,13 +706,10 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
     const int kvh = (int)((x - cum[s] * Hkv) / nb);
     const long long P0 = cum[s] * Hkv + (long long)kvh * nb;
     if (P0 == x || sc.lo(c - 1) > P0) return;     // not cut here, or cut first by an earlier boundary
-    const int seq = TREE ? s % (N / groups) : s;
-    const int skip = TREE ? s / (N / groups) * group_nodes : 0;    // the group's first node
-    const int q0 = q_start[seq], qb = q_start[seq + 1];
-    const int n_all = qb - q0;
-    const int ctx = context_lens[seq];
-    if (q0 < 0 || qb > total_q || n_all < 0 || n_all > max_q || n_all > ctx) return;    // reported by the kernel
-    const int qa = q0 + skip, n = TREE ? min(group_nodes, n_all - skip) : n_all;
+    const int qa = q_start[s], qb = q_start[s + 1];
+    const int n = qb - qa;
+    const int ctx = context_lens[s];
+    if (qa < 0 || qb > total_q || n < 0 || n > max_q || n > ctx) return;    // reported by the kernel
     const long long cfirst = sc.of(P0), clast = sc.of(P0 + nb - 1);
     const size_t cstride = (size_t)2 * rows_per_chunk * PSTRIDE;
     const int np = (int)(clast - cfirst) + 1;
@@ -658,7 +769,7 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
             }
         }
         if (!writer) continue;
-        const float inv = TREE && L == 0.f ? 0.f : 1.f / L;
+        const float inv = 1.f / L;
         const float xv[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
         uint32_t w[2];
 #pragma unroll
@@ -670,6 +781,111 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
         uint16_t* dst = out + ((size_t)(qa + rr / G) * Hq + (size_t)kvh * G + rr % G) * D + d0;
         *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     }
+}
+
+// The post-pass of trees: as pa_multi_merge, for pairs that few sequences cut into
+// many pieces and for groups of up to 256 rows.
+// blockIdx.x: a chunk boundary, blockIdx.y: a row for each D / 4 lanes of the pair
+// that it is the first to cut; where a chunk begins the attention kernel has
+// written down.  A row's lanes load the (m, l) of a piece each, so that one round
+// of loads weighs D / 4 pieces, then 4 dims of every piece, eight pieces in flight.
+// Bound by three rounds of loads, one after the other.
+constexpr int TREE_MERGE_THREADS = 256;
+constexpr int AHEAD = 4;
+
+template <int D>
+__global__ void __launch_bounds__(TREE_MERGE_THREADS)
+pa_tree_merge(const int32_t* __restrict__ q_start, const TreeStart* __restrict__ starts,
+              const float* __restrict__ partials, uint16_t* __restrict__ out, int seqs, int Hkv, int G,
+              int rows_per_chunk, int ctas, int min_blocks, int bf16, int group_nodes) {
+    constexpr int PSTRIDE = D + 4;
+    constexpr int LPR = D / 4;                    // lanes per row
+    constexpr int ROWS = TREE_MERGE_THREADS / LPR;
+    const int sub = threadIdx.x % LPR;
+    griddep_wait();   // the attention grid is complete and its writes visible
+    const int c = (int)blockIdx.x + 1;            // boundary between chunks c - 1 and c
+    const TreeStart at = starts[c];
+    if (at.nb == 0 || at.b0 == 0) return;         // no such chunk, or its first pair is not cut here
+    const Sched sc = tree_sched(at.W, ctas, min_blocks);
+    const long long P0 = sc.lo(c) - at.b0;
+    if (sc.lo(c - 1) > P0) return;                // cut first by an earlier boundary
+    const int kvh = at.kvh, nb = at.nb, s = at.s % seqs, skip = at.s / seqs * group_nodes;
+    const int q0 = q_start[s] + skip;
+    const int rows = min(group_nodes, q_start[s + 1] - q0) * G;   // a sequence with blocks is well formed
+    const long long cfirst = sc.of(P0);
+    const int np = (int)(sc.of(P0 + nb - 1) - cfirst) + 1;
+    const size_t cstride = (size_t)2 * rows_per_chunk * PSTRIDE;
+    const size_t first_off = sc.lo(cfirst) < P0 ? (size_t)rows_per_chunk * PSTRIDE : 0;
+    const float* base = partials + (size_t)cfirst * cstride;
+    const int r = (int)blockIdx.y * ROWS + (int)threadIdx.x / LPR;
+    if ((int)blockIdx.y * ROWS >= rows) return;
+    const bool writer = r < rows;                 // (the others stay for the exchanges)
+    const int row = writer ? r : 0;
+    auto piece = [&](int i) -> const float* {
+        return base + (size_t)row * PSTRIDE + (i == 0 ? first_off : (size_t)i * cstride);
+    };
+    float4 ahead[AHEAD];                          // the first pieces' dims, beside their (m, l)
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < np) ahead[i] = *reinterpret_cast<const float4*>(piece(i) + 4 * sub);
+    float M = -INFINITY, m_mine = -INFINITY, l_mine = 0.f;
+    for (int i = sub; i < np; i += LPR) {
+        const float* p = piece(i);
+        m_mine = p[D];
+        l_mine = p[D + 1];
+        M = fmaxf(M, m_mine);
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += LPR) {
+        const int n = min(LPR, np - i0);
+        if (np > LPR) {                       // several rounds: this one's piece again
+            m_mine = -INFINITY;
+            l_mine = 0.f;
+            if (sub < n) {
+                const float* p = piece(i0 + sub);
+                m_mine = p[D];
+                l_mine = p[D + 1];
+            }
+        }
+        const float f_mine = ex2(m_mine - ref);
+        L += f_mine * l_mine;                 // (lanes without a piece: 0 * 0)
+        int i = 0;
+        if (i0 == 0) {
+#pragma unroll
+            for (; i < AHEAD; ++i) {
+                const float f = __shfl_sync(0xffffffffu, f_mine, i, LPR);
+                if (i >= np) continue;
+                acc.x += ahead[i].x * f;
+                acc.y += ahead[i].y * f;
+                acc.z += ahead[i].z * f;
+                acc.w += ahead[i].w * f;
+            }
+        }
+#pragma unroll 8
+        for (; i < n; ++i) {
+            const float f = __shfl_sync(0xffffffffu, f_mine, i, LPR);
+            const float4 v = *reinterpret_cast<const float4*>(piece(i0 + i) + 4 * sub);
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (!writer) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // a node that sees no key: zero
+    const float xv[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        w[k] = bf16 ? pack2<true>(xv[2 * k], xv[2 * k + 1]) : pack2<false>(xv[2 * k], xv[2 * k + 1]);
+    uint16_t* dst = out + ((size_t)(q0 + row / G) * Hkv * G + (size_t)kvh * G + row % G) * D + 4 * sub;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
 struct MultiLaunch {

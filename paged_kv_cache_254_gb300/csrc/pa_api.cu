@@ -118,21 +118,32 @@ size_t decode_region_bytes(const pa_shape* s, long long workers, long long nd) {
     return counters_bytes(s) + cum_bytes(s) + (size_t)(workers + nd) * piece_bytes(s);
 }
 
-// cum[0] = 0, cum[i + 1] = value(0) + .. + value(i) for i < n, by one CTA of
-// 1024 threads.
-template <class Value>
-__device__ __forceinline__ void prefix_sums(int n, long long* __restrict__ cum, Value value) {
+// Zero the chunk counter; cum[s] = blocks of the
+// sequences before s in the decode work list (with a shared-prefix pass,
+// blocks after each sequence's first_blocks).  One CTA.
+__global__ void __launch_bounds__(1024)
+pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ first_blocks, int N,
+                  int MB, int BS, int32_t* __restrict__ counters, long long n_counters,
+                  long long* __restrict__ cum) {
     __shared__ long long wsum[32];
     __shared__ long long carry;
+    griddep_launch_dependents();   // the attention kernel may set up meanwhile; it waits for this grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (long long i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
     if (threadIdx.x == 0) {
         carry = 0;
         cum[0] = 0;
     }
     __syncthreads();
-    for (int base = 0; base < n; base += 1024) {
+    for (int base = 0; base < N; base += 1024) {
         const int s = base + (int)threadIdx.x;
-        const long long v = s < n ? value(s) : 0;
+        long long v = 0;
+        if (s < N) {
+            const int c = context_lens[s];
+            const int nb = (c > 0 && c <= MB * BS) ? (c + BS - 1) / BS : 0;
+            const int f = first_blocks ? first_blocks[s] : 0;
+            v = nb - f > 0 ? nb - f : 0;
+        }
         long long x = v;
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, x, o);
@@ -150,42 +161,11 @@ __device__ __forceinline__ void prefix_sums(int n, long long* __restrict__ cum, 
         }
         __syncthreads();
         const long long incl = carry + (warp > 0 ? wsum[warp - 1] : 0) + x;
-        if (s < n) cum[s + 1] = incl;
+        if (s < N) cum[s + 1] = incl;
         __syncthreads();
         if (threadIdx.x == blockDim.x - 1) carry = incl;
         __syncthreads();
     }
-}
-
-// Zero the chunk counter; cum[s] = blocks of the
-// sequences before s in the decode work list (with a shared-prefix pass,
-// blocks after each sequence's first_blocks).  One CTA.
-__global__ void __launch_bounds__(1024)
-pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ first_blocks, int N,
-                  int MB, int BS, int32_t* __restrict__ counters, long long n_counters,
-                  long long* __restrict__ cum) {
-    griddep_launch_dependents();   // the attention kernel may set up meanwhile; it waits for this grid
-    for (long long i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
-    prefix_sums(N, cum, [&](int s) -> long long {
-        const int c = context_lens[s];
-        const int nb = (c > 0 && c <= MB * BS) ? (c + BS - 1) / BS : 0;
-        const int f = first_blocks ? first_blocks[s] : 0;
-        return nb - f > 0 ? nb - f : 0;
-    });
-}
-
-// The same for trees: (group, sequence) pairs, all sequences of group 0 first.  A
-// sequence has blocks in the groups that it has nodes in, a malformed one nowhere.
-__global__ void __launch_bounds__(1024)
-pa_tree_prepass(const int32_t* __restrict__ context_lens, const int32_t* __restrict__ q_start, int N, int groups,
-                int group_nodes, int max_nodes, int total_q, int MB, int BS, long long* __restrict__ cum) {
-    griddep_launch_dependents();
-    prefix_sums(N * groups, cum, [&](int i) -> long long {
-        const int s = i % N, a = q_start[s], b = q_start[s + 1], c = context_lens[s];
-        const long long n = (long long)b - a;
-        const bool ok = a >= 0 && b <= total_q && n <= max_nodes && n <= c && c > 0 && c <= MB * BS;
-        return ok && n > (long long)(i / N) * group_nodes ? (c + BS - 1) / BS : 0;
-    });
 }
 
 template <int D>
@@ -435,6 +415,7 @@ struct TreePlan {
     const MultiKernelInfo* k;
     int groups, group_nodes;     // row groups per tree, and the nodes of one
     int tile_nodes;              // nodes of one 128-row tile
+    int min_blocks;              // of a CTA's chunk: one stage
     bool tc;
 };
 
@@ -460,17 +441,16 @@ pa_status plan_tree(const pa_shape* s, int max_nodes, TreePlan* out) {
     out->group_nodes = out->k->rows / g;
     out->groups = (max_nodes + out->group_nodes - 1) / out->group_nodes;
     out->tile_nodes = 128 / g;
+    out->min_blocks = (rows > 128 ? 128 : 64) / s->block_size;
     return (long long)s->num_seqs * out->groups < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
-size_t tree_cum_bytes(const pa_shape* s, int groups) {
-    return (((size_t)s->num_seqs * groups + 1) * sizeof(long long) + 255) & ~size_t(255);
-}
+size_t tree_starts_bytes(int ctas) { return align256((size_t)ctas * sizeof(TreeStart)); }
 
-// Scratch of a tree launch: block prefix sums over (group, sequence), two
-// partial states per tile row per CTA.
+// Scratch of a tree launch: where each CTA's chunk begins, two partial states
+// per tile row per CTA.
 size_t tree_region_bytes(const pa_shape* s, const TreePlan& plan, int ctas) {
-    return tree_cum_bytes(s, plan.groups) + (size_t)ctas * 2 * plan.k->rows * (s->head_dim + 4) * sizeof(float);
+    return tree_starts_bytes(ctas) + (size_t)ctas * 2 * plan.k->rows * (s->head_dim + 4) * sizeof(float);
 }
 
 // Workspace of prefix-aware decode (offsets in off[]): [0] prefix counters,
@@ -944,9 +924,9 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
         const cudaError_t e =
             shape->head_dim == 128
                 ? cudaLaunchKernelEx(&cfg, pa_multi_merge<128>, d.cum, q_start, context_lens, parts, d.out, d.N,
-                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf, 1, 0)
+                                     d.Hkv, g, k->rows, ctas, max_q_len, total_q, bf)
                 : cudaLaunchKernelEx(&cfg, pa_multi_merge<64>, d.cum, q_start, context_lens, parts, d.out, d.N, d.Hkv,
-                                     g, k->rows, ctas, max_q_len, total_q, bf, 1, 0);
+                                     g, k->rows, ctas, max_q_len, total_q, bf);
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -1005,8 +985,8 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     d.context_lens = context_lens;
     d.out = static_cast<uint16_t*>(out);
     d.err = err_word;
-    d.cum = reinterpret_cast<const long long*>(base);
-    d.partials = reinterpret_cast<float*>(base + tree_cum_bytes(shape, plan.groups));
+    L.p.starts = reinterpret_cast<TreeStart*>(base);
+    d.partials = reinterpret_cast<float*>(base + tree_starts_bytes(ctas));
     d.N = shape->num_seqs;
     d.Hq = shape->num_q_heads;
     d.Hkv = shape->num_kv_heads;
@@ -1024,20 +1004,18 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     L.p.group_nodes = plan.group_nodes;
     L.stream = static_cast<cudaStream_t>(stream);
     L.grid = ctas;
-    pa_tree_prepass<<<1, 1024, 0, L.stream>>>(context_lens, q_start, shape->num_seqs, plan.groups, plan.group_nodes,
-                                              max_nodes, total_q, shape->max_blocks_per_seq, shape->block_size,
-                                              const_cast<long long*>(d.cum));
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     if (plan.k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
     if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
         const int g = shape->num_q_heads / shape->num_kv_heads;
         cudaLaunchAttribute attr[1];
-        const cudaLaunchConfig_t cfg = pdl_config(ctas - 1, MERGE_THREADS, 0, L.stream, attr);
+        cudaLaunchConfig_t cfg = pdl_config(ctas - 1, TREE_MERGE_THREADS, 0, L.stream, attr);
+        const int rows = std::min(plan.k->rows, max_nodes * g), per = TREE_MERGE_THREADS / (shape->head_dim / 4);
+        cfg.gridDim.y = (rows + per - 1) / per;
         const float* parts = d.partials;
-        const auto merge = shape->head_dim == 128 ? pa_multi_merge<128, true> : pa_multi_merge<64, true>;
-        if (cudaLaunchKernelEx(&cfg, merge, d.cum, q_start, context_lens, parts, d.out, d.N * plan.groups, d.Hkv, g,
-                               plan.k->rows, ctas, (int)max_nodes, (int)total_q, (int)(shape->dtype == PA_BF16),
-                               plan.groups, plan.group_nodes) != cudaSuccess)
+        const TreeStart* starts = L.p.starts;
+        const auto merge = shape->head_dim == 128 ? pa_tree_merge<128> : pa_tree_merge<64>;
+        if (cudaLaunchKernelEx(&cfg, merge, q_start, starts, parts, d.out, d.N, d.Hkv, g, plan.k->rows, ctas,
+                               plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes) != cudaSuccess)
             return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

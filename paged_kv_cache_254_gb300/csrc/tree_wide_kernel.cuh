@@ -64,7 +64,8 @@ struct WideTraits {
     static constexpr int NBAR = 3 * R_CAP + 2 * 4 + 2 + 2 + NREC;
     static constexpr int REC_OFF = (8 * NBAR + 15) / 16 * 16;
     static constexpr int MISC_OFF = REC_OFF + NREC * 48;
-    static constexpr int Q_OFF = (MISC_OFF + 16 + 1023) / 1024 * 1024;
+    static constexpr int START_OFF = MISC_OFF + 16;          // a TreeStart, a word per warp
+    static constexpr int Q_OFF = (START_OFF + 32 + 8 * 12 + 1023) / 1024 * 1024;
     static constexpr int OUT_OFF = Q_OFF + Q_BYTES;          // per softmax warp: 32 rows of 128 bytes on their way out
     static constexpr int OUT_BYTES = 32 * 128;
     static constexpr int RING_OFF = OUT_OFF + 8 * OUT_BYTES;
@@ -180,7 +181,20 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
             p.out[i] = qnan16<Tr::BF16>();
     }
 
-    const Sched sc = make_sched(__ldg(p.cum + p.N) * p.Hkv, gridDim.x, 0);
+    TreeTab tab;
+    tab.ctx = p.context_lens;
+    tab.qst = qst;
+    tab.N = seqs;
+    tab.groups = mp.groups;
+    tab.group_nodes = mp.group_nodes;
+    tab.max_nodes = mp.max_q;
+    tab.total_q = mp.total_q;
+    tab.MB = p.MB;
+    tab.BS = BS;
+    const TreeStart& at = *reinterpret_cast<TreeStart*>(smem + Tr::START_OFF);
+    tree_start<Tr::THREADS>(tab, p.Hkv, SB, reinterpret_cast<long long*>(smem + Tr::START_OFF + 32),
+                            reinterpret_cast<TreeStart*>(smem + Tr::START_OFF));
+    const Sched sc = tree_sched(at.W, gridDim.x, SB);
     const bool has_work = (int)blockIdx.x < sc.NS;
     const long long lo = has_work ? sc.lo(blockIdx.x) : 0, hi = has_work ? sc.lo(blockIdx.x + 1) : 0;
 
@@ -191,10 +205,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
             // with one group the keys are read once per call; with more, another CTA
             // reads the same keys for the next group at about this time
             const uint64_t kv_pol = mp.groups == 1 ? l2_evict_first() : l2_evict_normal();
-            SeqTab tab;
-            tab.cum = p.cum;
-            tab.ctx = p.context_lens;
-            tab.first = nullptr;
+            if (lane == 0) mp.starts[blockIdx.x] = at;
             int item = 0, st = 0, j = 0, nseg = 0;   // ring item (two a stage), its slot and phase; stage
             uint32_t ph = 0;
             bool ok = true;
@@ -209,7 +220,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                 }
             };
             if (has_work) {
-                SegIter it = locate(p, tab, lo, lane);
+                SegIter it{lo, at.s, at.kvh, at.b0, at.nb, 0};
                 while (ok && it.gi < hi) {
                     const int len = seg_len(it, hi);
                     const int s = it.s % seqs, skip = it.s / seqs * mp.group_nodes;
