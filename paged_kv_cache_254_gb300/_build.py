@@ -1,19 +1,24 @@
-"""Build libpa.so in-tree with nvcc for sm_103a.
+"""Build libpa.so in-tree with nvcc for sm_103a, and the compiled host calls beside it.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into
 ``lib/libpa.so`` with the CUDA runtime linked statically.  A rebuild happens
 only when a source or header is newer than the library.  ptxas resource
 reports (registers, spills, shared memory) are kept next to the objects.
+``csrc/fast_calls.cpp`` becomes ``lib/_pa_fast.so``, a Python module against the
+installed torch's headers that calls into libpa.so.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -21,6 +26,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIBPATH = os.path.join(LIBDIR, "libpa.so")
+FASTSRC = os.path.join(CSRC, "fast_calls.cpp")
+FASTPATH = os.path.join(LIBDIR, "_pa_fast.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = ["-std=c++17", "-O3", ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -43,21 +50,25 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [
-        os.path.abspath(__file__)]
+        FASTSRC, os.path.abspath(__file__)]
 
 
 STAMP = os.path.join(LIBDIR, "host-arch.txt")
 
 
+def _stamp() -> str:
+    return f"{platform.machine()} torch {importlib.metadata.version('torch')}"
+
+
 def up_to_date() -> bool:
-    """The library exists, was built on this machine's architecture, and is
-    newer than every source."""
-    if not os.path.exists(LIBPATH) or not os.path.exists(STAMP):
+    """The libraries exist, were built on this machine's architecture with the
+    installed torch, and are newer than every source."""
+    if not all(os.path.exists(p) for p in (LIBPATH, FASTPATH, STAMP)):
         return False
     with open(STAMP) as f:
-        if f.read().strip() != platform.machine():
+        if f.read().strip() != _stamp():
             return False
-    t = os.path.getmtime(LIBPATH)
+    t = min(os.path.getmtime(LIBPATH), os.path.getmtime(FASTPATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -72,23 +83,50 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_fast() -> str:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(OBJDIR, "fast_calls.o")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-I{torch_dir}/include",
+           f"-I{torch_dir}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}/include",
+           "-c", FASTSRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {FASTSRC}:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_fast(obj: str) -> None:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = FASTPATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-lpa", f"-L{torch_dir}/lib", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, FASTPATH)
+
+
 def build(force: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libpa.so; returns its path."""
+    """Compile and link libpa.so and _pa_fast.so; returns the former's path."""
     if not force and up_to_date():
         return LIBPATH
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
     jobs = jobs or min(len(srcs), max(1, os.cpu_count() or 1))
-    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs + 1) as ex:
+        fast = ex.submit(_compile_fast)
         objs = list(ex.map(_compile, srcs))
+        fast_obj = fast.result()
     tmp = LIBPATH + ".tmp"
     cmd = [nvcc(), ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIBPATH)
+    _link_fast(fast_obj)
     with open(STAMP, "w") as f:
-        f.write(platform.machine() + "\n")
+        f.write(_stamp() + "\n")
     return LIBPATH
 
 

@@ -9,6 +9,8 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -144,6 +146,27 @@ def load() -> ctypes.CDLL:
         lib.pa_rope_append_kv.restype = I32
         _lib = lib
         return lib
+
+
+_fast = None
+
+
+def load_fast():
+    """The compiled host calls (``csrc/fast_calls.cpp``), built with libpa.so."""
+    global _fast
+    if _fast is None:
+        load()
+        with _lock:
+            if _fast is None:
+                path = _build.FASTPATH
+                if not os.path.exists(path):
+                    raise RuntimeError(f"{path} is not built; run paged_kv_cache_254_gb300._build.build()")
+                loader = importlib.machinery.ExtensionFileLoader("_pa_fast", path)
+                spec = importlib.util.spec_from_loader("_pa_fast", loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                _fast = module
+    return _fast
 
 
 def status_string(status: int) -> str:

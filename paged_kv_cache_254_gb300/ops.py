@@ -8,7 +8,6 @@ calls the matching ``pa_*`` function of libpa.so on the current stream.
 from __future__ import annotations
 
 import ctypes
-import functools
 import threading
 
 import torch
@@ -262,9 +261,10 @@ def pa_decode_multi(q, k_pool, v_pool, block_tables, context_lens, q_start, scal
 
 
 # --------------------------------------------------------------------------- drafted trees, rotary positions
-# These calls run beside kernels of a few microseconds, so their host side is
-# kept short: one check per argument, the raw stream handle, no context manager
-# unless another device is current.
+# These calls run beside kernels of a few microseconds, so calls in order go
+# through a compiled twin of their host side (csrc/fast_calls.cpp), which
+# declines whatever is not plainly right; the checks below then say what is
+# wrong, or do what is rare (a first workspace, another device, a capture).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -297,26 +297,31 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_stream(fn):
-    """Give ``fn`` a ``stream`` argument: the call runs with that stream
-    current, so what it allocates belongs to the stream, and its arguments'
-    memory is not reused before the stream has passed the call."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            result = fn(*args, **kwargs)
-        for t in (*args, *kwargs.values()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
-        return result
-    return call
+def _on_stream(stream, fn, *args):
+    """fn(*args) with ``stream`` current, so that what it allocates belongs to
+    the stream, and its arguments' memory is not reused before the stream has
+    passed the call."""
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return result
 
 
-def _largest_chunk(q_start, n):
-    qs = q_start.cpu()
-    return max(1, int((qs[1:] - qs[:-1]).max().item())) if n > 0 else 1
+def _largest_chunk(q_start) -> int:
+    """The longest chunk, read on the host (q_start may yet be of any shape)."""
+    sizes = q_start.detach().flatten().cpu().diff()
+    return max(1, int(sizes.max().item())) if sizes.numel() else 1
+
+
+_fast = None
+
+
+def _load_fast():
+    global _fast
+    _fast = _lib.load_fast()
+    return _fast
 
 
 _tree_bytes = {}
@@ -337,15 +342,27 @@ def _tree_workspace(dev, shape, max_nodes):
     return _kept_workspace(dev, _raw_stream(dev), need)
 
 
-@_on_stream
 def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_masks, scale, max_nodes=None,
-                   out=None, workspace=None, err=None):
+                   out=None, workspace=None, err=None, stream=None):
     """Attention of drafted trees over the cache (see include/pa.h): q
     [T, Hq, d] holds each sequence's nodes at rows q_start[b] .. q_start[b + 1]
     - 1 (q_start: int32 [N + 1]); bit j of tree_masks [T] (int64, see
     ``tree_masks()``) lets a row see node j of its own tree, next to every key
     cached before the tree.  max_nodes (1..64) defaults to the largest tree
     (read from q_start on the host)."""
+    if stream is not None:
+        return _on_stream(stream, pa_decode_tree, q, k_pool, v_pool, block_tables, context_lens, q_start,
+                          tree_masks, scale, max_nodes, out, workspace, err)
+    if max_nodes is None and isinstance(q_start, torch.Tensor):
+        max_nodes = _largest_chunk(q_start)
+    args = (q, k_pool, v_pool, block_tables, context_lens, q_start, tree_masks, scale, max_nodes, out, workspace, err)
+    done = (_fast or _load_fast()).decode_tree(_sp_cache, *args)
+    return _decode_tree(*args) if done is NotImplemented else done
+
+
+def _decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_masks, scale, max_nodes, out,
+                 workspace, err):
+    """pa_decode_tree by way of every check."""
     dev = _index("q", q)
     dt = q.dtype
     if dt not in _DTYPES:
@@ -366,8 +383,6 @@ def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_
         raise ValueError("q_start must have N + 1 entries, context_lens N and tree_masks T")
     if pool != v_pool.shape or pool[3] != d:
         raise ValueError("shape mismatch between q and the pools")
-    if max_nodes is None:
-        max_nodes = _largest_chunk(q_start, N)
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -390,12 +405,23 @@ def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_
     return out
 
 
-@_on_stream
 def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_lens, max_nodes=None, path=None,
-                   err=None):
+                   err=None, stream=None):
     """The drafted path that the target model's tokens agree with (see
     include/pa.h).  Returns (path int32 [N, max_nodes], num_accepted int32 [N],
     next_tokens int64 [N], new_context_lens int32 [N])."""
+    if stream is not None:
+        return _on_stream(stream, pa_tree_verify, tree_masks, draft_tokens, target_tokens, q_start, context_lens,
+                          max_nodes, path, err)
+    if max_nodes is None and isinstance(q_start, torch.Tensor):
+        max_nodes = _largest_chunk(q_start)
+    args = (tree_masks, draft_tokens, target_tokens, q_start, context_lens, max_nodes, path, err)
+    done = (_fast or _load_fast()).tree_verify(*args)
+    return _tree_verify(*args) if done is NotImplemented else done
+
+
+def _tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_lens, max_nodes, path, err):
+    """pa_tree_verify by way of every check."""
     dev = _index("tree_masks", tree_masks)
     _arg("tree_masks", tree_masks, torch.int64, dev)
     _arg("draft_tokens", draft_tokens, torch.int64, dev)
@@ -407,8 +433,6 @@ def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_len
     T, N = tree_masks.shape[0], context_lens.shape[0]
     if draft_tokens.shape != (T,) or target_tokens.shape != (T,) or q_start.shape != (N + 1,):
         raise ValueError("draft_tokens and target_tokens must have tree_masks' shape, q_start N + 1 entries")
-    if max_nodes is None:
-        max_nodes = _largest_chunk(q_start, N)
     if path is None:
         path = torch.empty((N, max(0, max_nodes)), dtype=torch.int32, device=context_lens.device)
     else:
@@ -427,11 +451,19 @@ def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_len
     return path, accepted, following, lens
 
 
-@_on_stream
-def pa_keep_kv(path, q_start, context_lens, block_tables, k_pool, v_pool, err=None):
+def pa_keep_kv(path, q_start, context_lens, block_tables, k_pool, v_pool, err=None, stream=None):
     """Move the accepted tokens' K and V rows to consecutive positions behind
     each sequence's context (see include/pa.h); path int32 [N, max_nodes] and
     the context lengths are those of the tree."""
+    if stream is not None:
+        return _on_stream(stream, pa_keep_kv, path, q_start, context_lens, block_tables, k_pool, v_pool, err)
+    args = (path, q_start, context_lens, block_tables, k_pool, v_pool, err)
+    if (_fast or _load_fast()).keep_kv(*args) is NotImplemented:
+        _keep_kv(*args)
+
+
+def _keep_kv(path, q_start, context_lens, block_tables, k_pool, v_pool, err):
+    """pa_keep_kv by way of every check."""
     dev = _index("k_pool", k_pool)
     dt = k_pool.dtype
     if dt not in _DTYPES:
@@ -479,14 +511,25 @@ def _token_rows(name, t, dtype, shape, device):
     return st
 
 
-@_on_stream
 def pa_rope_append_kv(q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, inv_freq, interleaved=False,
-                      rope_scale=1.0, q_weight=None, k_weight=None, eps=1e-6, out=None, err=None):
+                      rope_scale=1.0, q_weight=None, k_weight=None, eps=1e-6, out=None, err=None, stream=None):
     """Norm (with q_weight / k_weight) and rotate queries and keys, write keys
     and values into the pools at slot_mapping, and return the queries
     [T, Hq, d] (see include/pa.h).  q, k_new, v_new [T, heads, d] may be views
     of one projection's output; inv_freq [rotary_dim / 2] fp32 as from
     ``rope_inv_freq()``, or None for no rotation; out may be q."""
+    if stream is not None:
+        return _on_stream(stream, pa_rope_append_kv, q, k_new, v_new, positions, slot_mapping, k_pool, v_pool,
+                          inv_freq, interleaved, rope_scale, q_weight, k_weight, eps, out, err)
+    args = (q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, inv_freq, interleaved, rope_scale, q_weight,
+            k_weight, eps, out, err)
+    done = (_fast or _load_fast()).rope_append_kv(*args)
+    return _rope_append_kv(*args) if done is NotImplemented else done
+
+
+def _rope_append_kv(q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, inv_freq, interleaved, rope_scale,
+                    q_weight, k_weight, eps, out, err):
+    """pa_rope_append_kv by way of every check."""
     dev = _index("k_pool", k_pool)
     dt = k_pool.dtype
     if dt not in _DTYPES:
