@@ -226,11 +226,13 @@ struct TreeTab {
     __device__ __forceinline__ int fst(int) const { return 0; }
 };
 
-// Where a CTA's chunk of the list begins, and the list's length in (KV head,
-// block) units; nb is 0 for a CTA without a chunk.
+// Where a CTA's chunk of the list begins, the list's length in (KV head, block)
+// units, and whether the chunk's beginning cuts a pair as the first boundary to do
+// so; nb and cuts are 0 for a CTA without a chunk.
 struct alignas(16) TreeStart {
     int s, kvh, b0, nb;
-    long long W, pad;
+    long long W;
+    int cuts, pad;
 };
 
 // W blocks in equal chunks, each of min_blocks at least while there are that many.
@@ -263,7 +265,7 @@ __device__ __forceinline__ void tree_start(const TreeTab& tab, int Hkv, int min_
         if (lane >= o) incl += t;
     }
     if (lane == 31) wsum[warp] = incl;
-    if (threadIdx.x == 0) box->nb = 0;
+    if (threadIdx.x == 0) box->nb = box->cuts = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
 #pragma unroll
@@ -287,6 +289,7 @@ __device__ __forceinline__ void tree_start(const TreeTab& tab, int Hkv, int min_
                     box->kvh = (int)(off / nb);
                     box->b0 = (int)(off % nb);
                     box->nb = nb;
+                    box->cuts = box->b0 > 0 && sc.lo(blockIdx.x - 1) <= lo - box->b0;
                     break;
                 }
                 c += nb;
@@ -785,49 +788,82 @@ pa_multi_merge(const long long* __restrict__ cum, const int32_t* __restrict__ q_
 
 // The post-pass of trees: as pa_multi_merge, for pairs that few sequences cut into
 // many pieces and for groups of up to 256 rows.
-// blockIdx.x: a chunk boundary, blockIdx.y: a row for each D / 4 lanes of the pair
-// that it is the first to cut; where a chunk begins the attention kernel has
-// written down.  A row's lanes load the (m, l) of a piece each, so that one round
-// of loads weighs D / 4 pieces, then 4 dims of every piece, eight pieces in flight.
-// Bound by three rounds of loads, one after the other.
+// blockIdx.x: a chunk boundary, blockIdx.y: some rows of the pair that it is the
+// first to cut; where a chunk begins the attention kernel has written down.  With
+// few pairs (FEW) the grid counts the cut pairs instead, and each block
+// finds its own among the boundaries (blocks without work are not free: 38,000 of
+// them took 50 us).  D / 4
+// lanes hold a row: each loads the (m, l) of a piece, so that one round of loads
+// weighs D / 4 pieces, and then 4 dims of the pieces; `splits` such groups of lanes
+// share a row's pieces and add up in shared memory.  The library splits as far as
+// the launch's pairs are expected to be cut.  Bound by three rounds of loads, one
+// after the other; 16 rows of 62 pieces took 15 us unsplit.
 constexpr int TREE_MERGE_THREADS = 256;
-constexpr int AHEAD = 4;
+constexpr int TREE_MERGE_SPLITS = 8;              // at most
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(TREE_MERGE_THREADS)
 pa_tree_merge(const int32_t* __restrict__ q_start, const TreeStart* __restrict__ starts,
               const float* __restrict__ partials, uint16_t* __restrict__ out, int seqs, int Hkv, int G,
-              int rows_per_chunk, int ctas, int min_blocks, int bf16, int group_nodes) {
+              int rows_per_chunk, int ctas, int min_blocks, int bf16, int group_nodes, int splits_few) {
+    const int splits = FEW ? splits_few : 1;
     constexpr int PSTRIDE = D + 4;
-    constexpr int LPR = D / 4;                    // lanes per row
-    constexpr int ROWS = TREE_MERGE_THREADS / LPR;
-    const int sub = threadIdx.x % LPR;
+    constexpr int LPR = D / 4;                    // lanes of a group
+    constexpr int AHEAD = 4;                      // pieces loaded beside the weights
+    __shared__ float4 part[FEW ? TREE_MERGE_THREADS : 1];
+    const int sub = threadIdx.x % LPR, group = threadIdx.x / LPR, sp = group % splits;
     griddep_wait();   // the attention grid is complete and its writes visible
-    const int c = (int)blockIdx.x + 1;            // boundary between chunks c - 1 and c
+    int c = (int)blockIdx.x + 1;
+    if constexpr (FEW) {                          // the blockIdx.x-th cut pair
+        __shared__ int counts[TREE_MERGE_THREADS / 32], found;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int per = (ctas - 1 + TREE_MERGE_THREADS - 1) / TREE_MERGE_THREADS, first = 1 + (int)threadIdx.x * per;
+        unsigned set = 0;                         // this thread's boundaries that cut a pair (ctas <= 32 * 256)
+        for (int i = 0; i < per; ++i)
+            if (first + i < ctas && starts[first + i].cuts) set |= 1u << i;
+        const int n = __popc(set);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) counts[warp] = incl;
+        if (threadIdx.x == 0) found = 0;
+        __syncthreads();
+        int nth = (int)blockIdx.x - (incl - n);   // of this thread's own
+        for (int w = 0; w < warp; ++w) nth -= counts[w];
+        if (nth >= 0 && nth < n) {
+            while (nth-- > 0) set &= set - 1;
+            found = first + __ffs((int)set) - 1;
+        }
+        __syncthreads();
+        c = found;
+        if (c == 0) return;
+    } else if (!starts[c].cuts) {
+        return;
+    }
     const TreeStart at = starts[c];
-    if (at.nb == 0 || at.b0 == 0) return;         // no such chunk, or its first pair is not cut here
     const Sched sc = tree_sched(at.W, ctas, min_blocks);
     const long long P0 = sc.lo(c) - at.b0;
-    if (sc.lo(c - 1) > P0) return;                // cut first by an earlier boundary
-    const int kvh = at.kvh, nb = at.nb, s = at.s % seqs, skip = at.s / seqs * group_nodes;
+    const int s = at.s % seqs, skip = at.s / seqs * group_nodes;
     const int q0 = q_start[s] + skip;
     const int rows = min(group_nodes, q_start[s + 1] - q0) * G;   // a sequence with blocks is well formed
+    const int row0 = (int)blockIdx.y * (TREE_MERGE_THREADS / LPR / splits);
+    if (row0 >= rows) return;
+    const int mine = row0 + group / splits;
+    const bool writer = mine < rows && sp == 0;
+    const int row = mine < rows ? mine : row0;    // (the others stay for the exchanges)
     const long long cfirst = sc.of(P0);
-    const int np = (int)(sc.of(P0 + nb - 1) - cfirst) + 1;
+    const int np = (int)(sc.of(P0 + at.nb - 1) - cfirst) + 1;
     const size_t cstride = (size_t)2 * rows_per_chunk * PSTRIDE;
     const size_t first_off = sc.lo(cfirst) < P0 ? (size_t)rows_per_chunk * PSTRIDE : 0;
-    const float* base = partials + (size_t)cfirst * cstride;
-    const int r = (int)blockIdx.y * ROWS + (int)threadIdx.x / LPR;
-    if ((int)blockIdx.y * ROWS >= rows) return;
-    const bool writer = r < rows;                 // (the others stay for the exchanges)
-    const int row = writer ? r : 0;
-    auto piece = [&](int i) -> const float* {
-        return base + (size_t)row * PSTRIDE + (i == 0 ? first_off : (size_t)i * cstride);
-    };
-    float4 ahead[AHEAD];                          // the first pieces' dims, beside their (m, l)
+    const float* base = partials + (size_t)cfirst * cstride + (size_t)row * PSTRIDE;
+    auto piece = [&](int i) -> const float* { return base + (i == 0 ? first_off : (size_t)i * cstride); };
+    float4 ahead[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (i < np) ahead[i] = *reinterpret_cast<const float4*>(piece(i) + 4 * sub);
+    for (int k = 0; k < AHEAD; ++k)
+        if (sp + k * splits < np) ahead[k] = *reinterpret_cast<const float4*>(piece(sp + k * splits) + 4 * sub);
     float M = -INFINITY, m_mine = -INFINITY, l_mine = 0.f;
     for (int i = sub; i < np; i += LPR) {
         const float* p = piece(i);
@@ -840,9 +876,15 @@ pa_tree_merge(const int32_t* __restrict__ q_start, const TreeStart* __restrict__
     const float ref = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < np; i0 += LPR) {
+    auto add = [&](const float4& v, float f) {
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+    };
+    for (int i0 = 0; i0 < np; i0 += LPR) {        // LPR is a multiple of splits
         const int n = min(LPR, np - i0);
-        if (np > LPR) {                       // several rounds: this one's piece again
+        if (np > LPR) {                           // several rounds: this one's piece again
             m_mine = -INFINITY;
             l_mine = 0.f;
             if (sub < n) {
@@ -852,31 +894,32 @@ pa_tree_merge(const int32_t* __restrict__ q_start, const TreeStart* __restrict__
             }
         }
         const float f_mine = ex2(m_mine - ref);
-        L += f_mine * l_mine;                 // (lanes without a piece: 0 * 0)
-        int i = 0;
+        L += f_mine * l_mine;                     // (lanes without a piece: 0 * 0)
+        int k = 0;                                // piece i0 + sp + k * splits
         if (i0 == 0) {
 #pragma unroll
-            for (; i < AHEAD; ++i) {
-                const float f = __shfl_sync(0xffffffffu, f_mine, i, LPR);
-                if (i >= np) continue;
-                acc.x += ahead[i].x * f;
-                acc.y += ahead[i].y * f;
-                acc.z += ahead[i].z * f;
-                acc.w += ahead[i].w * f;
+            for (; k < AHEAD; ++k) {
+                const int i = sp + k * splits;
+                const float f = __shfl_sync(0xffffffffu, f_mine, i % LPR, LPR);
+                if (i < n) add(ahead[k], f);
             }
         }
+        const int most = (n + splits - 1) / splits;   // the same for every group
 #pragma unroll 8
-        for (; i < n; ++i) {
-            const float f = __shfl_sync(0xffffffffu, f_mine, i, LPR);
-            const float4 v = *reinterpret_cast<const float4*>(piece(i0 + i) + 4 * sub);
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
+        for (; k < most; ++k) {
+            const int i = sp + k * splits;
+            const float f = __shfl_sync(0xffffffffu, f_mine, i % LPR, LPR);
+            if (i < n) add(*reinterpret_cast<const float4*>(piece(i0 + i) + 4 * sub), f);
         }
     }
 #pragma unroll
     for (int o = 1; o < LPR; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if constexpr (FEW) {
+        part[threadIdx.x] = acc;
+        __syncthreads();
+        if (sp == 0)
+            for (int k = 1; k < splits; ++k) add(part[threadIdx.x + k * LPR], 1.f);
+    }
     if (!writer) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;   // a node that sees no key: zero
     const float xv[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
@@ -884,7 +927,7 @@ pa_tree_merge(const int32_t* __restrict__ q_start, const TreeStart* __restrict__
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         w[k] = bf16 ? pack2<true>(xv[2 * k], xv[2 * k + 1]) : pack2<false>(xv[2 * k], xv[2 * k + 1]);
-    uint16_t* dst = out + ((size_t)(q0 + row / G) * Hkv * G + (size_t)kvh * G + row % G) * D + 4 * sub;
+    uint16_t* dst = out + ((size_t)(q0 + row / G) * Hkv * G + (size_t)at.kvh * G + row % G) * D + 4 * sub;
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 

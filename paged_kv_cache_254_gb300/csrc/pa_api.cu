@@ -1008,14 +1008,26 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
         const int g = shape->num_q_heads / shape->num_kv_heads;
         cudaLaunchAttribute attr[1];
-        cudaLaunchConfig_t cfg = pdl_config(ctas - 1, TREE_MERGE_THREADS, 0, L.stream, attr);
-        const int rows = std::min(plan.k->rows, max_nodes * g), per = TREE_MERGE_THREADS / (shape->head_dim / 4);
+        cudaLaunchConfig_t cfg = pdl_config(1, TREE_MERGE_THREADS, 0, L.stream, attr);
+        // A pair is cut into at most about this many pieces.  Many of them are worth a
+        // search for the few pairs and several groups of lanes a row (one sequence of
+        // 4000 tokens, 62 pieces: 27 -> 19 us for the call), up to 16 are not (8
+        // sequences, 16 pieces: 29 against 31 us).
+        const long long pairs = (long long)shape->num_seqs * shape->num_kv_heads * plan.groups;
+        const long long pieces = std::min(ctas / pairs, (long long)shape->max_blocks_per_seq / plan.min_blocks + 1);
+        const bool few = pieces > 16 && ctas <= 32 * TREE_MERGE_THREADS;
+        int splits = 1;
+        while (few && splits < TREE_MERGE_SPLITS && 4 * splits <= pieces) splits *= 2;
+        cfg.gridDim.x = (unsigned)(few ? pairs : ctas - 1);
+        const int rows = std::min(plan.k->rows, max_nodes * g);
+        const int per = TREE_MERGE_THREADS / (shape->head_dim / 4) / splits;   // rows of a block
         cfg.gridDim.y = (rows + per - 1) / per;
         const float* parts = d.partials;
         const TreeStart* starts = L.p.starts;
-        const auto merge = shape->head_dim == 128 ? pa_tree_merge<128> : pa_tree_merge<64>;
+        const auto merge = shape->head_dim == 128 ? (few ? pa_tree_merge<128, true> : pa_tree_merge<128, false>)
+                                                  : (few ? pa_tree_merge<64, true> : pa_tree_merge<64, false>);
         if (cudaLaunchKernelEx(&cfg, merge, q_start, starts, parts, d.out, d.N, d.Hkv, g, plan.k->rows, ctas,
-                               plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes) != cudaSuccess)
+                               plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes, splits) != cudaSuccess)
             return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
