@@ -160,8 +160,7 @@ struct SegIter {
     int s, kvh, b0, nb, first;
 };
 
-template <class Tab>
-__device__ __forceinline__ void seg_advance(SegIter& it, int len, const DecodeParams& p, const Tab& tab) {
+__device__ __forceinline__ void seg_advance(SegIter& it, int len, const DecodeParams& p, const SeqTab& tab) {
     it.gi += len;
     it.b0 += len;
     if (it.b0 == it.nb) {

@@ -37,6 +37,7 @@
 #pragma once
 
 #include "decode_kernel.cuh"
+#include "packed.cuh"
 
 namespace pa {
 
@@ -223,8 +224,20 @@ struct TreeTab {
         const bool ok = a >= 0 && b <= total_q && n <= max_nodes && n <= c && c > 0 && c <= MB * BS;
         return ok && n > g * group_nodes ? (c + BS - 1) / BS : 0;
     }
-    __device__ __forceinline__ int fst(int) const { return 0; }
 };
+
+// The next segment, as for the other work lists.
+__device__ __forceinline__ void seg_advance(SegIter& it, int len, const DecodeParams& p, const TreeTab& tab) {
+    it.gi += len;
+    it.b0 += len;
+    if (it.b0 < it.nb) return;
+    it.b0 = 0;
+    if (++it.kvh < p.Hkv) return;
+    it.kvh = 0;
+    it.nb = 0;
+    for (const int n = tab.N * tab.groups; ++it.s < n;)
+        if ((it.nb = tab.nb(it.s)) > 0) break;
+}
 
 // Where a CTA's chunk of the list begins, the list's length in (KV head, block)
 // units, and whether the chunk's beginning cuts a pair as the first boundary to do

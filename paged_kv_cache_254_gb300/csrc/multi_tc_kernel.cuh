@@ -278,7 +278,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const bool has_work = (int)blockIdx.x < sc.NS;
     const long long lo = has_work ? sc.lo(blockIdx.x) : 0, hi = has_work ? sc.lo(blockIdx.x + 1) : 0;
 
-    // Trees: 256 x 208 + 128 x 80 registers, within the 384 x 168 of the launch.
+    // Trees: 256 x 200 + 128 x 104 registers, the 384 x 168 of the launch.
     if (warp >= SW) {
         if constexpr (Tr::TREE) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == Tr::COPY_WARP) {

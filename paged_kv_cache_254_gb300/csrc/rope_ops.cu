@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include "decode_common.cuh"
+#include "packed.cuh"
 #include "ptx.cuh"
 #include "../../include/pa.h"
 

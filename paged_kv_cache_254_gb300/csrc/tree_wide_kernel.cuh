@@ -102,9 +102,8 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     constexpr int D = Tr::D, BS = Tr::BS, SB = Tr::SB, HALVES = Tr::HALVES, KEYS = Tr::KEYS, R = Tr::R;
     constexpr uint32_t IDESC_S = idesc_f16<Tr::BF16>(128, KEYS, false, false);
     constexpr uint32_t IDESC_O = idesc_f16<Tr::BF16>(128, D, false, true);
-    DecodeParams p = mp.d;
+    const DecodeParams& p = mp.d;
     const int seqs = p.N;
-    p.N = seqs * mp.groups;                                   // sequences of the work list
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
