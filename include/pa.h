@@ -220,13 +220,16 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
  * untouched; a row that sees a V of a node with an infinity or NaN is NaN.
  *
  *   max_nodes     largest n_b of the call, 1..64
- *   total_q       T: rows of q, out and tree_masks (q_start[N] should equal it)
+ *   total_q       T: rows of q, out and tree_masks (q_start[N] should equal it; rows
+ *                 of out outside every tree are left as they are)
  *   tree_masks    device uint64 [T]
+ *   out           must not overlap q
  *   others        as pa_decode_multi; workspace: pa_decode_tree_workspace_bytes
  *
  * Malformed sizes set PA_DEVERR_CONTEXT and NaN rows as in pa_decode_multi.
  * Supported shapes as pa_decode (16-bit).  Results are deterministic and
- * independent of block placement.  Three launches on `stream`.
+ * independent of block placement.  Two launches on `stream`: attention,
+ * then the merge of split rows.
  */
 size_t pa_decode_tree_workspace_bytes(const pa_shape* shape, int32_t max_nodes);
 
@@ -390,7 +393,7 @@ pa_status pa_append_kv(const pa_shape* shape, int32_t num_tokens, const void* k_
  *                    of 8): the parts of one projection's output need no copy
  *   positions        int32 [num_tokens], any sign
  *   q_out            [num_tokens][Hq][d]; may be q itself when q is contiguous, must
- *                    not overlap it otherwise
+ *                    not overlap it, k_new or v_new otherwise
  *   rope->inv_freq   fp32 [rotary_dim / 2] radians per position (device); long-context
  *                    scalings are frequencies and a scale
  *   rope->q_weight, k_weight  16-bit [d] (device) or NULL

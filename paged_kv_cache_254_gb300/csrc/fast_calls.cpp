@@ -23,7 +23,10 @@
 
 namespace {
 
-PyObject* declined() { Py_RETURN_NOTIMPLEMENTED; }
+PyObject* declined() {
+    PyErr_Clear();                       // an int too large for a long
+    Py_RETURN_NOTIMPLEMENTED;
+}
 
 // The tensor behind `o` if it is contiguous, of type `t` and on device `dev`; else null.
 const at::Tensor* tensor(PyObject* o, at::ScalarType t, int dev) {
@@ -85,7 +88,6 @@ PyObject* guarded(F f) {
     try {
         return f();
     } catch (const std::exception&) {
-        PyErr_Clear();
         return declined();
     }
 }
@@ -128,7 +130,7 @@ PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
             !optional(a[7], at::kInt, dev, err))
             return declined();
         const long P = PyLong_AsLong(a[5]);
-        if (P < 1 || P > 64 || masks->dim() != 1 || ctx->dim() != 1) return declined();   // (an overflow is -1)
+        if (P < 1 || P > 64 || masks->dim() != 1 || ctx->dim() != 1) return declined();
         const int64_t T = masks->size(0), N = ctx->size(0);
         if (!fits_int(T) || !fits_int(N) || !is_shape(*draft, {T}) || !is_shape(*target, {T}) ||
             !is_shape(*start, {N + 1}) || (given && !is_shape(*given, {N, (int64_t)P})))
@@ -149,6 +151,11 @@ PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
         PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(accepted));
         PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(next));
         PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(lens));
+        for (int i = 0; i < 4; ++i)
+            if (!PyTuple_GET_ITEM(r, i)) {
+                Py_DECREF(r);
+                return (PyObject*)nullptr;
+            }
         return r;
     });
 }

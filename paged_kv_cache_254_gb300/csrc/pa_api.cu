@@ -56,6 +56,12 @@ int log2_exact(int g) {
     }
 }
 
+// Do two ranges of bytes overlap?
+bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int elem_bytes(int dtype) {
@@ -957,6 +963,8 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_start, 4) || !aligned(tree_masks, 8))
         return PA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    const uint64_t row_bytes = (uint64_t)shape->num_q_heads * shape->head_dim * 2;
+    if (total_q > 0 && overlap(q, total_q * row_bytes, out, total_q * row_bytes)) return PA_ERR_INVALID_ARG;
     if (shape->num_seqs == 0) return PA_OK;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
@@ -1072,7 +1080,8 @@ pa_status pa_keep_kv(const pa_shape* shape, int32_t max_nodes, const int32_t* pa
         return PA_ERR_INVALID_ARG;
     if (max_nodes < 1 || max_nodes > 64) return PA_ERR_INVALID_ARG;
     if (shape->num_seqs == 0) return PA_OK;
-    if (!path || !q_start || !block_tables || !context_lens || !k_pool || !v_pool) return PA_ERR_INVALID_ARG;
+    if (!path || !q_start || !block_tables || !context_lens || !k_pool || !v_pool || k_pool == v_pool)
+        return PA_ERR_INVALID_ARG;
     if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(path, 4) || !aligned(q_start, 4) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PA_ERR_INVALID_ARG;
@@ -1123,11 +1132,14 @@ pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t 
     const int64_t q_row = (int64_t)shape->num_q_heads * D, kv_row = (int64_t)shape->num_kv_heads * D;
     if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 || k_stride % 8 || v_stride % 8)
         return PA_ERR_INVALID_ARG;
-    // q_out may be q itself (a row is read before it is written), not a shifted part of it
-    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(q_out);
-    const uintptr_t q1 = q0 + 2 * (uintptr_t)((num_tokens - 1) * q_stride + q_row),
-                    o1 = o0 + 2 * (uintptr_t)(num_tokens * q_row);
-    if (q0 < o1 && o0 < q1 && !(q0 == o0 && q_stride == q_row)) return PA_ERR_INVALID_ARG;
+    // q_out may be q itself (a row is read before it is written), not a shifted part of
+    // it, nor lie over the keys and values
+    const int64_t last = num_tokens - 1, out_bytes = 2 * num_tokens * q_row;
+    if (overlap(q_out, out_bytes, q, 2 * (last * q_stride + q_row)) && !(q == q_out && q_stride == q_row))
+        return PA_ERR_INVALID_ARG;
+    if (overlap(q_out, out_bytes, k_new, 2 * (last * k_stride + kv_row)) ||
+        overlap(q_out, out_bytes, v_new, 2 * (last * v_stride + kv_row)) || k_pool == v_pool)
+        return PA_ERR_INVALID_ARG;
     const int sms = current_sms();
     if (sms <= 0) return PA_ERR_CUDA;
     RopeArgs a{};

@@ -364,6 +364,8 @@ def _decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_ma
                  workspace, err):
     """pa_decode_tree by way of every check."""
     dev = _index("q", q)
+    if not 1 <= max_nodes <= 64:
+        raise ValueError("max_nodes must be 1..64")
     dt = q.dtype
     if dt not in _DTYPES:
         raise TypeError("q must be float16 or bfloat16")
@@ -423,6 +425,8 @@ def pa_tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_len
 def _tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_lens, max_nodes, path, err):
     """pa_tree_verify by way of every check."""
     dev = _index("tree_masks", tree_masks)
+    if not 1 <= max_nodes <= 64:
+        raise ValueError("max_nodes must be 1..64")
     _arg("tree_masks", tree_masks, torch.int64, dev)
     _arg("draft_tokens", draft_tokens, torch.int64, dev)
     _arg("target_tokens", target_tokens, torch.int64, dev)
@@ -434,7 +438,7 @@ def _tree_verify(tree_masks, draft_tokens, target_tokens, q_start, context_lens,
     if draft_tokens.shape != (T,) or target_tokens.shape != (T,) or q_start.shape != (N + 1,):
         raise ValueError("draft_tokens and target_tokens must have tree_masks' shape, q_start N + 1 entries")
     if path is None:
-        path = torch.empty((N, max(0, max_nodes)), dtype=torch.int32, device=context_lens.device)
+        path = torch.empty((N, max_nodes), dtype=torch.int32, device=context_lens.device)
     else:
         _arg("path", path, torch.int32, dev)
         if path.shape != (N, max_nodes):

@@ -257,6 +257,71 @@ def test_refusals_on_the_device():
     assert pa().pa_decode_tree(**{**good, "q": q[:0], "tree_masks": signed([]), "q_start": none}).shape[0] == 0
 
 
+@pytest.mark.parametrize("g,nodes,N", [(2, 4, 700), (8, 3, 700), (16, 9, 400)])
+def test_many_short_sequences(g, nodes, N):
+    # more sequences than threads look for a chunk's beginning, empty trees and contexts among them
+    r = np.random.default_rng(N + nodes)
+    ctx = [int(x) for x in r.integers(0, 40, size=N)]
+    sizes = [int(r.integers(0, min(nodes, c) + 1)) for c in ctx]
+    cfg = DecodeConfig(name="many", num_seqs=N, num_q_heads=g, num_kv_heads=1, head_dim=64, block_size=16, dtype="fp16",
+                       seed=N, ctx_fixed=tuple(ctx), pool_factor=1.2)
+    case = make_decode_case(cfg, device="cuda", poison_unused=True)
+    qs = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    q = make_values((int(qs[-1]), g, 64), "fp16", torch.Generator(device="cuda").manual_seed(N), "cuda")
+    masks = [m for n in sizes for m in masks_ref(random_tree(n, r))]
+    close(run(case, q, qs, masks, nodes), oracle(case, q, qs, masks), case)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,nodes", [(4, 4), (2, 20), (4, 64)])
+def test_one_long_sequence_in_many_pieces(d, g, nodes):
+    case, q, qs, masks = tree_case([4000], [nodes], Hq=2 * g, Hkv=2, d=d, seed=161 + nodes)
+    close(run(case, q, qs, masks, nodes), oracle(case, q, qs, masks), case)
+
+
+def test_negative_and_zero_scales():
+    case, q, qs, masks = tree_case([70, 300, 40], [20, 33, 40], Hq=8, Hkv=2, seed=171)
+    for case.scale in (-0.09, 0.0):
+        close(run(case, q, qs, masks, 40), oracle(case, q, qs, masks), case, f"scale {case.scale}")
+    small, sq, sqs, sm = tree_case([70, 30], [4, 3], Hq=8, Hkv=2, seed=181)
+    mid, mq, mqs, mm = tree_case([70, 90], [12, 9], Hq=8, Hkv=2, seed=191)
+    for s in (-0.09, 0.0):
+        small.scale = mid.scale = s
+        close(run(small, sq, sqs, sm, 4), oracle(small, sq, sqs, sm), small, f"scale {s}")
+        close(run(mid, mq, mqs, mm, 12), oracle(mid, mq, mqs, mm), mid, f"scale {s}")
+
+
+def test_compiled_and_checked_host_sides_agree():
+    # the compiled calls and the Python ones behind them give the same results
+    from paged_kv_cache_254_gb300 import ops
+    case, q, qs, masks = tree_case([300, 70], [20, 9], Hq=8, Hkv=2, seed=201)
+    bt, cl = dev_case(case)
+    args = (q, case.k_pool, case.v_pool, bt, cl, torch.from_numpy(qs).cuda(), signed(masks), case.scale, 20, None, None,
+            None)
+    want = ops._decode_tree(*args)
+    fast = ops._load_fast()
+    got = fast.decode_tree(ops._sp_cache, *args)
+    assert got is not NotImplemented and torch.equal(got, want)
+    assert fast.decode_tree({}, *args) is NotImplemented                     # no workspace yet
+    trees, draft, target, vqs = verify_inputs([6, 13, 0, 64], seed=9)
+    v = (signed([m for t in trees for m in masks_ref(t)]), cat(draft), cat(target), torch.from_numpy(vqs).cuda(),
+         torch.tensor([10, 13, 4, 99], dtype=torch.int32, device="cuda"), 64, None, None)
+    for a, b in zip(fast.tree_verify(*v), ops._tree_verify(*v)):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.is_contiguous() and torch.equal(a, b)
+    given = torch.empty(4, 64, dtype=torch.int32, device="cuda")
+    assert fast.tree_verify(*v[:6], given, None)[0] is given
+    # whatever is not plainly right is declined, and nothing is launched
+    for bad in ((q.float(),) + args[1:], args[:8] + (0,) + args[9:], args[:8] + (65,) + args[9:], args[:7] + (1,) + args[8:],
+                args[:4] + (cl.long(),) + args[5:], args[:9] + (q,) + args[10:], (q.cpu(),) + args[1:]):
+        assert fast.decode_tree(ops._sp_cache, *bad) is NotImplemented
+    for bad in (1 << 70, -(1 << 70)):
+        with pytest.raises(ValueError):
+            pa().pa_decode_tree(*args[:8], max_nodes=bad)
+        with pytest.raises(ValueError):
+            pa().pa_tree_verify(*v[:5], bad)
+    assert fast.tree_verify(*v[:5]) is NotImplemented and fast.keep_kv() is NotImplemented
+
+
 def test_captured_graphs_share_nothing():
     # two captured calls replayed side by side on two streams, after eager calls that regrow the shared workspace
     a = tree_case([3000, 900], [20, 20], Hq=8, Hkv=2, seed=121)

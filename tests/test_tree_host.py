@@ -28,12 +28,13 @@ def off(k):
     (dict(q=NULL), 1), (dict(masks=NULL), 1), (dict(q_start=NULL), 1), (dict(q=off(2)), 1), (dict(masks=off(4)), 1),
     (dict(sh=dict(head_dim=96)), 2), (dict(sh=dict(block_size=8)), 2), (dict(sh=dict(num_q_heads=6)), 2),
     (dict(sh=dict(dtype=2)), 1), (dict(sh=dict(num_seqs=-1)), 1), (dict(sh=dict(num_seqs=0)), 0),
+    (dict(out=FAKE), 1), (dict(out=ctypes.c_void_p(FAKE.value + 2048)), 1),      # over q
 ])
 def test_decode_tree_checks(lib, kw, status):
     sh = shape(**{**dict(head_dim=128, num_q_heads=8, num_kv_heads=2), **kw.pop("sh", {})})
     a = {**dict(max_nodes=4, total=8, q=FAKE, q_start=FAKE, masks=FAKE, scale=0.1), **kw}
     assert lib.pa_decode_tree(sh, a["max_nodes"], a["total"], a["q"], a["q_start"], a["masks"], FAKE, FAKE, FAKE,
-                              FAKE, a["scale"], FAKE, FAKE, BUF_BYTES, NULL, NULL) == status
+                              FAKE, a["scale"], a.get("out", off(1 << 16)), FAKE, BUF_BYTES, NULL, NULL) == status
 
 
 def test_tree_workspace_of_bad_shapes_is_zero(lib):
@@ -52,8 +53,9 @@ def test_verify_checks(lib):
 
 
 def test_keep_checks(lib):
-    def k(p=8, path=FAKE, k_pool=FAKE, table=FAKE, **sh):
-        return lib.pa_keep_kv(shape(**sh), p, path, FAKE, table, FAKE, k_pool, FAKE, NULL, NULL)
+    def k(p=8, path=FAKE, k_pool=FAKE, v_pool=off(1 << 16), table=FAKE, **sh):
+        return lib.pa_keep_kv(shape(**sh), p, path, FAKE, table, FAKE, k_pool, v_pool, NULL, NULL)
+    assert k(v_pool=FAKE) == 1                            # one pool for both
     assert k(p=0) == 1 and k(p=65) == 1 and k(path=NULL) == 1 and k(table=NULL) == 1 and k(k_pool=off(8)) == 1
     assert k(dtype=2) == 1 and k(num_seqs=-1) == 1 and k(max_blocks_per_seq=0) == 1
     assert k(num_blocks=1 << 27) == 2
@@ -62,11 +64,10 @@ def test_keep_checks(lib):
 
 
 def test_rope_append_checks(lib):
-    def r(n=4, q=FAKE, qs=512, ks=512, vs=512, out=off(1 << 16), rot=64, freq=FAKE, scale=1.0, eps=1e-6, qw=None,
+    def r(n=4, q=FAKE, k=off(1 << 17), v=off(3 << 16), qs=512, ks=512, vs=512, out=off(1 << 16), v_pool=off(1 << 19), rot=64, freq=FAKE, scale=1.0, eps=1e-6, qw=None,
           rope=True, pos=FAKE, **sh):
         rp = _lib.PaRope(freq.value, rot, 0, scale, eps, qw, None) if rope else None
-        return lib.pa_rope_append_kv(shape(**sh), rp, n, q, qs, FAKE, ks, FAKE, vs, pos, FAKE, out, FAKE, FAKE, NULL,
-                                     NULL)
+        return lib.pa_rope_append_kv(shape(**sh), rp, n, q, qs, k, ks, v, vs, pos, FAKE, out, FAKE, v_pool, NULL, NULL)
     assert r(n=0) == 0
     assert r(rope=False) == 1 and r(n=-1) == 1 and r(q=NULL) == 1 and r(out=NULL) == 1 and r(pos=NULL) == 1
     assert r(freq=NULL) == 1 and r(rot=80) == 1 and r(rot=-16) == 1
@@ -74,6 +75,8 @@ def test_rope_append_checks(lib):
     assert r(qs=504) == 1 and r(ks=504) == 1 and r(vs=516) == 1          # shorter than a row; not 16 bytes
     assert r(scale=float("nan")) == 1 and r(eps=-1.0) == 1 and r(eps=float("inf")) == 1
     assert r(qw=FAKE.value + 8) == 1 and r(q=off(8)) == 1 and r(dtype=3) == 1 and r(num_q_heads=0) == 1
+    assert r(v_pool=FAKE) == 1                            # one pool for both
+    assert r(k=off((1 << 16) + 512)) == 1 and r(v=off((1 << 16) - 512)) == 1   # q_out over the keys, the values
     # q_out over a shifted or strided q
     assert r(out=off(16)) == 1 and r(out=FAKE, qs=520) == 1 and r(q=off(1024), out=off(512)) == 1
 
