@@ -386,7 +386,8 @@ pa_status pa_append_kv(const pa_shape* shape, int32_t num_tokens, const void* k_
  * Angles are exact to 2^-32 of a turn at any int32 position.  Queries go to
  * q_out, keys and (untouched) values to the pools at slot_mapping[t] as in
  * pa_append_kv (a negative slot skips them; a slot past the pool sets
- * PA_DEVERR_SLOT and skips them; the token's queries are written all the same).
+ * PA_DEVERR_SLOT and skips them; the token's queries are written all the same;
+ * no slot appears twice in one call).
  *
  *   q, k_new, v_new  [num_tokens] rows of [Hq][d], [Hkv][d], [Hkv][d], consecutive
  *                    tokens q_stride, k_stride, v_stride elements apart (multiples
