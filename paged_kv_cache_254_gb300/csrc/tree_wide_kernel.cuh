@@ -11,11 +11,22 @@
 //   S_t  = Q_t K^T   M 128, N 128, K = head_dim   (Q, K: K-major swizzled tiles)
 //   O_t += P_t V     M 128, N = head_dim, K 128   (P from tensor memory, V MN-major)
 //
-// What bounds it: the tensor core.  A stage costs (2 + 2 * 2) * 512 cycles of MMA
-// at head_dim 128 (the PV product runs twice, hi and lo) for 64 KB of keys and
-// values, which HBM delivers in about 2800.  Two tiles share each copied stage,
-// so the keys are read once per 256 rows, and one tile's softmax runs while the
-// other's products do.  N = 128 because an MMA of N = 64 takes as long.
+// What bounds it: each tile's chain of scores, softmax and products, and the tensor
+// core.  A stage costs 2 * (1 + 2) * 512 cycles of MMA at head_dim 128 (the PV
+// product runs twice, hi and lo) for 64 KB of keys and values, which HBM delivers in
+// about 2800; it takes about 5400.  Two tiles share each copied stage, so the keys
+// are read once per 256 rows, and tile 1 follows tile 0 by its score product, so that
+// one tile's softmax runs beside the other's products.  N = 128 because an MMA of
+// N = 64 takes as long.
+//
+// Measured: 64 sequences of 1024-8192 tokens, 64 nodes, 64 / 8 heads, d 128, bf16:
+// 0.765 ms, 0.80 PFLOP/s with each product counted once (0.41 of cuBLAS).  The softmax is short of instructions, not of units: with its loops over the
+// 128 scores unrolled, the masks among them and both tiles in step it took 0.92 ms;
+// 0.89 with the weights handed over by the quarter and the wait for the next keys
+// before the one for the products, 0.86 with rolled loops, 0.82 with the tiles apart,
+// 0.77 with masks and signs out of the loops.  16 softmax warps, two to a row, took
+// 1.11 ms unrolled.  The products' issue stays unrolled: rolled, an MMA takes 130
+// cycles to issue instead of 64.
 //
 // Tensor memory (512 columns): S_0, S_1 at 0 and 128, O_0, O_1 at 256 and 384.  P_t
 // overwrites S_t, 32 keys at a time (16 columns of hi, 16 of lo, in the 32 columns
@@ -60,8 +71,8 @@ struct WideTraits {
     static constexpr int Q_BYTES = 2 * HALVES * Q_HALF;
     static constexpr int NREC = 8;                           // stage records in use at most: slots / 2 + 2
     static constexpr int R_CAP = 8;
-    // full, empty, ready; s_full, p_half[2], pv_done; q_full, q_empty; fin; described
-    static constexpr int NBAR = 3 * R_CAP + 2 * 4 + 2 + 2 + NREC;
+    // full, empty, ready; s_full, p_part[4], pv_done; q_full, q_empty; fin; described; lead, follow
+    static constexpr int NBAR = 3 * R_CAP + 2 * 6 + 2 + 2 + NREC + 2;
     static constexpr int REC_OFF = (8 * NBAR + 15) / 16 * 16;
     static constexpr int MISC_OFF = REC_OFF + NREC * 48;
     static constexpr int START_OFF = MISC_OFF + 16;          // a TreeStart, a word per warp
@@ -115,11 +126,13 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     auto empty = [&](int st) -> uint32_t { return sbase + 8 * (Tr::R_CAP + st); };
     auto ready = [&](int st) -> uint32_t { return sbase + 8 * (2 * Tr::R_CAP + st); };
     const uint32_t tile_bars = sbase + 8 * 3 * Tr::R_CAP;
-    auto s_full = [&](int t) -> uint32_t { return tile_bars + 32 * t; };
-    auto p_half = [&](int t, int h) -> uint32_t { return tile_bars + 32 * t + 8 + 8 * h; };
-    auto pv_done = [&](int t) -> uint32_t { return tile_bars + 32 * t + 24; };
-    const uint32_t q_full = tile_bars + 64, q_empty = q_full + 8, fin = q_empty + 8;   // fin[2]
+    auto s_full = [&](int t) -> uint32_t { return tile_bars + 48 * t; };
+    auto p_part = [&](int t, int c) -> uint32_t { return tile_bars + 48 * t + 8 + 8 * c; };
+    auto pv_done = [&](int t) -> uint32_t { return tile_bars + 48 * t + 40; };
+    const uint32_t q_full = tile_bars + 96, q_empty = q_full + 8, fin = q_empty + 8;   // fin[2]
     const uint32_t described = fin + 16;                      // [NREC] the stage's record is written
+    // tile 1's scores of a stage come after tile 0's, tile 0's next ones after those have been issued
+    const uint32_t lead = described + 8 * Tr::NREC, follow = lead + 8;
     WideStage* recs = reinterpret_cast<WideStage*>(smem + Tr::REC_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Tr::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Tr::MISC_OFF + 4);
@@ -132,14 +145,15 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_half(t, 0), 4);             // the tile's four warps
-            mbar_init(p_half(t, 1), 4);
+            for (int c = 0; c < 4; ++c) mbar_init(p_part(t, c), 4);   // the tile's four warps
             mbar_init(pv_done(t), 1);
             mbar_init(fin + 8 * t, 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 2);
         for (int i = 0; i < Tr::NREC; ++i) mbar_init(described + 8 * i, 1);
+        mbar_init(lead, 1);
+        mbar_init(follow, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -156,7 +170,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();                 // the pre-pass is complete
+    griddep_wait();                 // the launch before is complete
     griddep_launch_dependents();
 
     const int32_t* qst = mp.q_start;
@@ -198,7 +212,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
     const long long lo = has_work ? sc.lo(blockIdx.x) : 0, hi = has_work ? sc.lo(blockIdx.x + 1) : 0;
 
     if (warp >= Tr::COPY_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == Tr::COPY_WARP) {
             // ============================================================ copies
             // with one group the keys are read once per call; with more, another CTA
@@ -393,6 +407,7 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
             uint32_t ph = 0;
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+                if (mbar_try_wait(bar, parity)) return true;
                 if (*abort_flag || !mbar_wait_bounded(bar, parity, p.timeout_ns)) ok = false;
                 return ok;
             };
@@ -402,17 +417,25 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                     ph ^= 1u;
                 }
             };
-            for (int j = 0;; ++j) {
-                const uint32_t par = (uint32_t)(j & 1);
-                if (!wait(ready(st), ph)) break;                  // (the look warp never falls a slot's use behind)
+            int flags = 0;
+            bool active = false;
+            auto keys = [&](int j) -> bool {                      // stage j's keys, and its segment's Q, are there
+                if (!wait(ready(st), ph)) return false;           // (the look warp never falls a slot's use behind)
                 const WideStage& rc = recs[j % Tr::NREC];
-                const int flags = rc.flags;
-                if (flags & TC_END) break;
-                const bool active = rc.n > tile_rows0;
+                flags = rc.flags;
+                if (flags & TC_END) return false;
+                active = rc.n > tile_rows0;
                 if (flags & TC_FIRST) {
-                    if (!wait(q_full, (uint32_t)(nseg & 1))) break;
+                    if (!wait(q_full, (uint32_t)(nseg & 1))) return false;
                     ++nseg;
                 }
+                return true;
+            };
+            for (int j = 0, more = keys(0); more; ++j) {
+                const uint32_t par = (uint32_t)(j & 1);
+                // Not with the other tile: its scores, then this tile's, so that one tile's softmax runs
+                // beside the other's products (together, each waited for the other: 814 against 770 us).
+                if (t == 1 ? !wait(lead, par) : j > 0 && !wait(follow, par ^ 1u)) break;
                 if (active) {
                     tc_fence_after();
                     const uint64_t qd = sdesc_sw128(q_base + t * HALVES * Tr::Q_HALF, 16, 1024);
@@ -422,27 +445,30 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                         mma_f16(s_col, qd + (uint64_t)((k / 4) * (Tr::Q_HALF >> 4) + (k % 4) * 2),
                                 kd + (uint64_t)((k / 4) * (1024 >> 4) + (k % 4) * 2), IDESC_S, k > 0 ? 1u : 0u);
                     mma_commit(s_full(t));
+                    if (t == 0) mma_commit(lead);
                     mma_commit(empty(st));
                     if (flags & TC_LAST) mma_commit(q_empty);
                 } else {
                     mbar_arrive(s_full(t));
+                    if (t == 0) mbar_arrive(lead);
                     mbar_arrive(empty(st));
                     if (flags & TC_LAST) mbar_arrive(q_empty);
                 }
+                if (t == 1) mbar_arrive(follow);
                 next_slot();
                 if (!wait(ready(st), ph)) break;
                 const uint32_t vbase = ring + st * Tr::SLOT_BYTES;
                 bool stop = false;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {                     // as each half of the weights is there
-                    if (!wait(p_half(t, h), par)) {
+                for (int h = 0; h < 4; ++h) {                     // as each quarter of the weights is there
+                    if (!wait(p_part(t, h), par)) {
                         stop = true;
                         break;
                     }
                     if (active) {
                         tc_fence_after();
 #pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k) {
+                        for (int k = 2 * h; k < 2 * h + 2; ++k) {
                             const uint64_t bv = sdesc_sw128(vbase + ((16 * k) / BS) * Tr::BLK_BYTES + ((16 * k) % BS) * 128,
                                                             Tr::HALF_STRIDE, 1024);
                             const uint32_t pt = s_col + 32 * (k / 2) + 8 * (k % 2);
@@ -452,16 +478,18 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                     }
                 }
                 if (stop) break;
+                const bool issued = active;
                 if (active) {
                     mma_commit(pv_done(t));
                     mma_commit(empty(st));
-                    // the next scores overwrite the weights
-                    if (!wait(pv_done(t), par)) break;
                 } else {
                     mbar_arrive(pv_done(t));
                     mbar_arrive(empty(st));
                 }
                 next_slot();
+                more = keys(j + 1);
+                // the next scores overwrite the weights
+                if (issued && more && !wait(pv_done(t), par)) break;
             }
             if (!ok) {
                 set_err(p.err, PA_DEVERR_TIMEOUT);
@@ -474,8 +502,8 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
         __syncwarp();
     } else {
         // ================================================================ softmax
-        // 256 x 216 + 128 x 72 registers: the 384 x 168 of the launch
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // 256 x 200 + 128 x 104 registers: the 384 x 168 of the launch
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;                        // row of the tile = TMEM lane
         const int node = (t * Tr::TILE + r) >> gs;                // node of the group
@@ -524,34 +552,17 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
             const bool busy = active && __any_sync(0xffffffffu, alive);
             if (busy) {
                 tc_fence_after();
-                float x[KEYS];
-                {
-                    uint32_t u[KEYS / 32][32];
-#pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) tmem_ld32(s_addr + 32 * c, u[c]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        after_wait(u[c]);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) x[32 * c + k] = __uint_as_float(u[c][k]);
+                uint32_t u[32];
+                // Scores that some row may not see, or whose order a scale turns, are rewritten first,
+                // so that the loops below, which every stage runs, stay short: they are bound by
+                // instruction fetches.
+                if (flip || t0 + KEYS > base || nkeys < KEYS) {
+                    auto held = [&](int n) -> uint64_t { return n >= 64 ? ~0ull : n > 0 ? (1ull << n) - 1 : 0ull; };
+                    uint64_t s0 = 0, s1 = 0;                      // the keys that the row sees
+                    if (alive) {
+                        s0 = tree_visible(sees, base - t0) & held(nkeys);
+                        s1 = tree_visible(sees, base - t0 - 64) & held(nkeys - 64);
                     }
-                }
-                if (flip)
-#pragma unroll
-                    for (int k = 0; k < KEYS; ++k) x[k] *= p.scale_log2;
-                if (t0 + KEYS > base || nkeys < KEYS) {           // uniform: keys that some row may not see
-                    const uint64_t s0 = tree_visible(sees, base - t0), s1 = tree_visible(sees, base - t0 - 64);
-                    uint32_t w[4] = {(uint32_t)s0, (uint32_t)(s0 >> 32), (uint32_t)s1, (uint32_t)(s1 >> 32)};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int left = nkeys - 32 * i;
-                        if (left < 32) w[i] &= left > 0 ? (1u << left) - 1 : 0u;
-                        if (!alive) w[i] = 0;
-                    }
-#pragma unroll
-                    for (int k = 0; k < KEYS; ++k)
-                        if (!((w[k / 32] >> (k % 32)) & 1u)) x[k] = -INFINITY;
                     if (base < t0 + nkeys) {                      // the stage holds nodes: their V has been looked at
                         int vs = st + 1;
                         uint32_t vph = ph;
@@ -566,12 +577,36 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                         const volatile uint32_t* words = rc.spoilt;
                         if (((uint64_t)words[0] | ((uint64_t)words[1] << 32)) & sees) l = qnan;
                     }
+#pragma unroll 1
+                    for (int c = 0; c < KEYS / 32; ++c) {
+                        tmem_ld32(s_addr + 32 * c, u);
+                        tmem_ld_wait();
+                        after_wait(u);
+                        const uint32_t w = (uint32_t)((c < 2 ? s0 : s1) >> (32 * (c & 1)));
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float x = __uint_as_float(u[k]);
+                            u[k] = (w >> k) & 1u ? __float_as_uint(flip ? x * p.scale_log2 : x) : 0xff800000u;
+                        }
+                        tmem_st32(s_addr + 32 * c, u);
+                    }
+                    tmem_st_wait();
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int c = 0; c < KEYS / 32; c += 2) {
+                    uint32_t v[32];
+                    tmem_ld32(s_addr + 32 * c, u);
+                    tmem_ld32(s_addr + 32 * c + 32, v);
+                    tmem_ld_wait();
+                    after_wait(u);
+                    after_wait(v);
 #pragma unroll
-                for (int k = 0; k < KEYS; k += 8)
+                    for (int k = 0; k < 32; k += 4)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], x[k + i]), x[k + 4 + i]);
+                        for (int i = 0; i < 4; ++i)
+                            m4[i] = fmaxf(fmaxf(m4[i], __uint_as_float(u[k + i])), __uint_as_float(v[k + i]));
+                }
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
                 const bool need = mx > m + Tr::TAU && alive;
                 const float alpha = need ? ex2(m - mx) : 1.f;     // m = -inf: 0
@@ -586,9 +621,8 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                         break;
                     }
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
-                        uint32_t u[32];
                         tmem_ld32(o_addr + 32 * c, u);
                         tmem_ld_wait();
                         after_wait(u);
@@ -598,23 +632,30 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                     }
                     tmem_st_wait();
                 }
+                tmem_ld32(s_addr, u);
                 const float mref = m == -INFINITY ? 0.f : m;      // no visible key yet: weights 0
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+                const f32x2 scale2 = pair2(scale, scale), mref2 = pair2(-mref, -mref);
+                f32x2 sum2[2] = {0ull, 0ull};
+                tmem_ld_wait();
+                after_wait(u);
+#pragma unroll 1
                 for (int c = 0; c < KEYS / 32; ++c) {
                     uint32_t w[32];                               // 16 columns of hi, 16 of lo
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(x[32 * c + 2 * e], scale, -mref));
-                        const float p1 = ex2(fmaf(x[32 * c + 2 * e + 1], scale, -mref));
-                        s4[e & 3] += p0 + p1;
+                        float p0, p1;
+                        split2(fma2(pair2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), scale2, mref2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum2[e & 1] = add2(sum2[e & 1], pair2(p0, p1));
                         if constexpr (Tr::BF16) {
                             // hi: the weights cut to bf16; lo: the exact remainders, cut the same way
                             // (relative error < 2^-14 in all)
                             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                             w[e] = __byte_perm(u0, u1, 0x7632);
-                            const float r0 = p0 - __uint_as_float(u0 & 0xffff0000u);
-                            const float r1 = p1 - __uint_as_float(u1 & 0xffff0000u);
+                            float r0, r1;
+                            split2(add2(pair2(p0, p1), pair2(-__uint_as_float(u0 & 0xffff0000u),
+                                                             -__uint_as_float(u1 & 0xffff0000u))), r0, r1);
                             w[16 + e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
                         } else {
                             const uint32_t hv = pack2<false>(p0, p1);
@@ -622,21 +663,22 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                             w[16 + e] = pack2<false>(p0 - lo_of<false>(hv), p1 - hi_of<false>(hv));
                         }
                     }
+                    if (c + 1 < KEYS / 32) tmem_ld32(s_addr + 32 * c + 32, u);
                     tmem_st32(s_addr + 32 * c, w);
-                    if (c & 1) {                                  // half of the weights are there
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_half(t, c >> 1));
-                    }
+                    tmem_st_wait();                               // a quarter of the weights is there
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_part(t, c));
+                    tmem_ld_wait();
+                    after_wait(u);
                 }
-                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                float sa, sb;
+                split2(add2(sum2[0], sum2[1]), sa, sb);
+                l += sa + sb;
             } else {
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(p_half(t, 0));
-                    mbar_arrive(p_half(t, 1));
-                }
+                if (lane == 0)
+                    for (int c = 0; c < 4; ++c) mbar_arrive(p_part(t, c));
             }
             if (flags & TC_LAST) {
                 if (!wait_all(pv_done(t), par)) {
