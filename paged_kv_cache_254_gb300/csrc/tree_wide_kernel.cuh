@@ -20,13 +20,14 @@
 // N = 64 takes as long.
 //
 // Measured: 64 sequences of 1024-8192 tokens, 64 nodes, 64 / 8 heads, d 128, bf16:
-// 0.765 ms, 0.80 PFLOP/s with each product counted once (0.41 of cuBLAS).  The softmax is short of instructions, not of units: with its loops over the
-// 128 scores unrolled, the masks among them and both tiles in step it took 0.92 ms;
-// 0.89 with the weights handed over by the quarter and the wait for the next keys
-// before the one for the products, 0.86 with rolled loops, 0.82 with the tiles apart,
-// 0.77 with masks and signs out of the loops.  16 softmax warps, two to a row, took
-// 1.11 ms unrolled.  The products' issue stays unrolled: rolled, an MMA takes 130
-// cycles to issue instead of 64.
+// 0.765 ms, 0.80 PFLOP/s with each product counted once (0.41 of cuBLAS).  The
+// softmax is short of instructions, not of units: with its loops over the 128 scores
+// unrolled, the masks among them and both tiles in step it took 0.92 ms; 0.90 with
+// the weights handed over by the quarter and the wait for the next keys before the
+// one for the products, 0.86 with rolled loops, 0.82 with the tiles apart, 0.77 with
+// masks and signs out of the loops.  16 softmax warps, two to a row, took 1.11 ms
+// unrolled.  The products' issue stays unrolled: rolled, an MMA takes 130 cycles to
+// issue instead of 64.
 //
 // Tensor memory (512 columns): S_0, S_1 at 0 and 128, O_0, O_1 at 256 and 384.  P_t
 // overwrites S_t, 32 keys at a time (16 columns of hi, 16 of lo, in the 32 columns
