@@ -53,12 +53,11 @@
 
 namespace pa {
 
-template <int D_, int BS_, bool BF16_, bool TREE_ = false>
+template <int D_, int BS_, bool BF16_>
 struct TcTraits {
     static constexpr int D = D_;
     static constexpr int BS = BS_;
     static constexpr bool BF16 = BF16_;
-    static constexpr bool TREE = TREE_;                      // drafted trees: visible keys by ancestor masks
     static constexpr int ROWS = 128;                         // M of every MMA
     static constexpr int KEYS = 64;                          // keys per stage (N of the score MMA)
     static constexpr int SB = KEYS / BS;                     // blocks per stage
@@ -84,8 +83,7 @@ struct TcTraits {
     static constexpr int SMEM_BYTES = SMEM_CAP;              // all of it, 1024 of it alignment slack
     static constexpr int R_CAP = 12;
     static constexpr int REC_BYTES = 48;
-    // s_full[2] s_free[2] p_full[2] pv_done[2] q_full q_empty fin o_free; trees: scanned[2]
-    static constexpr int NBAR_FIXED = TREE ? 14 : 12;
+    static constexpr int NBAR_FIXED = 12;    // s_full[2] s_free[2] p_full[2] pv_done[2] q_full q_empty fin o_free
     // tagged cells per row: softmax references along a segment's stages [4],
     // and the partial row sums handed to a segment's last stage [4] (value, reference)
     static constexpr int XCH_BYTES = (4 + 2 * 4) * ROWS * 8;
@@ -93,8 +91,7 @@ struct TcTraits {
     static constexpr int REC_OFF = (BAR_OFF + 8 * (2 * R_CAP + NBAR_FIXED) + 15) / 16 * 16;
     static constexpr int XCH_OFF = REC_OFF + R_CAP * REC_BYTES;
     static constexpr int MISC_OFF = XCH_OFF + XCH_BYTES;      // TMEM base, abort flag, stage count
-    static constexpr int START_OFF = MISC_OFF + 16;           // trees: a TreeStart, a word per warp
-    static constexpr int Q_OFF = (MISC_OFF + 16 + (TREE ? 32 + 8 * 12 : 0) + 1023) / 1024 * 1024;
+    static constexpr int Q_OFF = (MISC_OFF + 16 + 1023) / 1024 * 1024;
     // rows of the Q tile: the launch's q_box tokens x g heads, whole 8-row swizzle atoms
     __host__ __device__ static constexpr int q_rows(int q_box, int g) {
         return q_box * g >= ROWS ? ROWS : (q_box * g + 7) / 8 * 8;
@@ -105,9 +102,7 @@ struct TcTraits {
                    : (SMEM_CAP - 1024 - Q_OFF - HALVES * qrows * 128) / STAGE_BYTES;
     }
     static constexpr int SOFT_WARPS = 8;
-    // trees: a twelfth, idle warp completes the third warpgroup, whose registers the
-    // softmax warps take over (masks need more than the even share)
-    static constexpr int THREADS = 32 * (SOFT_WARPS + (TREE ? 4 : 3));
+    static constexpr int THREADS = 32 * (SOFT_WARPS + 3);
     static constexpr int COPY_WARP = SOFT_WARPS, MMA_WARP = SOFT_WARPS + 1, PV_WARP = SOFT_WARPS + 2;
     static constexpr int TMEM_COLS = 512;
     static constexpr int O_COL = 128;                        // S buffers at columns 0 and 64
@@ -122,10 +117,9 @@ struct TcTraits {
 
 // One ring stage as the copy warp describes it to the consumers.
 struct alignas(16) TcStage {
-    int base, kvh, t0, nkeys;    // first position of the chunk, KV head, first key, keys copied (blocks x B)
+    int s, kvh, t0, nkeys;       // sequence, KV head, first key, keys copied (blocks x B)
     int n, ctx, q0, flags;       // chunk length, context, first query row of the sequence
-    int poison, seg;             // bad block id seen; segment number within the CTA
-    uint32_t spoilt[2];          // trees: stage keys (bits) whose V is not finite
+    int poison, seg, pad1, pad2;  // bad block id seen; segment number within the CTA
 };
 static_assert(sizeof(TcStage) == 48, "stage record");
 
@@ -179,7 +173,6 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     auto empty = [&](int st) -> uint32_t { return bars + 8 * (R + st); };
     const uint32_t s_full = bars + 16 * R, s_free = s_full + 16, p_full = s_free + 16, pv_done = p_full + 16;
     const uint32_t q_full = pv_done + 16, q_empty = q_full + 8, fin = q_empty + 8, o_free = fin + 8;
-    const uint32_t scanned = o_free + 8;                      // trees only
     TcStage* recs = reinterpret_cast<TcStage*>(smem + Tr::REC_OFF);
     volatile unsigned long long* xch = reinterpret_cast<volatile unsigned long long*>(smem + Tr::XCH_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Tr::MISC_OFF);
@@ -201,10 +194,6 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         mbar_init(q_empty, 1);
         mbar_init(fin, 2);                      // the score thread and the PV thread
         mbar_init(o_free, SW / 2);              // a segment's output read: the four warps of its last stage
-        if constexpr (Tr::TREE) {               // a stream's four warps have looked at the tree's V rows
-            mbar_init(scanned, SW / 2);
-            mbar_init(scanned + 8, SW / 2);
-        }
         *abort_flag = 0;
         *n_stages = 0x7fffffff;
         fence_mbar_init();
@@ -229,22 +218,11 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     griddep_wait();
     griddep_launch_dependents();
 
-    const int32_t* qst = mp.q_start;
-    std::conditional_t<Tr::TREE, TreeTab, SeqTab> tab;
+    SeqTab tab;
+    tab.cum = p.cum;
     tab.ctx = p.context_lens;
-    if constexpr (Tr::TREE) {
-        tab.qst = qst;
-        tab.N = p.N;
-        tab.groups = 1;
-        tab.group_nodes = mp.group_nodes;
-        tab.max_nodes = mp.max_q;
-        tab.total_q = mp.total_q;
-        tab.MB = p.MB;
-        tab.BS = BS;
-    } else {
-        tab.cum = p.cum;
-        tab.first = nullptr;
-    }
+    tab.first = nullptr;
+    const int32_t* qst = mp.q_start;
     // a sequence's chunk length, or -1 when it is malformed
     auto chunk_len = [&](int s) -> int {
         const int a = __ldg(qst + s), b = __ldg(qst + s + 1), ctx = __ldg(p.context_lens + s);
@@ -266,280 +244,254 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             p.out[i] = qnan16<Tr::BF16>();
     }
 
-    Sched sc;
-    const TreeStart& at = *reinterpret_cast<TreeStart*>(smem + Tr::START_OFF);
-    if constexpr (Tr::TREE) {
-        tree_start<Tr::THREADS>(tab, p.Hkv, SB, reinterpret_cast<long long*>(smem + Tr::START_OFF + 32),
-                                reinterpret_cast<TreeStart*>(smem + Tr::START_OFF));
-        sc = tree_sched(at.W, gridDim.x, SB);
-    } else {
-        sc = make_sched(__ldg(p.cum + p.N) * p.Hkv, gridDim.x, 0);
-    }
+    const Sched sc = make_sched(__ldg(p.cum + p.N) * p.Hkv, gridDim.x, 0);
     const bool has_work = (int)blockIdx.x < sc.NS;
     const long long lo = has_work ? sc.lo(blockIdx.x) : 0, hi = has_work ? sc.lo(blockIdx.x + 1) : 0;
 
-    // Trees: 256 x 200 + 128 x 104 registers, the 384 x 168 of the launch.
-    if (warp >= SW) {
-        if constexpr (Tr::TREE) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp == Tr::COPY_WARP) {
-            const uint64_t kv_pol = l2_evict_first();
-            // ================================================================ copies
-            int j = 0, st = 0, nseg = 0;            // stage, its ring slot and phase
-            uint32_t ph = 0;
-            bool ok = true;
-            if constexpr (Tr::TREE)
-                if (lane == 0) mp.starts[blockIdx.x] = at;
-            auto claim = [&]() -> bool {            // lane 0: slot st free for stage j (its last use done)
-                return j < R || mbar_wait_bounded(empty(st), ph ^ 1u, p.timeout_ns);
-            };
-            if (has_work) {
-                SegIter it;
-                if constexpr (Tr::TREE) {
-                    it.gi = lo;
-                    it.s = at.s;
-                    it.kvh = at.kvh;
-                    it.b0 = at.b0;
-                    it.nb = at.nb;
-                    it.first = 0;
-                } else {
-                    it = locate(p, tab, lo, lane);
-                }
-                while (ok && it.gi < hi) {
-                    const int len = seg_len(it, hi);
-                    const int n = chunk_len(it.s);
-                    if (n > 0) {
-                        const int ctx = __ldg(p.context_lens + it.s);
-                        const int q0 = __ldg(qst + it.s);
-                        const long long P0 = it.gi - it.b0;
-                        const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
-                        const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
+    if (warp == Tr::COPY_WARP) {
+        const uint64_t kv_pol = l2_evict_first();
+        // ================================================================ copies
+        int j = 0, st = 0, nseg = 0;            // stage, its ring slot and phase
+        uint32_t ph = 0;
+        bool ok = true;
+        auto claim = [&]() -> bool {            // lane 0: slot st free for stage j (its last use done)
+            return j < R || mbar_wait_bounded(empty(st), ph ^ 1u, p.timeout_ns);
+        };
+        if (has_work) {
+            SegIter it = locate(p, tab, lo, lane);
+            while (ok && it.gi < hi) {
+                const int len = seg_len(it, hi);
+                const int n = chunk_len(it.s);
+                if (n > 0) {
+                    const int ctx = __ldg(p.context_lens + it.s);
+                    const int q0 = __ldg(qst + it.s);
+                    const long long P0 = it.gi - it.b0;
+                    const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
+                    const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
+                    if (lane == 0) {
+                        if (nseg > 0 && !mbar_wait_bounded(q_empty, (uint32_t)((nseg - 1) & 1), p.timeout_ns)) {
+                            ok = false;
+                        } else {
+                            mbar_arrive_expect_tx(q_full, (uint32_t)(HALVES * 128 * G * mp.q_box));
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h)
+                                tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, it.kvh * G, q0, q_full);
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    ++nseg;
+                    const int32_t* trow = p.block_tables + (size_t)it.s * p.MB + it.b0;
+                    auto batch = [&](int from) -> int { return lane < len - from ? __ldg(trow + from + lane) : 0; };
+                    int ids = batch(0), ids_next = batch(32);
+                    const int nst = (len + SB - 1) / SB;
+                    for (int k = 0; ok && k < nst; ++k) {
+                        const int bb = k * SB;
+                        if (bb > 0 && (bb & 31) == 0) {
+                            ids = ids_next;
+                            ids_next = batch(bb + 32);
+                        }
+                        const int nbs = min(SB, len - bb);
+                        int idv[SB];
+#pragma unroll
+                        for (int i = 0; i < SB; ++i) idv[i] = __shfl_sync(0xffffffffu, ids, (bb + i) & 31);
                         if (lane == 0) {
-                            if (nseg > 0 && !mbar_wait_bounded(q_empty, (uint32_t)((nseg - 1) & 1), p.timeout_ns)) {
+                            if (!claim()) {
                                 ok = false;
                             } else {
-                                mbar_arrive_expect_tx(q_full, (uint32_t)(HALVES * 128 * G * mp.q_box));
-    #pragma unroll
-                                for (int h = 0; h < HALVES; ++h)
-                                    tma_load_3d(q_tile + h * q_half, &tmap_q, h * 64, it.kvh * G, q0, q_full);
+                                int poison = 0;
+#pragma unroll
+                                for (int i = 0; i < SB; ++i)
+                                    if (i < nbs && (unsigned)idv[i] >= (unsigned)p.NB) {
+                                        poison = 1;
+                                        idv[i] = 0;
+                                    }
+                                if (poison) set_err(p.err, PA_DEVERR_BLOCK_ID);
+                                TcStage& rc = recs[st];
+                                rc.s = it.s;
+                                rc.kvh = it.kvh;
+                                rc.t0 = (it.b0 + bb) * BS;
+                                rc.nkeys = nbs * BS;
+                                rc.n = n;
+                                rc.ctx = ctx;
+                                rc.q0 = q0;
+                                rc.flags = seg_flags | (k == 0 ? TC_FIRST : 0) | (k == nst - 1 ? TC_LAST : 0) |
+                                           (k == nst - 2 ? TC_PENULT : 0);
+                                rc.poison = poison;
+                                rc.seg = nseg;
+                                mbar_arrive_expect_tx(full(st), (uint32_t)(nbs * BS * 128 * HALVES * 2));
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, ok, 0);
-                        ++nseg;
-                        const int32_t* trow = p.block_tables + (size_t)it.s * p.MB + it.b0;
-                        auto batch = [&](int from) -> int { return lane < len - from ? __ldg(trow + from + lane) : 0; };
-                        int ids = batch(0), ids_next = batch(32);
-                        const int nst = (len + SB - 1) / SB;
-                        for (int k = 0; ok && k < nst; ++k) {
-                            const int bb = k * SB;
-                            if (bb > 0 && (bb & 31) == 0) {
-                                ids = ids_next;
-                                ids_next = batch(bb + 32);
-                            }
-                            const int nbs = min(SB, len - bb);
-                            int idv[SB];
-    #pragma unroll
-                            for (int i = 0; i < SB; ++i) idv[i] = __shfl_sync(0xffffffffu, ids, (bb + i) & 31);
-                            if (lane == 0) {
-                                if (!claim()) {
-                                    ok = false;
-                                } else {
-                                    int poison = 0;
-    #pragma unroll
-                                    for (int i = 0; i < SB; ++i)
-                                        if (i < nbs && (unsigned)idv[i] >= (unsigned)p.NB) {
-                                            poison = 1;
-                                            idv[i] = 0;
-                                        }
-                                    if (poison) set_err(p.err, PA_DEVERR_BLOCK_ID);
-                                    TcStage& rc = recs[st];
-                                    rc.base = ctx - n;
-                                    rc.kvh = it.kvh;
-                                    if constexpr (Tr::TREE) rc.spoilt[0] = rc.spoilt[1] = 0u;
-                                    rc.t0 = (it.b0 + bb) * BS;
-                                    rc.nkeys = nbs * BS;
-                                    rc.n = n;
-                                    rc.ctx = ctx;
-                                    rc.q0 = q0;
-                                    rc.flags = seg_flags | (k == 0 ? TC_FIRST : 0) | (k == nst - 1 ? TC_LAST : 0) |
-                                               (k == nst - 2 ? TC_PENULT : 0);
-                                    rc.poison = poison;
-                                    rc.seg = nseg;
-                                    mbar_arrive_expect_tx(full(st), (uint32_t)(nbs * BS * 128 * HALVES * 2));
-                                }
-                            }
-                            ok = __shfl_sync(0xffffffffu, ok, 0);
-                            __syncwarp();   // lane 0's claim of the slot orders the other lanes' copies
-                            // the stage's copies, one box per lane (the TMA unit takes boxes
-                            // one at a time, so each block's K and V go as one box each):
-                            // lanes 0 .. SB - 1 the K boxes, the next SB lanes the V boxes
-                            {
-                                const bool kl = lane < SB;
-                                const int ci = kl ? lane : lane - SB;
-                                int cid = __shfl_sync(0xffffffffu, ids, (bb + (ci & (SB - 1))) & 31);
-                                if ((unsigned)cid >= (unsigned)p.NB) cid = 0;   // flagged and poisoned above
-                                const int y = (cid * p.Hkv + it.kvh) * BS;
-                                const uint32_t dst = ring + st * Tr::STAGE_BYTES + (kl ? 0 : Tr::KV_BYTES) + ci * Tr::BLK_BYTES;
-                                if (ok && lane < 2 * SB && ci < nbs) {
-                                    // each block is read once: L2 evict-first
-                                    if (kl)
-                                        tma_load_4d_hint(dst, &tmap_k, 0, 0, 0, y / 8, full(st), kv_pol);
-                                    else
-                                        tma_load_3d_hint(dst, &tmap_v, 0, y, 0, full(st), kv_pol);
-                                }
-                            }
-                            ++j;
-                            if (++st == R) {
-                                st = 0;
-                                ph ^= 1u;
+                        __syncwarp();   // lane 0's claim of the slot orders the other lanes' copies
+                        // the stage's copies, one box per lane (the TMA unit takes boxes
+                        // one at a time, so each block's K and V go as one box each):
+                        // lanes 0 .. SB - 1 the K boxes, the next SB lanes the V boxes
+                        {
+                            const bool kl = lane < SB;
+                            const int ci = kl ? lane : lane - SB;
+                            int cid = __shfl_sync(0xffffffffu, ids, (bb + (ci & (SB - 1))) & 31);
+                            if ((unsigned)cid >= (unsigned)p.NB) cid = 0;   // flagged and poisoned above
+                            const int y = (cid * p.Hkv + it.kvh) * BS;
+                            const uint32_t dst = ring + st * Tr::STAGE_BYTES + (kl ? 0 : Tr::KV_BYTES) + ci * Tr::BLK_BYTES;
+                            if (ok && lane < 2 * SB && ci < nbs) {
+                                // each block is read once: L2 evict-first
+                                if (kl)
+                                    tma_load_4d_hint(dst, &tmap_k, 0, 0, 0, y / 8, full(st), kv_pol);
+                                else
+                                    tma_load_3d_hint(dst, &tmap_v, 0, y, 0, full(st), kv_pol);
                             }
                         }
-                    }
-                    seg_advance(it, len, p, tab);
-                }
-            }
-            if (lane == 0) {
-                // the end record, twice: each softmax stream takes every other stage
-                for (int e = 0; e < 2 && ok; ++e) {
-                    if (claim()) {
-                        recs[st].flags = TC_END;
-                        mbar_arrive(full(st));
                         ++j;
                         if (++st == R) {
                             st = 0;
                             ph ^= 1u;
                         }
-                    } else {
-                        ok = false;
                     }
                 }
-                if (!ok) {
-                    set_err(p.err, PA_DEVERR_TIMEOUT);
-                    *abort_flag = 1;
-                    // copies still in flight land before the CTA's shared memory is released
-                    for (int k = j - R > 0 ? j - R : 0; k < j; ++k)
-                        mbar_wait_bounded(full(k % R), (uint32_t)((k / R) & 1), p.timeout_ns);
-                    if (nseg > 0) mbar_wait_bounded(q_full, (uint32_t)((nseg - 1) & 1), p.timeout_ns);
-                }
+                seg_advance(it, len, p, tab);
             }
-            __syncwarp();
-        } else if (warp == Tr::MMA_WARP) {
-            // ================================================================ scores
-            // One thread issues S_j as soon as its inputs are ready: the copy of
-            // stage j, the scores of stage j - 2 read out of its TMEM buffer
-            // (s_free) and, at a segment start, the Q tile.  The PV products are
-            // issued by another thread (PV_WARP), so neither kind of MMA waits
-            // behind the other's inputs.  At the end record it publishes the
-            // number of stages.  No progress for the wait limit: abort.
-            if (lane == 0) {
-                int js = 0, nseg = 0;                        // next S, Q tiles consumed
-                int s_st = 0;                                // ring slot and phase of stage js
-                uint32_t s_ph = 0;
-                bool ok = true;
-                uint64_t t_last = global_timer_ns();
-                for (uint32_t spin = 0;; ++spin) {
-                    if (mbar_test_wait(full(s_st), s_ph)) {
-                        const int flags = recs[s_st].flags;
-                        if (flags & TC_END) {
-                            *n_stages = js;
-                            break;
-                        }
-                        if ((!(flags & TC_FIRST) || mbar_test_wait(q_full, (uint32_t)(nseg & 1))) &&
-                            (js < 2 || mbar_test_wait(s_free + 8 * (js & 1), (uint32_t)(((js - 2) >> 1) & 1)))) {
-                            const int b = js & 1;
-                            if (flags & TC_FIRST) ++nseg;
-                            tc_fence_after();
-                            const uint64_t qd = sdesc_sw128(q_tile, 16, 1024);
-                            const uint64_t kd = sdesc_sw128(ring + s_st * Tr::STAGE_BYTES, 16, Tr::GROUP_STRIDE);
-    #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {      // +32 bytes per K step; per 4: Q's next half tile,
-                                                                    // K's next 1024-byte atom (address >> 4)
-                                mma_f16(tmem + 64 * b, qd + (uint64_t)((k / 4) * (q_half >> 4) + (k % 4) * 2),
-                                        kd + (uint64_t)((k / 4) * (1024 >> 4) + (k % 4) * 2), IDESC_S,
-                                        k > 0 ? 1u : 0u);
-                            }
-                            mma_commit(s_full + 8 * b);
-                            if (flags & TC_LAST) mma_commit(q_empty);
-                            ++js;
-                            if (++s_st == R) {
-                                s_st = 0;
-                                s_ph ^= 1u;
-                            }
-                            t_last = global_timer_ns();
-                            continue;
-                        }
-                    }
-                    if ((spin & 63u) == 0 && (*abort_flag || global_timer_ns() - t_last > p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (!ok) {
-                    set_err(p.err, PA_DEVERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                // every MMA issued (by both threads) completes before tensor memory is released
-                mma_commit(fin);
-                mbar_wait_bounded(fin, 0, p.timeout_ns);
-            }
-            __syncwarp();
-        } else if (warp == Tr::PV_WARP) {
-            // ================================================================ PV
-            // One thread issues PV_j in stage order once P_j is written and, at a
-            // segment start, the previous segment's output has been read; the
-            // commit frees the stage's ring slot.  It stops at the number of
-            // stages the score thread publishes.
-            if (lane == 0) {
-                int jp = 0, pv_seg = 0;
-                bool ok = true;
-                while (true) {
-                    const int b = jp & 1;
-                    bool ready = false;
-                    const uint64_t t0 = global_timer_ns();
-                    for (uint32_t spin = 0;; ++spin) {
-                        if (jp >= *n_stages) break;
-                        if (mbar_test_wait(p_full + 8 * b, (uint32_t)((jp >> 1) & 1))) {
-                            ready = true;
-                            break;
-                        }
-                        if ((spin & 63u) == 0 && (*abort_flag || global_timer_ns() - t0 > p.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    if (!ready) break;
-                    const int st = jp % R;
-                    const bool first = (recs[st].flags & TC_FIRST) != 0;
-                    // a segment's first PV overwrites O: the previous segment's output must have been read
-                    if (first && pv_seg > 0 && !mbar_wait_bounded(o_free, (uint32_t)((pv_seg - 1) & 1), p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (first) ++pv_seg;
-                    tc_fence_after();
-                    const uint32_t pt = tmem + Tr::P_COL + 64 * b;
-                    const uint32_t vbase = ring + st * Tr::STAGE_BYTES + Tr::KV_BYTES;
-    #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k) {
-                        // keys 16 k .. 16 k + 15: rows (16 k) % BS .. of block tile (16 k) / BS
-                        const uint64_t bv = sdesc_sw128(vbase + ((16 * k) / BS) * Tr::BLK_BYTES + ((16 * k) % BS) * 128,
-                                                        Tr::HALF_STRIDE, 1024);
-                        mma_f16_ts(tmem + Tr::O_COL, pt + 8 * k, bv, IDESC_O, (first && k == 0) ? 0u : 1u);
-                        mma_f16_ts(tmem + Tr::O_COL, pt + 32 + 8 * k, bv, IDESC_O, 1u);
-                    }
-                    mma_commit(pv_done + 8 * b);
-                    mma_commit(empty(st));
-                    ++jp;
-                }
-                if (!ok) {
-                    set_err(p.err, PA_DEVERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                mma_commit(fin);
-            }
-            __syncwarp();
         }
+        if (lane == 0) {
+            // the end record, twice: each softmax stream takes every other stage
+            for (int e = 0; e < 2 && ok; ++e) {
+                if (claim()) {
+                    recs[st].flags = TC_END;
+                    mbar_arrive(full(st));
+                    ++j;
+                    if (++st == R) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                } else {
+                    ok = false;
+                }
+            }
+            if (!ok) {
+                set_err(p.err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                // copies still in flight land before the CTA's shared memory is released
+                for (int k = j - R > 0 ? j - R : 0; k < j; ++k)
+                    mbar_wait_bounded(full(k % R), (uint32_t)((k / R) & 1), p.timeout_ns);
+                if (nseg > 0) mbar_wait_bounded(q_full, (uint32_t)((nseg - 1) & 1), p.timeout_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == Tr::MMA_WARP) {
+        // ================================================================ scores
+        // One thread issues S_j as soon as its inputs are ready: the copy of
+        // stage j, the scores of stage j - 2 read out of its TMEM buffer
+        // (s_free) and, at a segment start, the Q tile.  The PV products are
+        // issued by another thread (PV_WARP), so neither kind of MMA waits
+        // behind the other's inputs.  At the end record it publishes the
+        // number of stages.  No progress for the wait limit: abort.
+        if (lane == 0) {
+            int js = 0, nseg = 0;                        // next S, Q tiles consumed
+            int s_st = 0;                                // ring slot and phase of stage js
+            uint32_t s_ph = 0;
+            bool ok = true;
+            uint64_t t_last = global_timer_ns();
+            for (uint32_t spin = 0;; ++spin) {
+                if (mbar_test_wait(full(s_st), s_ph)) {
+                    const int flags = recs[s_st].flags;
+                    if (flags & TC_END) {
+                        *n_stages = js;
+                        break;
+                    }
+                    if ((!(flags & TC_FIRST) || mbar_test_wait(q_full, (uint32_t)(nseg & 1))) &&
+                        (js < 2 || mbar_test_wait(s_free + 8 * (js & 1), (uint32_t)(((js - 2) >> 1) & 1)))) {
+                        const int b = js & 1;
+                        if (flags & TC_FIRST) ++nseg;
+                        tc_fence_after();
+                        const uint64_t qd = sdesc_sw128(q_tile, 16, 1024);
+                        const uint64_t kd = sdesc_sw128(ring + s_st * Tr::STAGE_BYTES, 16, Tr::GROUP_STRIDE);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {      // +32 bytes per K step; per 4: Q's next half tile,
+                                                                // K's next 1024-byte atom (address >> 4)
+                            mma_f16(tmem + 64 * b, qd + (uint64_t)((k / 4) * (q_half >> 4) + (k % 4) * 2),
+                                    kd + (uint64_t)((k / 4) * (1024 >> 4) + (k % 4) * 2), IDESC_S,
+                                    k > 0 ? 1u : 0u);
+                        }
+                        mma_commit(s_full + 8 * b);
+                        if (flags & TC_LAST) mma_commit(q_empty);
+                        ++js;
+                        if (++s_st == R) {
+                            s_st = 0;
+                            s_ph ^= 1u;
+                        }
+                        t_last = global_timer_ns();
+                        continue;
+                    }
+                }
+                if ((spin & 63u) == 0 && (*abort_flag || global_timer_ns() - t_last > p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) {
+                set_err(p.err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA issued (by both threads) completes before tensor memory is released
+            mma_commit(fin);
+            mbar_wait_bounded(fin, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == Tr::PV_WARP) {
+        // ================================================================ PV
+        // One thread issues PV_j in stage order once P_j is written and, at a
+        // segment start, the previous segment's output has been read; the
+        // commit frees the stage's ring slot.  It stops at the number of
+        // stages the score thread publishes.
+        if (lane == 0) {
+            int jp = 0, pv_seg = 0;
+            bool ok = true;
+            while (true) {
+                const int b = jp & 1;
+                bool ready = false;
+                const uint64_t t0 = global_timer_ns();
+                for (uint32_t spin = 0;; ++spin) {
+                    if (jp >= *n_stages) break;
+                    if (mbar_test_wait(p_full + 8 * b, (uint32_t)((jp >> 1) & 1))) {
+                        ready = true;
+                        break;
+                    }
+                    if ((spin & 63u) == 0 && (*abort_flag || global_timer_ns() - t0 > p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!ready) break;
+                const int st = jp % R;
+                const bool first = (recs[st].flags & TC_FIRST) != 0;
+                // a segment's first PV overwrites O: the previous segment's output must have been read
+                if (first && pv_seg > 0 && !mbar_wait_bounded(o_free, (uint32_t)((pv_seg - 1) & 1), p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (first) ++pv_seg;
+                tc_fence_after();
+                const uint32_t pt = tmem + Tr::P_COL + 64 * b;
+                const uint32_t vbase = ring + st * Tr::STAGE_BYTES + Tr::KV_BYTES;
+#pragma unroll
+                for (int k = 0; k < KEYS / 16; ++k) {
+                    // keys 16 k .. 16 k + 15: rows (16 k) % BS .. of block tile (16 k) / BS
+                    const uint64_t bv = sdesc_sw128(vbase + ((16 * k) / BS) * Tr::BLK_BYTES + ((16 * k) % BS) * 128,
+                                                    Tr::HALF_STRIDE, 1024);
+                    mma_f16_ts(tmem + Tr::O_COL, pt + 8 * k, bv, IDESC_O, (first && k == 0) ? 0u : 1u);
+                    mma_f16_ts(tmem + Tr::O_COL, pt + 32 + 8 * k, bv, IDESC_O, 1u);
+                }
+                mma_commit(pv_done + 8 * b);
+                mma_commit(empty(st));
+                ++jp;
+            }
+            if (!ok) {
+                set_err(p.err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            mma_commit(fin);
+        }
+        __syncwarp();
     } else {
-        if constexpr (Tr::TREE) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ================================================================ softmax
         // Warp w takes rows 32 (w % 4) .. + 31 (its TMEM lane quarter; thread =
         // query row) of every other stage: stream w / 4 takes the stages of its
@@ -570,13 +522,6 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         float m_mine = -INFINITY, l = 0.f;                      // reference of this stream's sum, the sum
         int pois = 0, lim = -1, cur_seg = -1, seg_kvh = 0, seg_q0 = 0;
         bool wact = false, ok = true;
-        // trees: the nodes this row sees (a row of no node looks at every key, so that
-        // it never takes its warp off the unmasked path; its results go nowhere)
-        uint64_t sees = 0;
-        bool alive = false;
-        uint32_t scan_ph = 0;
-        const bool flip = !(p.scale_log2 > 0.f);
-        const float scale = flip ? 1.f : p.scale_log2;
         while (true) {
             if (*abort_flag) break;
             if (!wait_all(full(st), ph)) {
@@ -595,11 +540,6 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 l = 0.f;
                 pois = 0;
                 lim = r < n * G ? ctx - n + r / G : -1;
-                if constexpr (Tr::TREE) {
-                    alive = r < n * G;
-                    lim = alive ? 0 : -1;
-                    sees = alive ? node_bits(__ldg(mp.tree_masks + seg_q0 + r / G), ctx - recs[st].base) : 0;
-                }
                 wact = __any_sync(0xffffffffu, lim >= 0);
             }
             pois |= recs[st].poison;
@@ -613,44 +553,6 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (!p_free) p_free = wait_all(pv_done + 8 * b, (uint32_t)(((j - 2) >> 1) & 1));
                 return p_free;
             };
-            uint64_t spoilt = 0;
-            if constexpr (Tr::TREE) {
-                // Nodes whose V holds an infinity or NaN: a weight of 0 would still spoil
-                // the rows that do not see them, so their V leaves the product, and the
-                // rows that do see them become NaN.  The stream's warps share the look
-                // (while the scores are computed) and meet at a barrier before acting.
-                const int from = max(0, recs[st].base - t0), held = min(nkeys, ctx - t0);
-                if (from < held) {
-                    uint8_t* vt = smem + ring_off + st * Tr::STAGE_BYTES + Tr::KV_BYTES;
-                    auto part_of = [&](int i) -> uint4* {
-                        const int key = i / (HALVES * 8), part = i % (HALVES * 8);
-                        return reinterpret_cast<uint4*>(vt + (key / BS) * Tr::BLK_BYTES + (part / 8) * Tr::HALF_STRIDE +
-                                                        (key % BS) * 128 + (part % 8) * 16);
-                    };
-                    uint64_t mine = 0;
-                    for (int i = from * HALVES * 8 + stid; i < held * HALVES * 8; i += 128)
-                        if (vec_not_finite<Tr::BF16>(*part_of(i))) mine |= 1ull << (i / (HALVES * 8));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t bits = __reduce_or_sync(0xffffffffu, (uint32_t)(mine >> (32 * h)));
-                        if (lane == 0 && bits) atomicOr(&recs[st].spoilt[h], bits);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(scanned + 8 * stream);
-                    if (!wait_all(scanned + 8 * stream, scan_ph)) {
-                        ok = false;
-                        break;
-                    }
-                    scan_ph ^= 1u;
-                    const volatile uint32_t* words = recs[st].spoilt;
-                    spoilt = (uint64_t)words[0] | ((uint64_t)words[1] << 32);
-                    if (spoilt) {                            // uniform over the stream
-                        for (int i = from * HALVES * 8 + stid; i < held * HALVES * 8; i += 128)
-                            if ((spoilt >> (i / (HALVES * 8))) & 1) *part_of(i) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                    }
-                }
-            }
             if (!wait_all(s_full + 8 * b, (uint32_t)((j >> 1) & 1))) {
                 ok = false;
                 break;
@@ -672,45 +574,22 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free + 8 * b);
             if (wact) {
-                uint64_t set = ~0ull;                              // trees: the keys that this row sees here
-                float mx;
-                if constexpr (Tr::TREE) {
-                    // the scores stay as they are (the scale joins the exponent's FMA), unless a
-                    // scale turns their order
-                    if (flip)
+                const int kv = min(nkeys, max(0, lim - t0 + 1));   // keys this row sees here
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (__all_sync(0xffffffffu, kv >= KEYS)) {
 #pragma unroll
-                        for (int k = 0; k < KEYS; ++k) x[k] *= p.scale_log2;
-                    if (alive)   // t0 < ctx <= base + 64, so the offset is in range
-                        set = tree_visible(sees, recs[st].base - t0) & (nkeys < KEYS ? (1ull << nkeys) - 1 : ~0ull);
-                    if (!__all_sync(0xffffffffu, set == ~0ull)) {
-#pragma unroll
-                        for (int k = 0; k < KEYS; ++k)
-                            if (!(((k < 32 ? (uint32_t)set : (uint32_t)(set >> 32)) >> (k & 31)) & 1u)) x[k] = -INFINITY;
+                    for (int k = 0; k < KEYS; ++k) {
+                        x[k] *= p.scale_log2;
+                        m4[k & 3] = fmaxf(m4[k & 3], x[k]);
                     }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < KEYS; k += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], x[k + i]), x[k + 4 + i]);
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
                 } else {
-                    const int kv = min(nkeys, max(0, lim - t0 + 1));   // keys this row sees here
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (__all_sync(0xffffffffu, kv >= KEYS)) {
 #pragma unroll
-                        for (int k = 0; k < KEYS; ++k) {
-                            x[k] *= p.scale_log2;
-                            m4[k & 3] = fmaxf(m4[k & 3], x[k]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < KEYS; ++k) {
-                            x[k] = k < kv ? x[k] * p.scale_log2 : -INFINITY;
-                            m4[k & 3] = fmaxf(m4[k & 3], x[k]);
-                        }
+                    for (int k = 0; k < KEYS; ++k) {
+                        x[k] = k < kv ? x[k] * p.scale_log2 : -INFINITY;
+                        m4[k & 3] = fmaxf(m4[k & 3], x[k]);
                     }
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // the reference after the previous stage of the segment (other stream)
                 float m_prev = -INFINITY;
                 if (!(flags & TC_FIRST) && !get_all(ref_cell + (j & 3) * Tr::ROWS + r, (uint32_t)j, m_prev)) {
@@ -722,7 +601,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     m_mine = m_prev;
                 }
                 const float m_new = fmaxf(m_prev, mx);
-                const bool need = m_new > m_prev + Tr::TAU && (!Tr::TREE || alive);
+                const bool need = m_new > m_prev + Tr::TAU;
                 if (need) m_mine = m_new;
                 if (!(flags & TC_LAST)) xch_put(ref_cell + ((j + 1) & 3) * Tr::ROWS + r, m_mine, (uint32_t)(j + 1));
                 const float alpha = need ? ex2(m_prev - m_new) : 1.f;      // m_prev = -inf: 0
@@ -734,7 +613,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         break;
                     }
                     tc_fence_after();
-#pragma unroll (Tr::TREE ? 1 : D / 32)
+#pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t u[32];
                         tmem_ld32(o_addr + 32 * c, u);
@@ -751,37 +630,20 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     break;
                 }
                 float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                f32x2 sum2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {            // 32 keys at a time: hi, lo columns 16 c ..
                     uint32_t hw[16], lw[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float p0, p1;
-                        if constexpr (Tr::TREE) {                // packed: this code has to fit the instruction cache
-                            split2(fma2(pair2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), pair2(scale, scale),
-                                        pair2(-mref, -mref)), p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            sum2[e & 1] = add2(sum2[e & 1], pair2(p0, p1));
-                        } else {
-                            p0 = ex2(x[32 * c + 2 * e] - mref);
-                            p1 = ex2(x[32 * c + 2 * e + 1] - mref);
-                            s4[e & 3] += p0 + p1;
-                        }
+                        const float p0 = ex2(x[32 * c + 2 * e] - mref), p1 = ex2(x[32 * c + 2 * e + 1] - mref);
+                        s4[e & 3] += p0 + p1;
                         if constexpr (Tr::BF16) {
                             // hi: the weights cut to bf16 (their top 16 bits); lo: the exact
                             // remainders, cut the same way (relative error < 2^-14 in all)
                             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                             hw[e] = __byte_perm(u0, u1, 0x7632);
-                            float r0, r1;
-                            if constexpr (Tr::TREE) {
-                                split2(add2(pair2(p0, p1), pair2(-__uint_as_float(u0 & 0xffff0000u),
-                                                                 -__uint_as_float(u1 & 0xffff0000u))), r0, r1);
-                            } else {
-                                r0 = p0 - __uint_as_float(u0 & 0xffff0000u);
-                                r1 = p1 - __uint_as_float(u1 & 0xffff0000u);
-                            }
+                            const float r0 = p0 - __uint_as_float(u0 & 0xffff0000u);
+                            const float r1 = p1 - __uint_as_float(u1 & 0xffff0000u);
                             lw[e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
                         } else {
                             const uint32_t hv = pack2<false>(p0, p1);
@@ -792,13 +654,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     tmem_st16(lane_addr + Tr::P_COL + 64 * b + 16 * c, hw);
                     tmem_st16(lane_addr + Tr::P_COL + 64 * b + 32 + 16 * c, lw);
                 }
-                if constexpr (Tr::TREE) {
-                    split2(add2(sum2[0], sum2[1]), s4[0], s4[1]);
-                    l += s4[0] + s4[1];
-                    if (spoilt & set) l = qnan;
-                } else {
-                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                }
+                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             }
             // V rows past the context or past the blocks copied are zero for the PV product
             const int vvalid = max(0, min(nkeys, ctx - t0));
@@ -845,8 +701,8 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const bool live = lim >= 0;
                     if (flags & TC_COMPLETE) {
                         uint16_t* orow = p.out + ((size_t)(seg_q0 + r / G) * p.Hq + (size_t)seg_kvh * G + r % G) * D;
-                        const float inv = Tr::TREE && L == 0.f ? 0.f : 1.f / L;   // a node that sees no key: zero
-#pragma unroll (Tr::TREE ? 1 : D / 32)
+                        const float inv = 1.f / L;
+#pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t u[32];
                             tmem_ld32(o_addr + 32 * c, u);
@@ -869,7 +725,7 @@ pa_multi_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         float* prow = p.partials +
                                       (((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS + r) *
                                           Tr::PSTRIDE;
-#pragma unroll (Tr::TREE ? 1 : D / 32)
+#pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t u[32];
                             tmem_ld32(o_addr + 32 * c, u);
@@ -936,8 +792,5 @@ void multi_tc_table_bf16_d128(MultiKernelInfo (&t)[2]);
 void multi_tc_table_bf16_d64(MultiKernelInfo (&t)[2]);
 void multi_tc_table_fp16_d128(MultiKernelInfo (&t)[2]);
 void multi_tc_table_fp16_d64(MultiKernelInfo (&t)[2]);
-// Drafted trees: [d == 128][bs == 32], defined in tree_*.cu.
-void tree_tc_table_bf16(MultiKernelInfo (&t)[2][2]);
-void tree_tc_table_fp16(MultiKernelInfo (&t)[2][2]);
 
 }  // namespace pa

@@ -17,6 +17,7 @@
 #include "prefix_kernel.cuh"
 #include "rope_ops.cuh"
 #include "tree_ops.cuh"
+#include "tree_tc_kernel.cuh"
 #include "tree_wide_kernel.cuh"
 
 namespace {

@@ -25,8 +25,8 @@
 // unrolled, the masks among them and both tiles in step it took 0.92 ms; 0.90 with
 // the weights handed over by the quarter and the wait for the next keys before the
 // one for the products, 0.86 with rolled loops, 0.82 with the tiles apart, 0.77 with
-// masks and signs out of the loops.  16 softmax warps, two to a row, took 1.11 ms
-// unrolled.  The products' issue stays unrolled: rolled, an MMA takes 130 cycles to
+// masks and signs out of the loops.  16 softmax warps, two to a row, took 0.89 ms
+// (unrolled 1.11).  The products' issue stays unrolled: rolled, an MMA takes 130 cycles to
 // issue instead of 64.
 //
 // Tensor memory (512 columns): S_0, S_1 at 0 and 128, O_0, O_1 at 256 and 384.  P_t
