@@ -14,7 +14,7 @@
 // What bounds it: each tile's chain of scores, softmax and products, and the tensor
 // core.  A stage costs 2 * (1 + 2) * 512 cycles of MMA at head_dim 128 (the PV
 // product runs twice, hi and lo) for 64 KB of keys and values, which HBM delivers in
-// about 2800; it takes about 5400.  Two tiles share each copied stage, so the keys
+// about 2800; it takes about 5000.  Two tiles share each copied stage, so the keys
 // are read once per 256 rows, and tile 1 follows tile 0 by its score product, so that
 // one tile's softmax runs beside the other's products.  N = 128 because an MMA of
 // N = 64 takes as long.
