@@ -650,14 +650,14 @@ pa_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_con
                         p1 = ex2(p1);
                         sum2[e & 1] = add2(sum2[e & 1], pair2(p0, p1));
                         if constexpr (Tr::BF16) {
-                            // hi: the weights cut to bf16; lo: the exact remainders, cut the same way
-                            // (relative error < 2^-14 in all)
+                            // hi: the weights cut to bf16; lo: the exact remainders, rounded to nearest
+                            // (2^-16 of a weight in all, to either side)
                             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                             w[e] = __byte_perm(u0, u1, 0x7632);
                             float r0, r1;
                             split2(add2(pair2(p0, p1), pair2(-__uint_as_float(u0 & 0xffff0000u),
                                                              -__uint_as_float(u1 & 0xffff0000u))), r0, r1);
-                            w[16 + e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+                            w[16 + e] = pack2<true>(r0, r1);
                         } else {
                             const uint32_t hv = pack2<false>(p0, p1);
                             w[e] = hv;
