@@ -214,8 +214,10 @@ int64_t token_stride(PyObject* o, at::ScalarType t, int dev, int64_t T, int64_t 
     const at::Tensor& x = THPVariable_Unpack(o);
     if (!x.is_cuda() || x.get_device() != dev || x.scalar_type() != t || !is_shape(x, {T, H, d})) return -1;
     out = &x;
-    if (T <= 1) return H * d;
-    return x.stride(2) == 1 && (x.stride(1) == d || H == 1) && x.stride(0) >= H * d ? x.stride(0) : -1;
+    if (T == 0) return H * d;                          // nothing is read
+    if (x.stride(2) != 1 || (x.stride(1) != d && H > 1)) return -1;
+    if (T == 1) return H * d;                          // a single token's own stride is never used
+    return x.stride(0) >= H * d ? x.stride(0) : -1;
 }
 
 // (q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, inv_freq, interleaved, rope_scale, q_weight, k_weight,

@@ -506,10 +506,12 @@ def _token_rows(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     T, H, d = shape
     st, sh, sd = t.stride()
-    if T <= 1:
-        return H * d                                    # a single token's stride is never used
+    if T == 0:
+        return H * d                                    # nothing is read
     if sd != 1 or (sh != d and H > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
+    if T == 1:
+        return H * d                                    # a single token's own stride is never used
     if st < H * d:
         raise ValueError(f"{name}: tokens must not overlap")
     return st

@@ -1,0 +1,57 @@
+"""The tree-speculation calls on the device: strides of single tokens through
+both host sides."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle.kv_ops import bits
+from tests.gpu_util import need_gpu
+from tests.test_tree_calls import strided_views
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def pa():
+    import paged_kv_cache_254_gb300 as m
+    return m
+
+
+# ---------------------------------------------------------------- one token's strides
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("view", ["interleaved", "expanded", "sliced", "half", "transposed"])
+@pytest.mark.parametrize("arg", ["q", "k_new", "v_new"])
+def test_scattered_heads_are_refused(T, view, arg):
+    from paged_kv_cache_254_gb300 import ops
+    H, d = 4, 64
+    freq, _ = pa().rope_inv_freq(d)
+    dense = torch.ones(T, H, d, dtype=torch.bfloat16, device="cuda")
+    pools = [torch.zeros(4, H, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    a = dict(q=dense, k_new=dense, v_new=dense, positions=torch.zeros(T, dtype=torch.int32, device="cuda"),
+             slot_mapping=torch.arange(T, device="cuda"), k_pool=pools[0], v_pool=pools[1], inv_freq=freq)
+    a[arg] = strided_views(T, H, d, "cuda")[view]
+    with pytest.raises(ValueError, match="contiguous"):
+        pa().pa_rope_append_kv(**a)
+    rest = (False, 1.0, None, None, 1e-6, None, None)
+    assert ops._load_fast().rope_append_kv(*a.values(), *rest) is NotImplemented
+    torch.cuda.synchronize()
+    assert not bits(pools[0]).any() and not bits(pools[1]).any()
+
+
+def test_one_token_of_a_fused_projection():
+    # one row of [q | k | v], whose parts are dense within the token: as before
+    H, d = 4, 64
+    freq, _ = pa().rope_inv_freq(d)
+    row = torch.randn(1, 3 * H * d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    q, k, v = (x.unflatten(1, (H, d)) for x in row.split(H * d, 1))
+    pools = [torch.zeros(4, H, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    pos, slot = torch.full((1,), 9, dtype=torch.int32, device="cuda"), torch.full((1,), 21, device="cuda")
+    a = pa().pa_rope_append_kv(q, k, v, pos, slot, pools[0], pools[1], freq)
+    b = pa().pa_rope_append_kv(*(x.contiguous() for x in (q, k, v)), pos, slot, pools[2], pools[3], freq)
+    assert torch.equal(a, b) and np.array_equal(bits(pools[0]), bits(pools[2]))
+    assert torch.equal(pools[1][1, :, 5], v[0])
