@@ -328,13 +328,14 @@ _tree_bytes = {}
 
 
 def _tree_workspace(dev, shape, max_nodes):
-    # the size depends on these and the device's SM count alone
+    # the size of a valid shape's workspace depends on these and the device's SM count alone
     key = (dev, max_nodes, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim, shape.block_size,
            shape.dtype)
     need = _tree_bytes.get(key)
     if need is None:
         need = int(_call(_lib.load().pa_decode_tree_workspace_bytes, dev, shape, max_nodes))
-        _tree_bytes[key] = need          # 0: an invalid shape or tree size, which the call reports
+        if need:                         # 0: something about the shape is invalid, which the call reports
+            _tree_bytes[key] = need
     if need == 0 or torch.cuda.is_current_stream_capturing():
         # a captured call keeps a workspace of its graph's own: the shared one may be
         # replaced by a larger one, and another graph may run beside this one

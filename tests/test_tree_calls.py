@@ -1,9 +1,12 @@
-"""Host side of the tree-speculation calls, on the CPU: strides of single tokens."""
+"""Host side of the tree-speculation calls, on the CPU: strides of single
+tokens, and sizes of workspaces."""
+
+import types
 
 import pytest
 import torch
 
-from paged_kv_cache_254_gb300 import ops
+from paged_kv_cache_254_gb300 import _lib, ops
 
 
 def strided_views(T, H, d, device="cpu"):
@@ -31,3 +34,20 @@ def test_token_strides_that_are_fine():
     assert ops._token_rows("q", q[:0], torch.bfloat16, (0, 4, 16), -1) == 64
     one_head = rows.unflatten(1, (7, 16))[:, 3:4]
     assert ops._token_rows("k", one_head, torch.bfloat16, (5, 1, 16), -1) == 112
+
+
+# ---------------------------------------------------------------- workspaces
+def test_a_refused_shape_leaves_no_size_behind(monkeypatch):
+    # the library answers 0 for a shape that it refuses; a valid one that differs from it in a field
+    # that the size does not depend on still gets its own
+    fake = types.SimpleNamespace(pa_decode_tree_workspace_bytes=lambda s, p: 4096 if s.max_blocks_per_seq > 0 else 0)
+    monkeypatch.setattr(_lib, "load", lambda: fake)
+    monkeypatch.setattr(ops, "_call", lambda fn, dev, *a: fn(*a))
+    monkeypatch.setattr(ops, "_tree_bytes", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    sizes = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: sizes.append(a[0]) or empty(*a))
+    for mb, want in ((0, 0), (9, 4096), (0, 4096), (9, 4096)):
+        ops._tree_workspace(0, _lib.PaShape(2, 8, 2, 128, 16, 64, mb, _lib.PA_BF16), 8)
+        assert sizes[-1] == want

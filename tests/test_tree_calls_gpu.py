@@ -1,5 +1,5 @@
 """The tree-speculation calls on the device: strides of single tokens through
-both host sides."""
+both host sides, and calls after a refused one."""
 
 import numpy as np
 import pytest
@@ -55,3 +55,32 @@ def test_one_token_of_a_fused_projection():
     b = pa().pa_rope_append_kv(*(x.contiguous() for x in (q, k, v)), pos, slot, pools[2], pools[3], freq)
     assert torch.equal(a, b) and np.array_equal(bits(pools[0]), bits(pools[2]))
     assert torch.equal(pools[1][1, :, 5], v[0])
+
+
+# ---------------------------------------------------------------- workspaces
+def small_tree(N=2, nodes=5, Hq=8, Hkv=2, d=64, B=16, MB=4, seed=7):
+    """Arguments of a pa_decode_tree call: contexts of 3 blocks and a bit, chains of ``nodes``."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    values = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+    table = torch.randperm(N * MB, device="cuda", generator=g).int().view(N, MB)
+    masks = torch.tensor([(2 << i) - 1 for i in range(nodes)] * N, device="cuda")
+    return dict(q=values(N * nodes, Hq, d), k_pool=values(N * MB, Hkv, B, d), v_pool=values(N * MB, Hkv, B, d),
+                block_tables=table, context_lens=torch.full((N,), 3 * B + 2, dtype=torch.int32, device="cuda"),
+                q_start=torch.arange(0, N * nodes + 1, nodes, dtype=torch.int32, device="cuda"), tree_masks=masks,
+                scale=d ** -0.5, max_nodes=nodes)
+
+
+def test_a_valid_call_after_a_refused_one():
+    a = small_tree(N=3, nodes=7)                       # sizes that no other test has
+    with pytest.raises(pa().PagedAttentionError):
+        pa().pa_decode_tree(**{**a, "block_tables": a["block_tables"][:, :0].contiguous()})
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        captured = pa().pa_decode_tree(**a)
+    graph.replay()
+    torch.cuda.synchronize()
+    eager = pa().pa_decode_tree(**a, stream=torch.cuda.Stream())     # no workspace kept for this one
+    torch.cuda.synchronize()
+    assert torch.isfinite(eager.float()).all() and torch.equal(captured, eager)
