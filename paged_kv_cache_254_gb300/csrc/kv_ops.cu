@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "kv_ops.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "../../include/pa.h"
 #include <cuda_fp16.h>
@@ -234,9 +235,8 @@ cudaError_t append4_launch(const void* k_new, const void* v_new, const int64_t* 
     auto kn = static_cast<const uint16_t*>(k_new);
     auto vn = static_cast<const uint16_t*>(v_new);
     auto kv = static_cast<uint8_t*>(kv_pool);
-    if (bf16) pa_append4_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-    else pa_append4_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-    return cudaGetLastError();
+    return launch(bf16 ? pa_append4_kernel<true> : pa_append4_kernel<false>, (unsigned)blocks, 256, 0, stream, kn, vn,
+                  slots, kv, a);
 }
 
 cudaError_t append8_launch(const void* k_new, const void* v_new, const int64_t* slots, void* kv_pool,
@@ -249,14 +249,9 @@ cudaError_t append8_launch(const void* k_new, const void* v_new, const int64_t* 
     auto kn = static_cast<const uint16_t*>(k_new);
     auto vn = static_cast<const uint16_t*>(v_new);
     auto kv = static_cast<uint8_t*>(kv_pool);
-    if (bf16) {
-        if (e5m2) pa_append8_kernel<true, true><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-        else pa_append8_kernel<true, false><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-    } else {
-        if (e5m2) pa_append8_kernel<false, true><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-        else pa_append8_kernel<false, false><<<(unsigned)blocks, 256, 0, stream>>>(kn, vn, slots, kv, a);
-    }
-    return cudaGetLastError();
+    const auto kernel = bf16 ? (e5m2 ? pa_append8_kernel<true, true> : pa_append8_kernel<true, false>)
+                             : (e5m2 ? pa_append8_kernel<false, true> : pa_append8_kernel<false, false>);
+    return launch(kernel, (unsigned)blocks, 256, 0, stream, kn, vn, slots, kv, a);
 }
 
 cudaError_t append_launch(const void* k_new, const void* v_new, const int64_t* slots, void* k_pool,
@@ -266,10 +261,8 @@ cudaError_t append_launch(const void* k_new, const void* v_new, const int64_t* s
     const long long cap = (long long)sms * 8;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
-    pa_append_kernel<<<(unsigned)blocks, 256, 0, stream>>>(
-        static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slots,
-        static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), a);
-    return cudaGetLastError();
+    return launch(pa_append_kernel, (unsigned)blocks, 256, 0, stream, static_cast<const uint4*>(k_new),
+                  static_cast<const uint4*>(v_new), slots, static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), a);
 }
 
 cudaError_t copy_launch(const int32_t* pairs, void* k_pool, void* v_pool, const CopyArgs& a,
@@ -281,9 +274,8 @@ cudaError_t copy_launch(const int32_t* pairs, void* k_pool, void* v_pool, const 
     const long long cap = (long long)sms * 16;
     if (gx * gy > cap) gy = cap / gx > 0 ? cap / gx : 1;
     if (gy > 65535) gy = 65535;
-    pa_copy_kernel<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, stream>>>(
-        pairs, static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), a);
-    return cudaGetLastError();
+    return launch(pa_copy_kernel, dim3((unsigned)gx, (unsigned)gy), 256, 0, stream, pairs, static_cast<uint4*>(k_pool),
+                  static_cast<uint4*>(v_pool), a);
 }
 
 }  // namespace pa

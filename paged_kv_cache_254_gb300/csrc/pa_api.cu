@@ -12,6 +12,7 @@
 #include "../../include/pa.h"
 #include "decode_kernel.cuh"
 #include "kv_ops.cuh"
+#include "launch.cuh"
 #include "multi_kernel.cuh"
 #include "multi_tc_kernel.cuh"
 #include "prefix_kernel.cuh"
@@ -208,10 +209,9 @@ pa_status run_decode(const DecodeKernelInfo* k, int ctas, DecodeLaunch& L, const
     L.p.stall_ns = g_stall_ns.load(std::memory_order_relaxed);
     L.grid = ctas;
     L.bf16 = s->dtype == PA_BF16;
-    pa_decode_prepass<<<1, 1024, 0, L.stream>>>(L.p.context_lens, first_blocks, s->num_seqs,
-                                                s->max_blocks_per_seq, s->block_size, L.p.chunk_ctr, 1,
-                                                const_cast<long long*>(L.p.cum));
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    if (launch(pa_decode_prepass, 1, 1024, 0, L.stream, L.p.context_lens, first_blocks, s->num_seqs,
+               s->max_blocks_per_seq, s->block_size, L.p.chunk_ctr, 1ll, const_cast<long long*>(L.p.cum)) != cudaSuccess)
+        return PA_ERR_CUDA;
     if (k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
     const int g = s->num_q_heads / s->num_kv_heads;
     const cudaError_t e = s->head_dim == 128 ? merge_launch<128>(L, g, workers, L.stream)
@@ -917,10 +917,10 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
     L.p.q_box = q_box;
     L.stream = static_cast<cudaStream_t>(stream);
     L.grid = ctas;
-    pa_decode_prepass<<<1, 1024, 0, L.stream>>>(context_lens, nullptr, shape->num_seqs,
-                                                shape->max_blocks_per_seq, shape->block_size, d.chunk_ctr, 1,
-                                                const_cast<long long*>(d.cum));
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    if (launch(pa_decode_prepass, 1, 1024, 0, L.stream, context_lens, static_cast<const int32_t*>(nullptr),
+               shape->num_seqs, shape->max_blocks_per_seq, shape->block_size, d.chunk_ctr, 1ll,
+               const_cast<long long*>(d.cum)) != cudaSuccess)
+        return PA_ERR_CUDA;
     if (k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
     const int g = shape->num_q_heads / shape->num_kv_heads;
     if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
@@ -936,7 +936,7 @@ pa_status pa_decode_multi(const pa_shape* shape, int32_t max_q_len, int32_t tota
                                      g, k->rows, ctas, max_q_len, total_q, bf);
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return PA_OK;
 }
 
 
@@ -1039,7 +1039,7 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
                                plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes, splits) != cudaSuccess)
             return PA_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return PA_OK;
 }
 
 pa_status pa_tree_verify(int32_t num_seqs, int32_t max_nodes, int32_t total_q, const int32_t* q_start,

@@ -26,6 +26,7 @@
 #pragma once
 
 #include "decode_common.cuh"
+#include "launch.cuh"
 
 namespace pa {
 
@@ -586,8 +587,7 @@ struct PrefixKernelInfo {
 
 template <class Tr>
 cudaError_t prefix_launch(const PrefixLaunch& L) {
-    pa_prefix_kernel<Tr><<<L.grid, Tr::THREADS, Tr::SMEM_BYTES, L.stream>>>(*L.tmap_k, *L.tmap_v, L.p);
-    return cudaGetLastError();
+    return launch(pa_prefix_kernel<Tr>, L.grid, Tr::THREADS, Tr::SMEM_BYTES, L.stream, *L.tmap_k, *L.tmap_v, L.p);
 }
 
 template <class Tr>

@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include "decode_common.cuh"
+#include "launch.cuh"
 #include "packed.cuh"
 #include "ptx.cuh"
 #include "../../include/pa.h"
@@ -319,9 +320,8 @@ pa_rope_append_kernel(const RopeArgs a) {
 
 template <bool BF16, int LPR>
 cudaError_t rope_append_run(const RopeArgs& a, unsigned blocks, cudaStream_t stream) {
-    if (a.interleaved) pa_rope_append_kernel<BF16, LPR, true><<<blocks, 32 * WARPS, 0, stream>>>(a);
-    else pa_rope_append_kernel<BF16, LPR, false><<<blocks, 32 * WARPS, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch(a.interleaved ? pa_rope_append_kernel<BF16, LPR, true> : pa_rope_append_kernel<BF16, LPR, false>,
+                  blocks, 32 * WARPS, 0, stream, a);
 }
 
 cudaError_t rope_append_launch(RopeArgs a, bool bf16, cudaStream_t stream, int sms) {

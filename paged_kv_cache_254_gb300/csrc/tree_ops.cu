@@ -3,6 +3,7 @@
 // and values to consecutive positions of the cache.
 #include "tree_ops.cuh"
 
+#include "launch.cuh"
 #include "../../include/pa.h"
 
 namespace pa {
@@ -168,16 +169,14 @@ pa_keep_kernel(const KeepArgs a, int ctas_per_seq) {
 }
 
 cudaError_t tree_verify_launch(const VerifyArgs& a, cudaStream_t stream) {
-    pa_tree_verify_kernel<<<(unsigned)(((long long)a.N + 3) / 4), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch(pa_tree_verify_kernel, (unsigned)(((long long)a.N + 3) / 4), 128, 0, stream, a);
 }
 
 cudaError_t keep_launch(const KeepArgs& a, cudaStream_t stream) {
     const int per_seq = (2 * a.Hkv * a.vec_per_row + 255) / 256;
     const long long blocks = (long long)a.N * per_seq;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    pa_keep_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a, per_seq);
-    return cudaGetLastError();
+    return launch(pa_keep_kernel, (unsigned)blocks, 256, 0, stream, a, per_seq);
 }
 
 }  // namespace pa

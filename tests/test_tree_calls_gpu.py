@@ -1,11 +1,15 @@
 """The tree-speculation calls on the device: strides of single tokens through
-both host sides, and calls after a refused one."""
+both host sides, calls after a refused one, and errors that other calls left."""
+
+import contextlib
+import ctypes
 
 import numpy as np
 import pytest
 import torch
 
 from oracle.kv_ops import bits
+from oracle.tree import keep_ref
 from tests.gpu_util import need_gpu
 from tests.test_tree_calls import strided_views
 
@@ -84,3 +88,69 @@ def test_a_valid_call_after_a_refused_one():
     eager = pa().pa_decode_tree(**a, stream=torch.cuda.Stream())     # no workspace kept for this one
     torch.cuda.synchronize()
     assert torch.isfinite(eager.float()).all() and torch.equal(captured, eager)
+
+
+# ---------------------------------------------------------------- errors of other calls
+def cudart():
+    """The runtime that torch has loaded."""
+    with open("/proc/self/maps") as f:
+        path = next(line.split()[-1] for line in f if "libcudart" in line)
+    return ctypes.CDLL(path)
+
+
+@contextlib.contextmanager
+def broken_capture():
+    """A stream whose capture a synchronising call has invalidated: more work on it is refused until the block ends."""
+    rt, s = cudart(), torch.cuda.Stream()
+    handle = ctypes.c_void_p(s.cuda_stream)
+    err = pa().new_error_word("cuda")
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(handle, 2) == 0              # 2: relaxed, other streams are free
+    try:
+        assert pa().pa_read_error(err, s) == 3                    # PA_ERR_CUDA: a capturing stream does not synchronise
+        yield s
+    finally:
+        ended = rt.cudaStreamEndCapture(handle, ctypes.byref(ctypes.c_void_p()))
+        rt.cudaGetLastError()                                     # torch's own runtime forgets about it
+        assert ended != 0
+
+
+def leave_an_error():
+    """The library's last call in this thread failed, and nothing is the matter any more."""
+    with broken_capture():
+        pass
+
+
+def path_to_keep():
+    """A tree, pa_keep_kv arguments and the pools after it; a second run would move other rows."""
+    a = small_tree(N=1, nodes=6, seed=11)
+    path = torch.tensor([[0, 2, 3, 5, -1, -1]], dtype=torch.int32, device="cuda")
+    rest = (path.cpu().numpy(), [0, 6], a["block_tables"].cpu().numpy(), a["context_lens"].tolist(), 16)
+    want = keep_ref(bits(a["k_pool"]), bits(a["v_pool"]), *rest)
+    assert not np.array_equal(want[0], keep_ref(*want, *rest)[0])
+    return a, (path, a["q_start"], a["context_lens"], a["block_tables"], a["k_pool"], a["v_pool"]), want
+
+
+def test_an_old_error_is_not_taken_for_the_calls_own():
+    a, keep, want = path_to_keep()
+    clean = pa().pa_decode_tree(**a)
+    leave_an_error()
+    assert torch.equal(pa().pa_decode_tree(**a), clean)
+    leave_an_error()
+    pa().pa_keep_kv(*keep)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(a["k_pool"]), want[0]) and np.array_equal(bits(a["v_pool"]), want[1])
+    # queries in place: rotated once
+    freq, _ = pa().rope_inv_freq(64)
+    q, kv = a["q"], a["q"][:, :2].contiguous()
+    rope = (kv, kv, torch.arange(6, dtype=torch.int32, device="cuda") + 3, torch.arange(6, device="cuda"), a["k_pool"],
+            a["v_pool"], freq)
+    want_q = pa().pa_rope_append_kv(q, *rope)
+    leave_an_error()
+    assert torch.equal(pa().pa_rope_append_kv(q, *rope, out=q), want_q)
+    # the calls that do not run twice, but failed for nothing
+    leave_an_error()
+    pa().pa_append_kv(kv, kv, rope[3], a["k_pool"], a["v_pool"])
+    leave_an_error()
+    one = pa().pa_decode(q[:1], a["k_pool"], a["v_pool"], a["block_tables"], a["context_lens"], 0.1)
+    assert torch.isfinite(one.float()).all()
