@@ -165,6 +165,7 @@ def load_fast():
                 spec = importlib.util.spec_from_loader("_pa_fast", loader)
                 module = importlib.util.module_from_spec(spec)
                 loader.exec_module(module)
+                module.on_failure(check)
                 _fast = module
     return _fast
 

@@ -5,8 +5,10 @@
 // Python.  Each function here takes its Python namesake's arguments in order and
 // answers NotImplemented, having done nothing, as soon as anything is not plainly
 // right (a wrong type, device, shape or layout, another current device, a workspace
-// that has yet to be allocated, a status other than PA_OK); the Python function
-// then goes through its own checks and says what is wrong.
+// that has yet to be allocated, arguments that the library refuses); the Python
+// function then goes through its own checks and says what is wrong.  PA_ERR_CUDA may
+// come after a launch, and moving rows or rotating queries twice is not the same as
+// once: it is raised from here.
 #include <Python.h>
 
 #include <ATen/core/TensorBody.h>
@@ -26,6 +28,22 @@ namespace {
 PyObject* declined() {
     PyErr_Clear();                       // an int too large for a long
     Py_RETURN_NOTIMPLEMENTED;
+}
+
+PyObject* check_status = nullptr;        // Python's check(status, call), which raises the package's error
+
+// A call that the library did not take.
+PyObject* refused(pa_status st, const char* call) {
+    if (st != PA_ERR_CUDA) return declined();                    // before any launch
+    if (check_status) Py_XDECREF(PyObject_CallFunction(check_status, "is", (int)st, call));
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s: %s", call, pa_status_string(st));
+    return nullptr;
+}
+
+PyObject* on_failure(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 1) return declined();
+    Py_XSETREF(check_status, Py_NewRef(a[0]));
+    Py_RETURN_NONE;
 }
 
 // The tensor behind `o` if it is contiguous, of type `t` and on device `dev`; else null.
@@ -110,9 +128,10 @@ PyObject* keep_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return declined();
         s.num_seqs = (int32_t)N;
         s.max_blocks_per_seq = (int32_t)table->size(1);
-        if (pa_keep_kv(&s, (int32_t)P, data<int32_t>(path), data<int32_t>(start), data<int32_t>(table),
-                       data<int32_t>(ctx), data<void>(k), data<void>(v), data<uint32_t>(err), stream_of(dev)) != PA_OK)
-            return declined();
+        const pa_status st =
+            pa_keep_kv(&s, (int32_t)P, data<int32_t>(path), data<int32_t>(start), data<int32_t>(table), data<int32_t>(ctx),
+                       data<void>(k), data<void>(v), data<uint32_t>(err), stream_of(dev));
+        if (st != PA_OK) return refused(st, "pa_keep_kv");
         Py_RETURN_NONE;
     });
 }
@@ -140,11 +159,12 @@ PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor next = part(room, at::kLong, {N}, 0), accepted = part(room, at::kInt, {N}, 2 * N),
                          lens = part(room, at::kInt, {N}, 3 * N),
                          path = given ? *given : part(room, at::kInt, {N, (int64_t)P}, 4 * N);
-        if (pa_tree_verify((int32_t)N, (int32_t)P, (int32_t)T, data<int32_t>(start), data<uint64_t>(masks),
+        const pa_status st =
+            pa_tree_verify((int32_t)N, (int32_t)P, (int32_t)T, data<int32_t>(start), data<uint64_t>(masks),
                            data<int64_t>(draft), data<int64_t>(target), data<int32_t>(ctx), data<int32_t>(&path),
                            data<int32_t>(&accepted), data<int64_t>(&next), data<int32_t>(&lens), data<uint32_t>(err),
-                           stream_of(dev)) != PA_OK)
-            return declined();
+                           stream_of(dev));
+        if (st != PA_OK) return refused(st, "pa_tree_verify");
         PyObject* r = PyTuple_New(4);
         if (!r) return nullptr;
         PyTuple_SET_ITEM(r, 0, given ? Py_NewRef(a[6]) : THPVariable_Wrap(path));
@@ -199,11 +219,12 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         if (!ws) return declined();
         const at::Tensor out = given ? *given : at::empty_like(*q);
-        if (pa_decode_tree(&s, (int32_t)P, (int32_t)T, data<void>(q), data<int32_t>(start), data<uint64_t>(masks),
+        const pa_status st =
+            pa_decode_tree(&s, (int32_t)P, (int32_t)T, data<void>(q), data<int32_t>(start), data<uint64_t>(masks),
                            data<void>(k), data<void>(v), data<int32_t>(table), data<int32_t>(ctx),
                            (float)PyFloat_AS_DOUBLE(a[8]), data<void>(&out), data<void>(ws), ws->nbytes(),
-                           data<uint32_t>(err), stream) != PA_OK)
-            return declined();
+                           data<uint32_t>(err), stream);
+        if (st != PA_OK) return refused(st, "pa_decode_tree");
         return given ? Py_NewRef(a[10]) : THPVariable_Wrap(out);
     });
 }
@@ -251,17 +272,18 @@ PyObject* rope_append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const pa_rope rope{rotary ? data<float>(freq) : nullptr, rotary, a[8] == Py_True, (float)PyFloat_AS_DOUBLE(a[9]),
                            (float)PyFloat_AS_DOUBLE(a[12]), data<void>(qw), data<void>(kw)};
         const at::Tensor out = given ? *given : at::empty({T, Hq, d}, q->options());
-        if (pa_rope_append_kv(&s, &rope, (int32_t)T, data<void>(q), qs, data<void>(k), ks, data<void>(v), vs,
+        const pa_status st =
+            pa_rope_append_kv(&s, &rope, (int32_t)T, data<void>(q), qs, data<void>(k), ks, data<void>(v), vs,
                               data<int32_t>(pos), data<int64_t>(slots), data<void>(&out), data<void>(kp),
-                              data<void>(vp), data<uint32_t>(err), stream_of(dev)) != PA_OK)
-            return declined();
+                              data<void>(vp), data<uint32_t>(err), stream_of(dev));
+        if (st != PA_OK) return refused(st, "pa_rope_append_kv");
         return given ? Py_NewRef(a[13]) : THPVariable_Wrap(out);
     });
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(keep_kv), METHOD(tree_verify), METHOD(decode_tree), METHOD(rope_append_kv),
-                         {nullptr, nullptr, 0, nullptr}};
+                         METHOD(on_failure), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

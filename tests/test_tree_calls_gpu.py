@@ -154,3 +154,24 @@ def test_an_old_error_is_not_taken_for_the_calls_own():
     leave_an_error()
     one = pa().pa_decode(q[:1], a["k_pool"], a["v_pool"], a["block_tables"], a["context_lens"], 0.1)
     assert torch.isfinite(one.float()).all()
+
+
+def test_a_failed_call_is_not_made_again(monkeypatch):
+    # a launch that the runtime refuses is raised at once: a second try could run what the first left half done
+    from paged_kv_cache_254_gb300 import ops
+    tries = []
+    for name in ("_keep_kv", "_rope_append_kv"):
+        monkeypatch.setattr(ops, name, lambda *a, name=name: tries.append(name))
+    a, keep, _ = path_to_keep()
+    freq, _ = pa().rope_inv_freq(64)
+    q, kv = a["q"], a["q"][:, :2].contiguous()
+    rope = (kv, kv, torch.arange(6, dtype=torch.int32, device="cuda"), torch.arange(6, device="cuda"), a["k_pool"],
+            a["v_pool"], freq)
+    before = bits(a["k_pool"])
+    with broken_capture() as s:
+        for call in (lambda: pa().pa_keep_kv(*keep, stream=s), lambda: pa().pa_rope_append_kv(q, *rope, out=q, stream=s)):
+            with pytest.raises(pa().PagedAttentionError) as e:
+                call()
+            assert e.value.status == 3
+    torch.cuda.synchronize()
+    assert not tries and np.array_equal(bits(a["k_pool"]), before)
