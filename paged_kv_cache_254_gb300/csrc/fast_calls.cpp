@@ -206,6 +206,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
         s.num_q_heads = (int32_t)q->size(1);
         s.max_blocks_per_seq = (int32_t)table->size(1);
         void* stream = stream_of(dev);
+        const at::Tensor out = given ? *given : at::empty_like(*q);
+        // From here to the end of the call the interpreter lock stays held, so no other thread
+        // takes the stream's workspace or queues a call that uses it; while one that runs
+        // without the lock uses it, it is not in the dict.
         const at::Tensor* ws = nullptr;
         if (a[11] != Py_None) {
             if (!THPVariable_Check(a[11])) return declined();
@@ -218,7 +222,6 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (ws && ws->nbytes() < pa_decode_tree_workspace_bytes(&s, (int32_t)P)) ws = nullptr;
         }
         if (!ws) return declined();
-        const at::Tensor out = given ? *given : at::empty_like(*q);
         const pa_status st =
             pa_decode_tree(&s, (int32_t)P, (int32_t)T, data<void>(q), data<int32_t>(start), data<uint64_t>(masks),
                            data<void>(k), data<void>(v), data<int32_t>(table), data<int32_t>(ctx),

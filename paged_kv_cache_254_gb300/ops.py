@@ -60,8 +60,10 @@ _ws_cache = {}
 
 
 def workspace_for(q, k_pool, block_tables, stream=None) -> torch.Tensor:
-    """A workspace kept per (device, stream) and grown on demand; pa_decode
-    clears its counter region itself, so the buffer is reused as is."""
+    """A pa_decode workspace kept per (device, stream) and grown on demand, for
+    callers that pass one; pa_decode clears its counter region itself, so the
+    buffer is reused as is.  Every caller on the stream gets the same one:
+    threads that share a stream need their own, or none (see _lend)."""
     need = pa_decode_workspace_bytes(q, k_pool, block_tables)
     if need == 0:
         return torch.empty(0, dtype=torch.uint8, device=q.device)
@@ -73,6 +75,40 @@ def workspace_for(q, k_pool, block_tables, stream=None) -> torch.Tensor:
             ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=q.device)
             _ws_cache[key] = ws
         return ws
+
+
+# Workspaces of calls that are given none, by (device index, stream handle).
+_sp_cache = {}
+
+
+def _lend(given, index, handle, need, call, stream=None):
+    """call(workspace) with the one given, or with one of ``need`` bytes that
+    is this call's alone until it returns.
+
+    A call is several launches that hand their intermediate state over in the
+    workspace, and other threads may queue work on the same stream between
+    them.  So the stream's workspace leaves ``_sp_cache`` for the call (dict.pop
+    is one step under the interpreter lock); a call that finds none allocates,
+    and the larger one is kept.  Everything stays in the stream's order, so a
+    workspace that is dropped or used again meets no work of its last call.
+    A captured call's belongs to its graph: the stream's may be replaced by a
+    larger one, and another graph may run beside this one.  ``stream`` says
+    where to allocate if that is not the current stream."""
+    if given is not None:
+        return call(given)
+    if torch.cuda.is_current_stream_capturing():
+        return call(torch.empty(need, dtype=torch.uint8, device=f"cuda:{index}"))
+    key = (index, handle)
+    ws = _sp_cache.pop(key, None)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(stream):                  # None: where we are
+            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{index}")
+    try:
+        return call(ws)
+    finally:
+        other = _sp_cache.get(key)
+        if other is None or other.numel() < ws.numel():
+            _sp_cache[key] = ws
 
 
 def new_error_word(device) -> torch.Tensor:
@@ -100,18 +136,19 @@ def pa_decode(q, k_pool, v_pool, block_tables, context_lens, scale, out=None, wo
         _need_cuda("out", out, q.dtype)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    if workspace is None:
-        workspace = workspace_for(q, k_pool, block_tables, stream)
-    else:
+    if workspace is not None:
         _need_cuda("workspace", workspace)
     if err is not None:
         _need_cuda("err", err, torch.int32)
     shape = _pool_shape(k_pool, N, Hq, block_tables.shape[1])
+    lib = _lib.load()
     with torch.cuda.device(q.device):
-        st = _lib.load().pa_decode(ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
-                                   _ptr(context_lens), ctypes.c_float(scale), _ptr(out), _ptr(workspace),
-                                   ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
-                                   _stream(q.device, stream))
+        need = 0 if workspace is not None else int(lib.pa_decode_workspace_bytes(ctypes.byref(shape)))
+        s = _stream(q.device, stream)
+        st = _lend(workspace, q.device.index, s.value or 0, need,
+                   lambda ws: lib.pa_decode(ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
+                                            _ptr(context_lens), ctypes.c_float(scale), _ptr(out), _ptr(ws),
+                                            ctypes.c_size_t(ws.numel() * ws.element_size()), _ptr(err), s), stream)
     _lib.check(st, "pa_decode")
     return out
 
@@ -194,18 +231,16 @@ def pa_decode_shared_prefix(q, k_pool, v_pool, block_tables, context_lens, group
     lib = _lib.load()
     with torch.cuda.device(q.device):
         need = int(lib.pa_decode_shared_prefix_workspace_bytes(ctypes.byref(shape)))
-        if workspace is None:
-            workspace = _shared_workspace(q.device, need, stream)
-        else:
+        if workspace is not None:
             _need_cuda("workspace", workspace)
         if err is not None:
             _need_cuda("err", err, torch.int32)
-        st = lib.pa_decode_shared_prefix(ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool),
-                                         _ptr(block_tables), _ptr(context_lens), ctypes.c_int32(n_groups),
-                                         _ptr(group_starts), _ptr(group_prefix_blocks), ctypes.c_float(scale),
-                                         _ptr(out), _ptr(workspace),
-                                         ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
-                                         _stream(q.device, stream))
+        s = _stream(q.device, stream)
+        st = _lend(workspace, q.device.index, s.value or 0, need,
+                   lambda ws: lib.pa_decode_shared_prefix(
+                       ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens),
+                       ctypes.c_int32(n_groups), _ptr(group_starts), _ptr(group_prefix_blocks), ctypes.c_float(scale),
+                       _ptr(out), _ptr(ws), ctypes.c_size_t(ws.numel() * ws.element_size()), _ptr(err), s), stream)
     _lib.check(st, "pa_decode_shared_prefix")
     return out
 
@@ -245,17 +280,16 @@ def pa_decode_multi(q, k_pool, v_pool, block_tables, context_lens, q_start, scal
         if need == 0 and workspace is None:
             # an invalid shape or chunk bound: let the call report which
             workspace = torch.empty(0, dtype=torch.uint8, device=q.device)
-        elif workspace is None:
-            workspace = _shared_workspace(q.device, need, stream)
-        else:
+        elif workspace is not None:
             _need_cuda("workspace", workspace)
         if err is not None:
             _need_cuda("err", err, torch.int32)
-        st = lib.pa_decode_multi(ctypes.byref(shape), ctypes.c_int32(max_q_len), ctypes.c_int32(T), _ptr(q),
-                                 _ptr(q_start), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
-                                 _ptr(context_lens), ctypes.c_float(scale), _ptr(out), _ptr(workspace),
-                                 ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
-                                 _stream(q.device, stream))
+        s = _stream(q.device, stream)
+        st = _lend(workspace, q.device.index, s.value or 0, need,
+                   lambda ws: lib.pa_decode_multi(
+                       ctypes.byref(shape), ctypes.c_int32(max_q_len), ctypes.c_int32(T), _ptr(q), _ptr(q_start),
+                       _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), ctypes.c_float(scale),
+                       _ptr(out), _ptr(ws), ctypes.c_size_t(ws.numel() * ws.element_size()), _ptr(err), s), stream)
     _lib.check(st, "pa_decode_multi")
     return out
 
@@ -327,7 +361,7 @@ def _load_fast():
 _tree_bytes = {}
 
 
-def _tree_workspace(dev, shape, max_nodes):
+def _tree_workspace_bytes(dev, shape, max_nodes):
     # the size of a valid shape's workspace depends on these and the device's SM count alone
     key = (dev, max_nodes, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim, shape.block_size,
            shape.dtype)
@@ -336,11 +370,7 @@ def _tree_workspace(dev, shape, max_nodes):
         need = int(_call(_lib.load().pa_decode_tree_workspace_bytes, dev, shape, max_nodes))
         if need:                         # 0: something about the shape is invalid, which the call reports
             _tree_bytes[key] = need
-    if need == 0 or torch.cuda.is_current_stream_capturing():
-        # a captured call keeps a workspace of its graph's own: the shared one may be
-        # replaced by a larger one, and another graph may run beside this one
-        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
-    return _kept_workspace(dev, _raw_stream(dev), need)
+    return need
 
 
 def pa_decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_masks, scale, max_nodes=None,
@@ -395,14 +425,19 @@ def _decode_tree(q, k_pool, v_pool, block_tables, context_lens, q_start, tree_ma
     if err is not None:
         _arg("err", err, torch.int32, dev)
     shape = _lib.PaShape(N, Hq, pool[1], d, pool[2], pool[0], MB, _DTYPES[dt])
-    if workspace is None:
-        workspace = _tree_workspace(dev, shape, max_nodes)
-    else:
+    need = 0
+    if workspace is not None:
         _arg("workspace", workspace, workspace.dtype, dev)
-    st = _call(_lib.load().pa_decode_tree, dev, shape, max_nodes, T, q.data_ptr(), q_start.data_ptr(),
-               tree_masks.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
-               context_lens.data_ptr(), scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _addr(err),
-               _raw_stream(dev))
+    else:
+        need = _tree_workspace_bytes(dev, shape, max_nodes)
+        if need == 0:
+            workspace = torch.empty(0, dtype=torch.uint8, device=q.device)
+    handle = _raw_stream(dev)
+    st = _lend(workspace, dev, handle, need,
+               lambda ws: _call(_lib.load().pa_decode_tree, dev, shape, max_nodes, T, q.data_ptr(), q_start.data_ptr(),
+                                tree_masks.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+                                context_lens.data_ptr(), scale, out.data_ptr(), ws.data_ptr(), ws.nbytes, _addr(err),
+                                handle))
     if st:
         _lib.check(st, "pa_decode_tree")
     return out
@@ -590,24 +625,6 @@ def _rope_append_kv(q, k_new, v_new, positions, slot_mapping, k_pool, v_pool, in
     return out
 
 
-_sp_cache = {}
-
-
-def _shared_workspace(device, need, stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return _kept_workspace(device.index, s.cuda_stream, need)
-
-
-def _kept_workspace(index, stream_handle, need):
-    key = (index, stream_handle)
-    with _ws_lock:
-        ws = _sp_cache.get(key)
-        if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{index}")
-            _sp_cache[key] = ws
-        return ws
-
-
 KV_FORMATS = {"e4m3": _lib.PA_FP8_E4M3, "e5m2": _lib.PA_FP8_E5M2}
 
 
@@ -633,14 +650,13 @@ def pa_decode_fp8(q, kv_pool, block_tables, context_lens, scale, k_scale, v_scal
     shape = make_shape(N, Hq, Hkv, d, B, NB, block_tables.shape[1], q.dtype)
     lib = _lib.load()
     with torch.cuda.device(q.device):
-        if workspace is None:
-            need = int(lib.pa_decode_fp8_workspace_bytes(ctypes.byref(shape), fmt))
-            workspace = _shared_workspace(q.device, max(need, 1), stream)
-        st = lib.pa_decode_fp8(ctypes.byref(shape), fmt, _ptr(q), _ptr(kv_pool), _ptr(block_tables),
-                               _ptr(context_lens), ctypes.c_float(scale), ctypes.c_float(k_scale),
-                               ctypes.c_float(v_scale), _ptr(out), _ptr(workspace),
-                               ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
-                               _stream(q.device, stream))
+        need = 0 if workspace is not None else int(lib.pa_decode_fp8_workspace_bytes(ctypes.byref(shape), fmt))
+        s = _stream(q.device, stream)
+        st = _lend(workspace, q.device.index, s.value or 0, max(need, 1),
+                   lambda ws: lib.pa_decode_fp8(ctypes.byref(shape), fmt, _ptr(q), _ptr(kv_pool), _ptr(block_tables),
+                                                _ptr(context_lens), ctypes.c_float(scale), ctypes.c_float(k_scale),
+                                                ctypes.c_float(v_scale), _ptr(out), _ptr(ws),
+                                                ctypes.c_size_t(ws.numel() * ws.element_size()), _ptr(err), s), stream)
     _lib.check(st, "pa_decode_fp8")
     return out
 
@@ -703,13 +719,12 @@ def pa_decode_int4(q, kv_pool, block_tables, context_lens, scale, out=None, work
     shape = make_shape(N, Hq, Hkv, d, B, NB, block_tables.shape[1], q.dtype)
     lib = _lib.load()
     with torch.cuda.device(q.device):
-        if workspace is None:
-            need = int(lib.pa_decode_int4_workspace_bytes(ctypes.byref(shape)))
-            workspace = _shared_workspace(q.device, max(need, 1), stream)
-        st = lib.pa_decode_int4(ctypes.byref(shape), _ptr(q), _ptr(kv_pool), _ptr(block_tables),
-                                _ptr(context_lens), ctypes.c_float(scale), _ptr(out), _ptr(workspace),
-                                ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(err),
-                                _stream(q.device, stream))
+        need = 0 if workspace is not None else int(lib.pa_decode_int4_workspace_bytes(ctypes.byref(shape)))
+        s = _stream(q.device, stream)
+        st = _lend(workspace, q.device.index, s.value or 0, max(need, 1),
+                   lambda ws: lib.pa_decode_int4(ctypes.byref(shape), _ptr(q), _ptr(kv_pool), _ptr(block_tables),
+                                                 _ptr(context_lens), ctypes.c_float(scale), _ptr(out), _ptr(ws),
+                                                 ctypes.c_size_t(ws.numel() * ws.element_size()), _ptr(err), s), stream)
     _lib.check(st, "pa_decode_int4")
     return out
 

@@ -1,6 +1,9 @@
 """Host side of the tree-speculation calls, on the CPU: strides of single
-tokens, and sizes of workspaces."""
+tokens, sizes of workspaces, and who uses one."""
 
+import contextlib
+import ctypes
+import threading
 import types
 
 import pytest
@@ -44,10 +47,91 @@ def test_a_refused_shape_leaves_no_size_behind(monkeypatch):
     monkeypatch.setattr(_lib, "load", lambda: fake)
     monkeypatch.setattr(ops, "_call", lambda fn, dev, *a: fn(*a))
     monkeypatch.setattr(ops, "_tree_bytes", {})
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
-    sizes = []
-    empty = torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, **kw: sizes.append(a[0]) or empty(*a))
     for mb, want in ((0, 0), (9, 4096), (0, 4096), (9, 4096)):
-        ops._tree_workspace(0, _lib.PaShape(2, 8, 2, 128, 16, 64, mb, _lib.PA_BF16), 8)
-        assert sizes[-1] == want
+        assert ops._tree_workspace_bytes(0, _lib.PaShape(2, 8, 2, 128, 16, 64, mb, _lib.PA_BF16), 8) == want
+
+
+class FakeLibrary:
+    """Stands for libpa: sizes are 1000 bytes, and a call waits until another is inside as well.  ``used`` are the
+    workspaces that the calls were given."""
+
+    def __init__(self, buffers):
+        self.buffers, self.used, self.inside = buffers, [], threading.Barrier(2)
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *a: 1000
+        return self.call
+
+    def call(self, *args):
+        values = {getattr(a, "value", a) for a in args if isinstance(a, (int, ctypes.c_void_p, ctypes.c_size_t))}
+        self.used.append(next(b for b in self.buffers if b.data_ptr() in values))
+        assert all(w is not self.used[-1] for w in ops._sp_cache.values())   # not to be found by a third call
+        self.inside.wait(timeout=30)
+        return 0
+
+
+@pytest.fixture
+def fake_library(monkeypatch):
+    buffers, empty, zeros = [], torch.empty, torch.zeros
+
+    def on_the_host(make):
+        def f(*size, dtype=None, device=None):
+            t = make(*size, dtype=dtype)
+            if dtype == torch.uint8:
+                buffers.append(t)
+            return t
+        return f
+
+    lib = FakeLibrary(buffers)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    monkeypatch.setattr(torch, "empty", on_the_host(empty))
+    monkeypatch.setattr(torch, "zeros", on_the_host(zeros))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(torch.cuda, "device", type("Here", (contextlib.nullcontext,), {}))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for name, value in (("_need_cuda", lambda *a: None), ("_arg", lambda *a: None), ("_index", lambda *a: 0),
+                        ("_raw_stream", lambda d: 7), ("_call", lambda fn, dev, *a: fn(*a)), ("_sp_cache", {}),
+                        ("_fast", types.SimpleNamespace(decode_tree=lambda *a: NotImplemented))):
+        monkeypatch.setattr(ops, name, value)
+    return lib
+
+
+def host_call(name):
+    """A call of one of the attention entry points with tensors of the right shapes."""
+    N, Hq, Hkv, d, B = 2, 4, 2, 128, 16
+    half = lambda *s: torch.ones(*s, dtype=torch.float16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    q, k, v, table, ctx = half(N, Hq, d), half(4, Hkv, B, d), half(4, Hkv, B, d), i32([0, 1], [2, 3]), i32(5, 6)
+    start, u8 = i32(0, 1, 2), lambda *s: torch.ones(s, dtype=torch.uint8)
+    return {"decode": lambda: ops.pa_decode(q, k, v, table, ctx, 0.1),
+            "multi": lambda: ops.pa_decode_multi(q, k, v, table, ctx, start, 0.1, max_q_len=1),
+            "shared_prefix": lambda: ops.pa_decode_shared_prefix(q, k, v, table, ctx, start[:2], i32(0), 0.1),
+            "fp8": lambda: ops.pa_decode_fp8(q, u8(4, Hkv, 2, B, d), table, ctx, 0.1, 1.0, 1.0),
+            "int4": lambda: ops.pa_decode_int4(q, u8(4, Hkv, B, d + 8), table, ctx, 0.1),
+            "tree": lambda: ops.pa_decode_tree(q, k, v, table, ctx, start, torch.ones(2, dtype=torch.int64), 0.1, 1)}[name]
+
+
+@pytest.mark.parametrize("one", ["decode", "multi", "shared_prefix", "fp8", "int4", "tree"])
+@pytest.mark.parametrize("other", ["tree", "multi"])
+def test_two_threads_on_one_stream_do_not_share_a_workspace(fake_library, one, other):
+    # a call is several launches: another thread's may come between them, on the same stream
+    for round_ in range(2):                               # the second time one is kept already
+        fake_library.used.clear()
+        failed = []
+
+        def run(call):
+            try:
+                call()
+            except Exception as e:                        # a broken barrier: the other call failed
+                failed.append(e)
+
+        threads = [threading.Thread(target=run, args=(host_call(n),)) for n in (one, other)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed, failed
+        a, b = fake_library.used
+        assert a is not b
+        assert len(ops._sp_cache) in (1, 2) and all(w is a or w is b for w in ops._sp_cache.values())   # one a key

@@ -1,8 +1,10 @@
 """The tree-speculation calls on the device: strides of single tokens through
-both host sides, calls after a refused one, and errors that other calls left."""
+both host sides, calls after a refused one, errors that other calls left, threads
+and graphs."""
 
 import contextlib
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -175,3 +177,70 @@ def test_a_failed_call_is_not_made_again(monkeypatch):
             assert e.value.status == 3
     torch.cuda.synchronize()
     assert not tries and np.array_equal(bits(a["k_pool"]), before)
+
+
+# ---------------------------------------------------------------- several threads, several graphs
+def chunk_args(a):
+    """pa_decode_multi arguments over the same cache (chains are what a chunk sees)."""
+    return {k: a[k] for k in ("q", "k_pool", "v_pool", "block_tables", "context_lens", "q_start", "scale")}
+
+
+def test_threads_on_one_stream():
+    # trees of several sizes (the cut pairs' states differ), through both host sides, and chunks
+    from paged_kv_cache_254_gb300 import ops
+    trees = [small_tree(N=n, nodes=p, Hq=8, Hkv=1, MB=40, seed=n + p) for n, p in ((3, 5), (9, 3), (2, 20))]
+    for t in trees:
+        t["context_lens"] += 500
+    args = [tuple(t.values()) + (None, None, None) for t in trees]
+    calls = [lambda a=a: ops._decode_tree(*a) for a in args]
+    calls += [lambda t=t: pa().pa_decode_tree(**t) for t in trees]
+    calls += [lambda t=t, p=p: pa().pa_decode_multi(**chunk_args(t), max_q_len=p) for t, p in zip(trees[:2], (5, 3))]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    outs = [[None] * 100 for _ in calls]
+
+    def run(i):
+        for k in range(100):
+            outs[i][k] = calls[i]()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+
+
+@pytest.mark.parametrize("kind", ["decode", "multi"])
+def test_captured_decodes_share_nothing(kind):
+    # two captured calls replayed side by side, after eager calls that replaced the stream's workspace
+    made = [small_tree(N=n, nodes=5, MB=60, seed=n) for n in (3, 6)]
+    calls = []
+    for t in made:
+        t["context_lens"] += 800
+        if kind == "multi":
+            calls.append(lambda t=t: pa().pa_decode_multi(**chunk_args(t), max_q_len=5))
+        else:
+            one = t["q"][:t["block_tables"].shape[0]].contiguous()
+            calls.append(lambda t=t, one=one: pa().pa_decode(one, t["k_pool"], t["v_pool"], t["block_tables"],
+                                                             t["context_lens"], t["scale"]))
+    want = [c() for c in calls]
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    big = small_tree(N=64, nodes=12, Hq=32, Hkv=2, d=128, seed=5)
+    pa().pa_decode_tree(**big)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
