@@ -1135,7 +1135,7 @@ pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t 
         return PA_ERR_INVALID_ARG;
     // q_out may be q itself (a row is read before it is written), not a shifted part of
     // it, nor lie over the keys and values
-    const int64_t last = num_tokens - 1, out_bytes = 2 * num_tokens * q_row;
+    const int64_t last = num_tokens - 1, out_bytes = 2 * (int64_t)num_tokens * q_row;
     if (overlap(q_out, out_bytes, q, 2 * (last * q_stride + q_row)) && !(q == q_out && q_stride == q_row))
         return PA_ERR_INVALID_ARG;
     if (overlap(q_out, out_bytes, k_new, 2 * (last * k_stride + kv_row)) ||

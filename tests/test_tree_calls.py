@@ -1,5 +1,5 @@
 """Host side of the tree-speculation calls, on the CPU: strides of single
-tokens, sizes of workspaces, and who uses one."""
+tokens, sizes of workspaces and who uses one, and operands that overlap."""
 
 import contextlib
 import ctypes
@@ -9,7 +9,8 @@ import types
 import pytest
 import torch
 
-from paged_kv_cache_254_gb300 import _lib, ops
+from paged_kv_cache_254_gb300 import _build, _lib, ops
+from tests.test_abi import FAKE, NULL, shape
 
 
 def strided_views(T, H, d, device="cpu"):
@@ -135,3 +136,23 @@ def test_two_threads_on_one_stream_do_not_share_a_workspace(fake_library, one, o
         a, b = fake_library.used
         assert a is not b
         assert len(ops._sp_cache) in (1, 2) and all(w is a or w is b for w in ops._sp_cache.values())   # one a key
+
+
+# ---------------------------------------------------------------- overlapping operands
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would start a kernel")
+@pytest.mark.parametrize("tokens", [1 << 20, 1 << 29, 1 << 30, (1 << 31) - 1])
+def test_rotated_queries_over_other_operands_at_any_token_count(tokens):
+    _build.build()
+    at = lambda rows: ctypes.c_void_p(FAKE.value + 32 * rows)          # a token's row is 32 bytes
+
+    def status(q, k, v, out):
+        rope = _lib.PaRope(None, 0, 0, 1.0, 1e-6, None, None)
+        return _lib.load().pa_rope_append_kv(shape(num_q_heads=1, num_kv_heads=1, head_dim=16), rope, tokens, q, 16, k, 16,
+                                             v, 16, FAKE, FAKE, out, FAKE, at(1), NULL, NULL)
+
+    n = tokens
+    assert status(at(0), at(2 * n), at(3 * n), at(n)) == 3              # side by side: fine (no GPU here)
+    assert status(at(0), at(2 * n), at(3 * n), at(n - 1)) == 1          # into q's last row
+    assert status(at(n), at(2 * n), at(3 * n), at(1)) == 1              # q_out's last row into q's first
+    assert status(at(0), at(2 * n - 1), at(3 * n), at(n)) == 1          # into the keys
+    assert status(at(0), at(3 * n), at(2 * n - 1), at(n)) == 1          # into the values
