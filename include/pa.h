@@ -396,7 +396,8 @@ pa_status pa_append_kv(const pa_shape* shape, int32_t num_tokens, const void* k_
  *   q_out            [num_tokens][Hq][d]; may be q itself when q is contiguous, must
  *                    not overlap it, k_new or v_new otherwise
  *   rope->inv_freq   fp32 [rotary_dim / 2] radians per position (device); long-context
- *                    scalings are frequencies and a scale
+ *                    scalings are frequencies and a scale; one that is not finite makes
+ *                    its pairs NaN
  *   rope->q_weight, k_weight  16-bit [d] (device) or NULL
  *
  * Supported: fp16 or bf16; d a multiple of 16 up to 256; rotary_dim a multiple

@@ -16,7 +16,8 @@
 // fraction of a turn exactly (whole turns fall off the top; a negative p works
 // alike), with an error below p * 2^-64 turns.  Its top 32 bits go to
 // sincospif.  u_j comes from the fp32 frequency's mantissa times 1 / 2 pi in
-// integer arithmetic: no fp64 (2 operations per clock and SM here).
+// integer arithmetic: no fp64 (2 operations per clock and SM here).  An infinite or
+// NaN frequency has no such number: its pairs' cosines and sines are NaN.
 //
 // What bounds it: HBM at first (every value is read once and written once), then
 // the instructions around it.  A row of D values is held by D / 16 lanes, 16
@@ -97,9 +98,14 @@ pa_rope_append_kernel(const RopeArgs a) {
     constexpr int U = STEPS;
     constexpr int PAIRS = 8 * LPR;                      // at most, in a row
     __shared__ __align__(16) uint64_t sfreq[PAIRS];
+    __shared__ float sscale[PAIRS];                     // of a pair's cosine and sine
     __shared__ __align__(16) float sweight[2][2 * PAIRS];  // of queries and of keys
     __shared__ __align__(16) float2 sturn[WARPS][PAIRS];   // (cos, sin) of the warp's token
-    for (int i = threadIdx.x; i < a.rot / 2; i += 32 * WARPS) sfreq[i] = turns_per_position(__ldg(a.inv_freq + i));
+    for (int i = threadIdx.x; i < a.rot / 2; i += 32 * WARPS) {
+        const float f = __ldg(a.inv_freq + i);
+        sfreq[i] = turns_per_position(f);
+        sscale[i] = isfinite(f) ? a.scale : __int_as_float(0x7fc00000);
+    }
     for (int i = threadIdx.x; i < a.D; i += 32 * WARPS) {
         auto f = [](uint16_t w) -> float { return lo_of<BF16>(w); };
         sweight[0][i] = a.q_weight ? f(__ldg(a.q_weight + i)) : 1.f;
@@ -195,8 +201,8 @@ pa_rope_append_kernel(const RopeArgs a) {
                 const float h = (float)(int32_t)(uint32_t)(turn >> 32) * 0x1p-31f;
                 float2 w;
                 sincospif(h, &w.y, &w.x);
-                w.x *= a.scale;
-                w.y *= a.scale;
+                w.x *= sscale[j];
+                w.y *= sscale[j];
                 sturn[warp][j] = w;
             }
             __syncwarp();

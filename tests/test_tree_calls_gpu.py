@@ -244,3 +244,25 @@ def test_captured_decodes_share_nothing(kind):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+# ---------------------------------------------------------------- rotary positions
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_that_are_not_finite(interleaved):
+    H, d, T = 2, 64, 5
+    freq, _ = pa().rope_inv_freq(d)
+    bad = {3: float("inf"), 17: float("-inf"), 30: float("nan")}
+    spoilt = freq.clone()
+    for j, f in bad.items():
+        spoilt[j] = f
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(T, H, d, device="cuda", generator=g).bfloat16() for _ in range(3))
+    pos, slots = torch.tensor([0, 1, -5, 4096, 77], dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda")
+    pools = [torch.zeros(1, H, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    want = pa().pa_rope_append_kv(q, k, v, pos, slots, pools[0], pools[1], freq, interleaved=interleaved)
+    got = pa().pa_rope_append_kv(q, k, v, pos, slots, pools[2], pools[3], spoilt, interleaved=interleaved)
+    nan = torch.zeros(d, dtype=torch.bool, device="cuda")
+    for j in bad:
+        nan[[2 * j, 2 * j + 1] if interleaved else [j, j + d // 2]] = True
+    for a, b in ((got, want), (pools[2][0, :, :T], pools[0][0, :, :T])):
+        assert torch.isnan(a[..., nan]).all() and torch.equal(a[..., ~nan], b[..., ~nan])
