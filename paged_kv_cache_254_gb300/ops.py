@@ -335,6 +335,9 @@ def _on_stream(stream, fn, *args):
     """fn(*args) with ``stream`` current, so that what it allocates belongs to
     the stream, and its arguments' memory is not reused before the stream has
     passed the call."""
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, a tensor on {t.device}")
     with torch.cuda.stream(stream):
         result = fn(*args)
     for t in args:

@@ -1,5 +1,6 @@
 """Host side of the tree-speculation calls, on the CPU: strides of single
-tokens, sizes of workspaces and who uses one, and operands that overlap."""
+tokens, sizes of workspaces and who uses one, operands that overlap, and streams
+of another device."""
 
 import contextlib
 import ctypes
@@ -8,6 +9,7 @@ import types
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 from paged_kv_cache_254_gb300 import _build, _lib, ops
 from tests.test_abi import FAKE, NULL, shape
@@ -156,3 +158,18 @@ def test_rotated_queries_over_other_operands_at_any_token_count(tokens):
     assert status(at(n), at(2 * n), at(3 * n), at(1)) == 1              # q_out's last row into q's first
     assert status(at(0), at(2 * n - 1), at(3 * n), at(n)) == 1          # into the keys
     assert status(at(0), at(3 * n), at(2 * n - 1), at(n)) == 1          # into the values
+
+
+# ---------------------------------------------------------------- streams
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    # with it current the call would go to the stream that is current on the tensors' device
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    with FakeTensorMode():
+        here = [torch.empty(2, device="cuda:0"), None, torch.empty(3, dtype=torch.int32, device="cuda:0"), 0.5]
+    made = []
+    with pytest.raises(ValueError, match="stream"):
+        ops._on_stream(types.SimpleNamespace(device=torch.device("cuda", 1)), lambda *a: made.append(a), *here)
+    assert not made
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: made.append(t))
+    ops._on_stream(types.SimpleNamespace(device=torch.device("cuda", 0)), lambda *a: made.append(a), *here)
+    assert len(made) == 3
