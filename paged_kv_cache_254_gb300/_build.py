@@ -5,7 +5,9 @@ Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into
 only when a source or header is newer than the library.  ptxas resource
 reports (registers, spills, shared memory) are kept next to the objects.
 ``csrc/fast_calls.cpp`` becomes ``lib/_pa_fast.so``, a Python module against the
-installed torch's headers that calls into libpa.so.
+installed torch's headers that calls into libpa.so.  It only saves host time:
+where it cannot be compiled (no g++, no Python or torch headers) the build says
+so and libpa.so stands alone, with the checks in Python.
 """
 
 from __future__ import annotations
@@ -19,6 +21,7 @@ import platform
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,19 +59,29 @@ def _deps():
 STAMP = os.path.join(LIBDIR, "host-arch.txt")
 
 
+NO_FAST = ", host calls not compiled"          # at the end of the stamp
+
+
 def _stamp() -> str:
-    return f"{platform.machine()} torch {importlib.metadata.version('torch')}"
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return f"{platform.machine()} torch {torch}"
 
 
 def up_to_date() -> bool:
-    """The libraries exist, were built on this machine's architecture with the
-    installed torch, and are newer than every source."""
-    if not all(os.path.exists(p) for p in (LIBPATH, FASTPATH, STAMP)):
+    """The libraries exist (_pa_fast.so unless it could not be compiled), were
+    built on this machine's architecture with the installed torch, and are
+    newer than every source."""
+    if not all(os.path.exists(p) for p in (LIBPATH, STAMP)):
         return False
     with open(STAMP) as f:
-        if f.read().strip() != _stamp():
-            return False
-    t = min(os.path.getmtime(LIBPATH), os.path.getmtime(FASTPATH))
+        stamp = f.read().strip()
+    built = [LIBPATH] if stamp == _stamp() + NO_FAST else [LIBPATH, FASTPATH]
+    if stamp.removesuffix(NO_FAST) != _stamp() or not all(os.path.exists(p) for p in built):
+        return False
+    t = min(os.path.getmtime(p) for p in built)
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -83,8 +96,15 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    return spec.submodule_search_locations[0]
+
+
 def _compile_fast() -> str:
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     obj = os.path.join(OBJDIR, "fast_calls.o")
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-I{torch_dir}/include",
@@ -97,7 +117,7 @@ def _compile_fast() -> str:
 
 
 def _link_fast(obj: str) -> None:
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     tmp = FASTPATH + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-lpa", f"-L{torch_dir}/lib", "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
@@ -108,7 +128,8 @@ def _link_fast(obj: str) -> None:
 
 
 def build(force: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libpa.so and _pa_fast.so; returns the former's path."""
+    """Compile and link libpa.so and, where that is possible, _pa_fast.so;
+    returns the former's path."""
     if not force and up_to_date():
         return LIBPATH
     os.makedirs(OBJDIR, exist_ok=True)
@@ -117,16 +138,23 @@ def build(force: bool = False, jobs: int | None = None) -> str:
     with cf.ThreadPoolExecutor(max_workers=jobs + 1) as ex:
         fast = ex.submit(_compile_fast)
         objs = list(ex.map(_compile, srcs))
-        fast_obj = fast.result()
     tmp = LIBPATH + ".tmp"
     cmd = [nvcc(), ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIBPATH)
-    _link_fast(fast_obj)
+    without = ""
+    try:
+        _link_fast(fast.result())
+    except (RuntimeError, OSError) as e:
+        without = NO_FAST
+        if os.path.exists(FASTPATH):
+            os.remove(FASTPATH)                  # of other sources
+        warnings.warn(f"{os.path.basename(FASTPATH)} was not built: the tree-speculation calls do their checks in Python, "
+                      f"about 10 microseconds a call; build(force=True) tries again.  {e}", RuntimeWarning, stacklevel=2)
     with open(STAMP, "w") as f:
-        f.write(_stamp() + "\n")
+        f.write(_stamp() + without + "\n")
     return LIBPATH
 
 

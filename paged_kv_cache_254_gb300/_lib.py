@@ -13,6 +13,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 
 from . import _build
 
@@ -151,21 +152,34 @@ def load() -> ctypes.CDLL:
 _fast = None
 
 
+class _Declining:
+    """The compiled host calls where they could not be built: each declines, and
+    the Python functions make the call."""
+
+    @staticmethod
+    def decode_tree(*args):
+        return NotImplemented
+
+    tree_verify = keep_kv = rope_append_kv = decode_tree
+
+
 def load_fast():
-    """The compiled host calls (``csrc/fast_calls.cpp``), built with libpa.so."""
+    """The compiled host calls (``csrc/fast_calls.cpp``), built with libpa.so;
+    without them, ones that decline."""
     global _fast
     if _fast is None:
         load()
         with _lock:
             if _fast is None:
-                path = _build.FASTPATH
-                if not os.path.exists(path):
-                    raise RuntimeError(f"{path} is not built; run paged_kv_cache_254_gb300._build.build()")
-                loader = importlib.machinery.ExtensionFileLoader("_pa_fast", path)
-                spec = importlib.util.spec_from_loader("_pa_fast", loader)
-                module = importlib.util.module_from_spec(spec)
-                loader.exec_module(module)
-                module.on_failure(check)
+                try:
+                    loader = importlib.machinery.ExtensionFileLoader("_pa_fast", _build.FASTPATH)
+                    spec = importlib.util.spec_from_loader("_pa_fast", loader)
+                    module = importlib.util.module_from_spec(spec)
+                    loader.exec_module(module)
+                    module.on_failure(check)
+                except ImportError as e:         # not there, or of another torch
+                    warnings.warn(f"the compiled host calls are not used: {e}", RuntimeWarning, stacklevel=3)
+                    module = _Declining()
                 _fast = module
     return _fast
 
