@@ -77,3 +77,40 @@ def test_weights_are_not_biased(g, nodes, d):
     rounded = torch.from_numpy(exact).to(torch.bfloat16).double().numpy()
     bias = (got.double().cpu().numpy().reshape(exact.shape) - rounded).mean()
     assert abs(bias) < 1.0e-6, f"outputs are off by {bias:.2e} on average"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,nodes", [(4, 4), (4, 30), (8, 40)])
+def test_every_key_of_a_long_context_counts_once(g, nodes, d, dtype):
+    # Keys are zero, so all weights are 1 and every sum is a whole number below 2^24: exact in fp32, whatever the order
+    # and the splits.  Each 16 tokens have a 1 in one dim, in turn; a dim has at most 33 such groups, so one that is
+    # lost or taken twice moves its output by 3 % or more.  What is left: 1 / L and the product with it (2 steps of 2^-24)
+    # and the output's own rounding.
+    B, ctxs = 16, [20000, 17 + nodes, 9000, 33000]
+    N, longest = len(ctxs), 33008
+    r = np.random.default_rng(g * nodes + d)
+    group = np.arange(longest) // 16
+    v = torch.zeros(N, longest, 1, d, dtype=dtype)
+    v[:, torch.arange(longest), 0, torch.from_numpy(group % d)] = 1.0
+    table = scattered_table(N, longest // B, nodes)
+    sizes = [nodes, nodes, max(1, nodes // 2), nodes]
+    starts = np.concatenate([[0], np.cumsum(sizes)])
+    masks, exact = [], []
+    for n, ctx in zip(sizes, ctxs):
+        before = np.bincount(group[:ctx - n] % d, minlength=d)
+        for i in range(n):
+            m = int(r.integers(0, 1 << 62)) & ((1 << (i + 1)) - 1)
+            seen = [ctx - n + j for j in range(n) if (m >> j) & 1]
+            masks.append(m)
+            exact.append((before + np.bincount(group[seen] % d, minlength=d)) / (ctx - n + len(seen)))
+    q = torch.randn(int(starts[-1]), g, d, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    got = pa().pa_decode_tree(q, torch.zeros(table.numel(), 1, B, d, dtype=dtype, device="cuda"), to_pool(v, table, B), table,
+                              torch.tensor(ctxs, dtype=torch.int32, device="cuda"),
+                              torch.from_numpy(starts.astype(np.int32)).cuda(), torch.tensor(masks, device="cuda"), 0.1,
+                              max_nodes=nodes)
+    exact = np.repeat(np.array(exact)[:, None], g, 1)
+    err = np.abs(got.double().cpu().numpy() - exact)
+    # fp16 steps are 2^-24 below its normal range (rows of the short sequence are above it)
+    bound = (torch.finfo(dtype).eps / 2 + 2.0 ** -22) * exact + (2.0 ** -25 if dtype == torch.float16 else 0)
+    assert (err <= bound).all(), f"{np.max(err / np.maximum(exact, 1e-9)):.4f} of a value off"
