@@ -92,17 +92,19 @@ def _lend(given, index, handle, need, call, stream=None):
     and the larger one is kept.  Everything stays in the stream's order, so a
     workspace that is dropped or used again meets no work of its last call.
     A captured call's belongs to its graph: the stream's may be replaced by a
-    larger one, and another graph may run beside this one.  ``stream`` says
-    where to allocate if that is not the current stream."""
+    larger one, and another graph may run beside this one.  ``stream`` is the
+    call's, where the memory has to belong, if that is not the current one."""
     if given is not None:
         return call(given)
-    if torch.cuda.is_current_stream_capturing():
-        return call(torch.empty(need, dtype=torch.uint8, device=f"cuda:{index}"))
     key = (index, handle)
-    ws = _sp_cache.pop(key, None)
-    if ws is None or ws.numel() < need:
-        with torch.cuda.stream(stream):                  # None: where we are
-            ws = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{index}")
+    with torch.cuda.stream(stream):                      # None: where we are
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else _sp_cache.pop(key, None)
+        if ws is None or ws.numel() < need:
+            size = need if capturing else max(need, 1 << 20)
+            ws = torch.empty(size, dtype=torch.uint8, device=f"cuda:{index}")
+    if capturing:
+        return call(ws)
     try:
         return call(ws)
     finally:

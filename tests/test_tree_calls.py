@@ -140,6 +140,30 @@ def test_two_threads_on_one_stream_do_not_share_a_workspace(fake_library, one, o
         assert len(ops._sp_cache) in (1, 2) and all(w is a or w is b for w in ops._sp_cache.values())   # one a key
 
 
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_workspace_belongs_to_the_stream_of_the_call(monkeypatch, capturing):
+    # freed memory is used again in the order of the stream that it was allocated on: a captured call's, which is freed
+    # at once, and one that a larger one replaces
+    current, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, current[0] = current[0], stream or current[0]
+        yield
+        current[0] = before
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(current[0]) or empty(*a))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing and current[0] == "side")
+    monkeypatch.setattr(ops, "_sp_cache", {})
+    for need in (10, 1 << 21):
+        ops._lend(None, 0, 5, need, lambda ws: ws, "side")
+    assert made == ["side", "side"] and len(ops._sp_cache) == (0 if capturing else 1)
+    ops._lend(None, 0, 0, 10, lambda ws: ws)
+    assert made[2:] == [None]
+
+
 # ---------------------------------------------------------------- overlapping operands
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would start a kernel")
 @pytest.mark.parametrize("tokens", [1 << 20, 1 << 29, 1 << 30, (1 << 31) - 1])

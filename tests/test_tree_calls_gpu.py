@@ -246,6 +246,34 @@ def test_captured_decodes_share_nothing(kind):
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+@pytest.mark.parametrize("kind", ["decode", "multi", "tree"])
+def test_a_captured_branch_on_another_stream(kind):
+    # a graph with two branches that run at once, each with calls that pick their own workspaces
+    made = [small_tree(N=n, nodes=5, MB=60, seed=n) for n in (3, 6)]
+    calls = []
+    for t in made:
+        t["context_lens"] += 800
+        one = t["q"][:t["block_tables"].shape[0]].contiguous()
+        calls.append({"tree": lambda s, t=t: pa().pa_decode_tree(**t, stream=s),
+                      "multi": lambda s, t=t: pa().pa_decode_multi(**chunk_args(t), max_q_len=5, stream=s),
+                      "decode": lambda s, t=t, one=one: pa().pa_decode(one, t["k_pool"], t["v_pool"], t["block_tables"],
+                                                                       t["context_lens"], t["scale"], stream=s)}[kind])
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    side, graph, outs = torch.cuda.Stream(), torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        for _ in range(4):
+            outs.append((0, calls[0](side)))
+            outs.append((1, calls[1](None)))
+        here.wait_stream(side)
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in outs)
+
+
 # ---------------------------------------------------------------- rotary positions
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_frequencies_that_are_not_finite(interleaved):
