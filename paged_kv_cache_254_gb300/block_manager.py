@@ -133,15 +133,12 @@ class BlockManager:
         tokens = sum(self._len.values())
         used = self.num_used
         slots = used * self.block_size
-        unique_tokens = 0
-        seen = set()
+        fill: Dict[int, int] = {}                # tokens that some owner has in a block
         for s, blocks in self._blocks.items():
             n = self._len[s]
             for i, b in enumerate(blocks):
-                if b in seen:
-                    continue
-                seen.add(b)
-                unique_tokens += min(self.block_size, n - i * self.block_size)
+                fill[b] = max(fill.get(b, 0), min(self.block_size, n - i * self.block_size))
+        unique_tokens = sum(fill.values())
         return {
             "blocks_used": used,
             "blocks_free": len(self._free),
