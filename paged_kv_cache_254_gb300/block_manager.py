@@ -256,8 +256,9 @@ class BlockManager:
     def truncate(self, seq, length: int) -> None:
         """Cut a sequence back to its first ``length`` tokens (drafted tokens
         that were not accepted): whole blocks past them drop one reference and
-        go back to the free list at 0.  Queued copies into those blocks must
-        have been taken before."""
+        go back to the free list at 0.  Queued copies into those blocks, or
+        from one that goes back to the free list, must have been taken before:
+        the block could be another copy's destination in the same batch."""
         if seq not in self._blocks:
             raise KeyError(f"unknown sequence {seq!r}")
         length = int(length)
@@ -266,8 +267,8 @@ class BlockManager:
         blocks = self._blocks[seq]
         keep = -(-length // self.block_size)
         dropped = blocks[keep:]
-        if any(dst in dropped for _, dst in self._copies):
-            raise RuntimeError("take_copies() first: a queued copy writes a block to be dropped")
+        if any(dst in dropped or (src in dropped and self._ref[src] == 1) for src, dst in self._copies):
+            raise RuntimeError("take_copies() first: a queued copy writes or reads a block to be dropped")
         del blocks[keep:]
         for b in dropped:
             self._ref[b] -= 1
