@@ -25,7 +25,9 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling=None, factor: 
       times within original_len positions stays, one that turns less than
       beta_slow times is divided by factor, the ones between are blended
       linearly in their number of turns, and rope_scale is
-      0.1 ln(factor) + 1."""
+      0.1 ln(factor) + 1.  A checkpoint whose frequencies were blended
+      otherwise (linearly in the pair's index, with rounded ends) has others
+      in the middle band, by up to a factor of 3: give those as inv_freq."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be a positive even number")
     if not base > 0 or not factor >= 1:

@@ -294,3 +294,39 @@ def test_frequencies_that_are_not_finite(interleaved):
         nan[[2 * j, 2 * j + 1] if interleaved else [j, j + d // 2]] = True
     for a, b in ((got, want), (pools[2][0, :, :T], pools[0][0, :, :T])):
         assert torch.isnan(a[..., nan]).all() and torch.equal(a[..., ~nan], b[..., ~nan])
+
+
+# ---------------------------------------------------------------- large pools
+@pytest.mark.parametrize("nodes", [2, 12, 40])
+def test_blocks_past_32_bits_of_elements(nodes):
+    # the same step over a small pool and over one whose blocks lie past element 2^32 (and byte 2^33)
+    N, Hq, Hkv, d, B, MB = 2, 32, 8, 128, 16, 6
+    a = small_tree(N=N, nodes=nodes, Hq=Hq, Hkv=Hkv, d=d, B=B, MB=MB, seed=nodes)
+    a["context_lens"] += nodes                         # 50 tokens before each tree
+    NB = (1 << 32) // (Hkv * B * d) + 40
+    first = NB - N * MB
+    assert first * Hkv * B * d > 1 << 32
+    large = dict(a, block_tables=a["block_tables"] + first)
+    for name in ("k_pool", "v_pool"):
+        large[name] = torch.empty(NB, Hkv, B, d, dtype=torch.bfloat16, device="cuda")
+        large[name][first:] = a[name]
+    freq, _ = pa().rope_inv_freq(d)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T = N * nodes
+    k, v = (torch.randn(T, Hkv, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    at = torch.cat([torch.arange(int(c) - nodes, int(c), device="cuda") for c in a["context_lens"]])
+    tokens = torch.arange(T, device="cuda")
+    path = torch.full((N, nodes), -1, dtype=torch.int32, device="cuda")
+    path[:, 0] = nodes - 1
+
+    def step(x):
+        slots = x["block_tables"][tokens // nodes, at // B].long() * B + at % B
+        q = pa().pa_rope_append_kv(x["q"], k, v, at.int(), slots, x["k_pool"], x["v_pool"], freq)
+        out = pa().pa_decode_tree(**dict(x, q=q))
+        pa().pa_keep_kv(path, x["q_start"], x["context_lens"], x["block_tables"], x["k_pool"], x["v_pool"])
+        return q, out
+
+    for x, y in zip(step(a), step(large)):
+        assert torch.isfinite(x.float()).all() and torch.equal(x, y)
+    for name in ("k_pool", "v_pool"):
+        assert torch.equal(a[name], large[name][first:])
