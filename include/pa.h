@@ -383,8 +383,9 @@ pa_status pa_append_kv(const pa_shape* shape, int32_t num_tokens, const void* k_
  *     (a, b) -> (a c - b s, b c + a s),  c = scale cos(p f_j), s = scale sin(p f_j)
  * for the pairs j < rotary_dim / 2: (y_j, y_{j + rotary_dim / 2}), or
  * (y_{2j}, y_{2j + 1}) when interleaved; values from rotary_dim on pass through.
- * Angles are exact to 2^-32 of a turn at any int32 position.  Queries go to
- * q_out, keys and (untouched) values to the pools at slot_mapping[t] as in
+ * Angles lose no whole turns at any int32 position: they are off by less than 1e-7
+ * radians (one rounding to fp32 after an exact reduction) and sincospif's error.
+ * Queries go to q_out, keys and (untouched) values to the pools at slot_mapping[t] as in
  * pa_append_kv (a negative slot skips them; a slot past the pool sets
  * PA_DEVERR_SLOT and skips them; the token's queries are written all the same;
  * no slot appears twice in one call).

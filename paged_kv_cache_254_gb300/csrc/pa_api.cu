@@ -415,9 +415,16 @@ size_t multi_region_bytes(const pa_shape* s, int ctas, int rows) {
 
 // ---------------------------------------------------------------- drafted trees
 // A tree launch: up to 16 query rows per (sequence, KV head) pair on the
-// mma.sync kernel, up to 128 on the tcgen05 kernel's tile (the measurements at
-// kTcMinRows; a tree's masks change neither side), more on the two-tile kernel
-// in groups of up to 256 rows.
+// mma.sync kernel, up to 128 on the tcgen05 kernel's tile, more on the two-tile
+// kernel in groups of up to 256 rows.  Whole calls at the borders, us (8 KV heads,
+// d 128; sequences x tokens):
+//                      1 x 700  1 x 4000  8 x 4000  4 x 30000  256 x 1024-8192
+//   16 rows, mma.sync     20.4      26.6      44.0        102              787
+//            one tile     20.5      23.6      44.0        100              820
+//   128 rows, one tile    24.6      30.7      53.2        113              926
+//            two tiles    28.7      30.8      60.9        141             1245
+// Two mma.sync tiles (17 to 32 rows) are not built for trees: at 16 rows the other
+// kernel is even already but for large batches, where two tiles cost more (kTcMinRows).
 struct TreePlan {
     const MultiKernelInfo* k;
     int groups, group_nodes;     // row groups per tree, and the nodes of one

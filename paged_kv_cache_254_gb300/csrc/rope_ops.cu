@@ -13,9 +13,9 @@
 // Angles.  p f_j reaches 10^6 radians and more, where an fp32 product keeps no
 // digit of the turn.  Here the frequency is held as turns per position in
 // 64-bit fixed point, u_j = frac(f_j / 2 pi) * 2^64: p * u_j modulo 2^64 is the
-// fraction of a turn exactly (whole turns fall off the top; a negative p works
-// alike), with an error below p * 2^-64 turns.  Its top 32 bits go to
-// sincospif.  u_j comes from the fp32 frequency's mantissa times 1 / 2 pi in
+// fraction of a turn (whole turns fall off the top; a negative p works alike) with
+// an error below p * 2^-64 turns.  Its top 32 bits, as one fp32 number of half turns
+// (rounded by up to 2^-25), go to sincospif.  u_j comes from the fp32 frequency's mantissa times 1 / 2 pi in
 // integer arithmetic: no fp64 (2 operations per clock and SM here).  An infinite or
 // NaN frequency has no such number: its pairs' cosines and sines are NaN.
 //
@@ -29,7 +29,7 @@
 // group's loads, the next token's too, are under way meanwhile.  Few tokens are
 // split over several warps each.
 //
-// Measured: 8192 tokens of 64 / 8 heads, d 128, norm and rotation: 60 us, 0.82 of
+// Measured: 8192 tokens of 64 / 8 heads, d 128, norm and rotation: 62 us, 0.80 of
 // the copy bandwidth on 336 MB (first version, angles per lane and loads per
 // step: 95 us; angles shared and loads ahead: 64 us).  Asynchronous copies to
 // shared memory instead of the registers ahead, 4 to 10 steps deep, were no

@@ -12,11 +12,15 @@
 // that one's code about and cost it 3 to 4 % (8-token chunks 0.863 -> 0.902 ms).
 //
 // Measured: 256 sequences of 1024-8192 tokens, 8 nodes, 64 / 8 heads, d 128, bf16:
-// 0.85 ms, 5.8 TB/s, 0.85 of the copy bandwidth; 4 of 24576-32768, 24 nodes, 64 / 64
-// heads: 0.63 ms, 0.88.  Bound by the softmax warps' instructions next to HBM: in
+// 0.86 to 0.89 ms, 5.6 TB/s, 0.82 of the copy bandwidth; 4 of 24576-32768, 24 nodes,
+// 64 / 64 heads: 0.62 to 0.65 ms, 0.87.  Bound by the softmax warps' instructions next to HBM: in
 // scalar fp32 as for chunks it took 1.00 ms with the masks' code added, and stacking
 // the hi and lo weights of 64 rows in one product's 128 rows (two thirds of the MMAs)
 // 0.87.
+//
+// The tensor core cuts its fp32 sums where it could round them: 2 steps per 16 keys
+// draw the outputs towards zero by 2e-9 of their size per key that one CTA sums up
+// (6.5e-5 at 33,000 keys, 2.6e-4 at 131,000; half a step of bf16 is 2e-3 to 4e-3).
 #pragma once
 
 #include "multi_tc_kernel.cuh"

@@ -20,9 +20,10 @@
 // N = 64 takes as long.
 //
 // Measured: 64 sequences of 1024-8192 tokens, 64 nodes, 64 / 8 heads, d 128, bf16:
-// 0.765 ms, 0.80 PFLOP/s with each product counted once (0.41 of cuBLAS).  The
+// 0.76 to 0.79 ms, 0.79 PFLOP/s with each product counted once (0.40 of cuBLAS).  The
 // softmax is short of instructions, not of units: with its loops over the 128 scores
-// unrolled, the masks among them and both tiles in step it took 0.92 ms; 0.90 with
+// unrolled, the masks among them and both tiles in step it took 0.92 ms (on a box where it
+// takes 0.765 now); 0.90 with
 // the weights handed over by the quarter and the wait for the next keys before the
 // one for the products, 0.86 with rolled loops, 0.82 with the tiles apart, 0.77 with
 // masks and signs out of the loops.  16 softmax warps, two to a row, took 0.89 ms
