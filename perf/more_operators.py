@@ -1,8 +1,8 @@
 """The 8-bit cache with a scale for each block of tokens and KV head, as measured cases.
 
-The pool is ``uint8 [NB, Hkv, 2 * B * d + 32]``: per (block, KV head) the codes of B keys and of B values
-(E4M3 or E5M2, rows of d bytes whose 16-byte parts are permuted, see ``_places``), then the keys' and the
-values' scale (fp32), then 24 spare bytes.  Five calls use it:
+The pool is ``uint8 [NB, Hkv, 32 + 2 * B * d]``: per (block, KV head) the keys' and the values' scale
+(fp32), 24 spare bytes, then the codes of B keys and of B values (E4M3 or E5M2, rows of d bytes whose
+16-byte parts are permuted, see ``_places``).  Five calls use it:
 
 * ``append`` -- new tokens' keys and values quantised into their blocks; a block whose largest value grows
   gets a larger scale (a power of two) and its older codes are rounded to it (``pa_append_kv_bs8``);
@@ -140,7 +140,7 @@ def work(case):
 
 # ---------------------------------------------------------------- the pool
 def _places(B, d):
-    """Bytes of a piece at which dimension i of key row r, and of value row r, stand: [2, B, d].  The 16-byte
+    """Bytes of a piece's codes at which dimension i of key row r, and of value row r, stand: [2, B, d].  The 16-byte
     parts of a row are permuted, and with d 64 value rows 16 to 31 change places in pairs, so that a plain
     copy in shared memory is read without bank conflicts."""
     r, i = np.arange(B)[:, None], np.arange(d)[None, :]
@@ -156,8 +156,7 @@ def _places(B, d):
 
 def _views(s):
     """The pool's codes [NB, Hkv, 2 * B * d] as 8-bit floats, and its scales [NB, Hkv, 2]."""
-    n = 2 * s["block"] * s["head_dim"]
-    return s["pool"][..., :n].view(CODES[s["format"]]), s["pool"][..., n:n + 8].view(torch.float32)
+    return s["pool"][..., 32:].view(CODES[s["format"]]), s["pool"][..., :8].view(torch.float32)
 
 
 # ---------------------------------------------------------------- inputs
@@ -182,14 +181,14 @@ def _dev(a):
 def _pool(NB, case, gen):
     """A pool in use: codes up to the format's largest, scales as appended values of size one or so leave them."""
     n, hkv, fmt = 2 * case["block"] * case["head_dim"], case["kv_heads"], case["format"]
-    pool = torch.zeros((NB, hkv, n + 32), dtype=torch.uint8, device="cuda")
+    pool = torch.zeros((NB, hkv, 32 + n), dtype=torch.uint8, device="cuda")
     codes = torch.empty((NB, hkv, n), dtype=CODES[fmt], device="cuda")
     for lo in range(0, NB, 4096):
         part = codes[lo:lo + 4096]
         part.copy_((_normal(part.shape, torch.float32, gen) * (LARGEST[fmt] / 4.5)).clamp_(-LARGEST[fmt], LARGEST[fmt]))
-    pool[..., :n] = codes.view(torch.uint8)
+    pool[..., 32:] = codes.view(torch.uint8)
     step = torch.randint(-2, 2, (NB, hkv, 2), device="cuda", generator=gen) + 3 - EXPONENT[fmt]
-    pool[..., n:n + 8] = torch.exp2(step.float()).view(torch.uint8)
+    pool[..., :8] = torch.exp2(step.float()).view(torch.uint8)
     return pool
 
 
