@@ -64,6 +64,7 @@ typedef enum pa_dtype { PA_FP16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_FP8_E5M2 =
 #define PA_DEVERR_Q_RANGE   64u  /* a bf16 query element beyond fp16's finite range (8-bit and 4-bit
                                     caches, which compute in fp16); its rows are not finite */
 #define PA_DEVERR_PATH      128u /* accepted path not ascending, or past its tree */
+#define PA_DEVERR_SCALE     256u /* a block's scale is negative or not finite (block-scaled 8-bit cache) */
 
 typedef struct pa_shape {
     int32_t num_seqs;            /* N: sequences in the batch (>= 0) */
@@ -324,6 +325,115 @@ pa_status pa_append_kv_fp8(const pa_shape* shape, int32_t kv_format, int32_t num
 
 pa_status pa_copy_blocks_fp8(const pa_shape* shape, const int32_t* src_dst_pairs, int32_t num_pairs,
                              void* kv_pool, uint32_t* err_word, void* stream);
+
+/*
+ * 8-bit (FP8) KV cache with a scale for each block and KV head, for keys and for
+ * values ("bs8").  Storing keys and values in 8 bits halves the cache (ontq "AI
+ * Inference Serving at Scale", section 6); quantised formats carry scale factors per
+ * group (letsbuildsolutions "How LLM Inference Engines Work", quantization).  The
+ * scales follow the data: nothing has to be known of a model's keys and values.
+ *
+ * Layout: ONE pool of bytes [NB][Hkv][P], P = 32 + 2 * B * d, 32-byte aligned.  A piece
+ * holds the keys' scale and the values' scale (fp32, finite and not negative), 24 spare
+ * bytes, B key rows of d codes, B value rows of d codes.  A stored value is scale * code.  The 16-byte parts of a row are permuted: part c (dimensions 16 c .. 16 c + 15)
+ * of key row r stands at part c XOR (r mod 8) for d = 128 and at c for d = 64; of value
+ * row r at part c XOR 2 (r / 8 mod 4) for d = 128, and for d = 64 at part c XOR 2 (r / 8
+ * mod 2) of row r XOR (r / 16 mod 2).  A pool of zeros is a valid empty one.
+ *
+ * kv_format: PA_FP8_E4M3 or PA_FP8_E5M2, F its largest value (448, 57344).  Codes are
+ * rounded to nearest even; an infinity becomes the largest code, NaN stays NaN.
+ * Supported by every call: shape->dtype fp16 or bf16 (queries, outputs, new values, the
+ * 16-bit pools), d in {64, 128}, B in {16, 32}.
+ */
+
+/*
+ * Append new tokens' keys and values.  Sequence b brings n_b = q_start[b + 1] -
+ * q_start[b] tokens (rows q_start[b] .. of k_new and v_new), which become its last n_b
+ * cached tokens: context_lens count them, and their blocks stand in the table.  In each
+ * block that they fall into, for each KV head, keys and values apart:
+ *     need = 2^e, e >= -126 the smallest with max |x| <= F 2^e over the finite new x
+ *     s'   = max(s, need), s the block's scale, or 0 when its first slot is written
+ *     older codes c of the block become code(c * (s / s')) when s' > s
+ *     new codes are code(x / s')
+ * A block's first slot starts it afresh, whatever it holds (a block off the free list).
+ * Blocks that new tokens fall into belong to one sequence each (copy-on-write has run
+ * before).  A malformed sequence (n_b < 0, n_b > max_new, n_b > its context, rows
+ * outside [0, total_new), a context past its table) sets PA_DEVERR_CONTEXT and appends
+ * nothing; a bad block id (PA_DEVERR_BLOCK_ID) or scale (PA_DEVERR_SCALE) leaves that
+ * piece as it was.
+ *
+ *   max_new           largest n_b of the call (>= 1)
+ *   k_new, v_new      [total_new] rows of [Hkv][d], consecutive tokens k_stride, v_stride
+ *                     elements apart (multiples of 8): the parts of one projection's output
+ *                     need no copy; not inside the pool
+ *   q_start           int32 [N + 1], non-decreasing
+ * Uses shape->num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+ * max_blocks_per_seq, dtype.  One launch.
+ */
+pa_status pa_append_kv_bs8(const pa_shape* shape, int32_t kv_format, int32_t max_new, int32_t total_new,
+                           const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                           const int32_t* q_start, const int32_t* block_tables, const int32_t* context_lens,
+                           void* kv_pool, uint32_t* err_word, void* stream);
+
+/*
+ * pa_decode over the block-scaled pool: attention over K = scale * code, V = scale * code
+ * of each piece, with any scales (not only appended ones).  Computed in fp16 on the
+ * tensor cores with fp32 sums: codes are exact in fp16, a bf16 query row is brought into
+ * fp16's range by a power of two (values below 2^-29 of the row's largest lose bits),
+ * softmax weights are rounded once to fp16 in proportion to their share of the output.  A
+ * bad scale sets PA_DEVERR_SCALE, and the rows that read it are NaN.  A value scale below
+ * 2^-126 counts as that.  out must not overlap q.  Other arguments, supported groups,
+ * errors and launches as pa_decode.
+ */
+size_t pa_decode_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format);
+
+pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q, const void* kv_pool,
+                        const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                        void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream);
+
+/*
+ * Chunks of new tokens over the block-scaled pool: pa_decode_multi (causal within the
+ * chunk), with chunks of any length: drafted tokens to verify, or a prompt (chunked
+ * prefill -- thewebvale "vLLM & High-Throughput Serving", section 4).  max_q_len: the
+ * largest n_b of the call (>= 1); a longer chunk is malformed.  Arithmetic as
+ * pa_decode_bs8.  NaN or an infinity in a value of the chunk's own tokens makes the rows
+ * that see it NaN and no others.  Rows of out outside every chunk are left as they are.
+ * out must not overlap q.  Two launches: attention, then the merge of split rows.
+ */
+size_t pa_decode_multi_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format, int32_t max_q_len);
+
+pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t max_q_len, int32_t total_q,
+                              const void* q, const int32_t* q_start, const void* kv_pool,
+                              const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                              void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream);
+
+/*
+ * Copy-on-write copies of whole blocks (codes and scales) of the block-scaled pool, as
+ * pa_copy_blocks.  shape->dtype: either 16-bit type.
+ */
+pa_status pa_copy_blocks_bs8(const pa_shape* shape, const int32_t* src_dst_pairs, int32_t num_pairs, void* kv_pool,
+                             uint32_t* err_word, void* stream);
+
+/*
+ * Whole blocks of a 16-bit cache into the block-scaled pool, and back: for each pair (src,
+ * dst), every slot and KV head.  Packing gives a piece the scales that its values need (see
+ * pa_append_kv_bs8, as a block started afresh); unpacking rounds scale * code to the 16-bit
+ * type.  Blocks that are served seldom take half the room packed; calls that read 16-bit
+ * pools alone (trees, shared prefixes) get them back.  A dst must not appear twice in one
+ * call.  A pair outside its pools sets PA_DEVERR_COPY_PAIR and is skipped; a bad scale sets
+ * PA_DEVERR_SCALE, and its values come out as NaN.
+ *
+ *   shape->num_blocks   blocks of kv_pool; num_blocks16: blocks of k_pool and v_pool
+ *   src_dst_pairs       int32 [num_pairs][2] (device)
+ * One launch.
+ */
+pa_status pa_pack_blocks_bs8(const pa_shape* shape, int32_t kv_format, int32_t num_blocks16,
+                             const int32_t* src_dst_pairs, int32_t num_pairs, const void* k_pool, const void* v_pool,
+                             void* kv_pool, uint32_t* err_word, void* stream);
+
+pa_status pa_unpack_blocks_bs8(const pa_shape* shape, int32_t kv_format, int32_t num_blocks16,
+                               const int32_t* src_dst_pairs, int32_t num_pairs, const void* kv_pool, void* k_pool,
+                               void* v_pool, uint32_t* err_word, void* stream);
 
 /*
  * Prefix-aware paged decode: the same results as pa_decode (up to rounding

@@ -6,6 +6,11 @@
   ``pa_keep_kv`` -- a step of tree speculation over the cache: norms and rotary
   positions with the append, tree attention, the accepted path, and its tokens
   moved into place.  ``rope_inv_freq`` and ``tree_masks`` prepare their inputs.
+* ``pa_append_kv_bs8``, ``pa_decode_bs8``, ``pa_decode_multi_bs8``,
+  ``pa_copy_blocks_bs8``, ``pa_pack_blocks_bs8``, ``pa_unpack_blocks_bs8`` -- the
+  8-bit cache with a scale for each block and KV head: quantising append, single
+  tokens and chunks of any length over it, copy-on-write, and whole blocks from
+  and to a 16-bit cache.  ``bs8_pool`` makes an empty pool.
 * ``BlockManager`` -- host bookkeeping that builds block tables, slot
   mappings and copy-on-write copy lists.
 
@@ -39,6 +44,14 @@ from .ops import (  # noqa: F401
     pa_keep_kv,
     pa_rope_append_kv,
     workspace_for,
+    bs8_pool,
+    bs8_scales,
+    pa_append_kv_bs8,
+    pa_copy_blocks_bs8,
+    pa_decode_bs8,
+    pa_decode_multi_bs8,
+    pa_pack_blocks_bs8,
+    pa_unpack_blocks_bs8,
 )
 
 __version__ = "0.1.0"

@@ -24,7 +24,7 @@ STATUS_NAMES = {
 }
 PA_FP16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2 = 0, 1, 2, 3
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_SLOT, DEVERR_COPY_PAIR, DEVERR_TIMEOUT, DEVERR_GROUP = 1, 2, 4, 8, 16, 32
-DEVERR_Q_RANGE, DEVERR_PATH = 64, 128
+DEVERR_Q_RANGE, DEVERR_PATH, DEVERR_SCALE = 64, 128, 256
 
 # Every symbol include/pa.h declares.
 EXPORTS = ("pa_decode_workspace_bytes", "pa_decode", "pa_append_kv", "pa_copy_blocks", "pa_read_error",
@@ -33,7 +33,9 @@ EXPORTS = ("pa_decode_workspace_bytes", "pa_decode", "pa_append_kv", "pa_copy_bl
            "pa_copy_blocks_fp8", "pa_decode_multi_workspace_bytes", "pa_decode_multi",
            "pa_decode_int4_workspace_bytes", "pa_decode_int4", "pa_append_kv_int4", "pa_copy_blocks_int4",
            "pa_set_decode_stall_ns", "pa_decode_tree_workspace_bytes", "pa_decode_tree", "pa_tree_verify",
-           "pa_keep_kv", "pa_rope_append_kv")
+           "pa_keep_kv", "pa_rope_append_kv", "pa_append_kv_bs8", "pa_decode_bs8_workspace_bytes", "pa_decode_bs8",
+           "pa_copy_blocks_bs8", "pa_pack_blocks_bs8", "pa_unpack_blocks_bs8", "pa_decode_multi_bs8_workspace_bytes",
+           "pa_decode_multi_bs8")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -145,6 +147,22 @@ def load() -> ctypes.CDLL:
         I64 = ctypes.c_int64
         lib.pa_rope_append_kv.argtypes = [SP, ctypes.POINTER(PaRope), I32, P, I64, P, I64, P, I64, P, P, P, P, P, P, P]
         lib.pa_rope_append_kv.restype = I32
+        lib.pa_append_kv_bs8.argtypes = [SP, I32, I32, I32, P, I64, P, I64, P, P, P, P, P, P]
+        lib.pa_append_kv_bs8.restype = I32
+        lib.pa_decode_bs8_workspace_bytes.argtypes = [SP, I32]
+        lib.pa_decode_bs8_workspace_bytes.restype = SZ
+        lib.pa_decode_bs8.argtypes = [SP, I32, P, P, P, P, F, P, P, SZ, P, P]
+        lib.pa_decode_bs8.restype = I32
+        lib.pa_decode_multi_bs8_workspace_bytes.argtypes = [SP, I32, I32]
+        lib.pa_decode_multi_bs8_workspace_bytes.restype = SZ
+        lib.pa_decode_multi_bs8.argtypes = [SP, I32, I32, I32, P, P, P, P, P, F, P, P, SZ, P, P]
+        lib.pa_decode_multi_bs8.restype = I32
+        lib.pa_copy_blocks_bs8.argtypes = [SP, P, I32, P, P, P]
+        lib.pa_copy_blocks_bs8.restype = I32
+        lib.pa_pack_blocks_bs8.argtypes = [SP, I32, I32, P, I32, P, P, P, P, P]
+        lib.pa_pack_blocks_bs8.restype = I32
+        lib.pa_unpack_blocks_bs8.argtypes = [SP, I32, I32, P, I32, P, P, P, P, P]
+        lib.pa_unpack_blocks_bs8.restype = I32
         _lib = lib
         return lib
 
@@ -160,7 +178,8 @@ class _Declining:
     def decode_tree(*args):
         return NotImplemented
 
-    tree_verify = keep_kv = rope_append_kv = decode_tree
+    tree_verify = keep_kv = rope_append_kv = append_kv_bs8 = decode_bs8 = decode_tree
+    decode_multi_bs8 = decode_tree
 
 
 def load_fast():

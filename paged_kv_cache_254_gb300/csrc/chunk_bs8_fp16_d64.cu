@@ -1,0 +1,17 @@
+// Instantiations of the chunk kernel over the 8-bit cache with a scale per block and head, fp16 queries, head_dim 64.
+#include "chunk_bs8_kernel.cuh"
+
+namespace pa {
+
+void chunk_bs8_table_fp16_d64(MultiKernelInfo (&t)[2][2][2]) {
+    t[0][0][0] = chunk_bs8_info<ChunkTraits<64, 16, false, false, true>>();
+    t[0][0][1] = chunk_bs8_info<ChunkTraits<64, 16, false, false, false>>();
+    t[0][1][0] = chunk_bs8_info<ChunkTraits<64, 32, false, false, true>>();
+    t[0][1][1] = chunk_bs8_info<ChunkTraits<64, 32, false, false, false>>();
+    t[1][0][0] = chunk_bs8_info<ChunkTraits<64, 16, false, true, true>>();
+    t[1][0][1] = chunk_bs8_info<ChunkTraits<64, 16, false, true, false>>();
+    t[1][1][0] = chunk_bs8_info<ChunkTraits<64, 32, false, true, true>>();
+    t[1][1][1] = chunk_bs8_info<ChunkTraits<64, 32, false, true, false>>();
+}
+
+}  // namespace pa

@@ -1,0 +1,17 @@
+// Instantiations of the paged decode kernel over the 8-bit cache with a scale per block and head, fp16 queries, head_dim 64.
+#include "decode_kernel.cuh"
+
+namespace pa {
+
+void decode_bs8_table_fp16_d64(DecodeKernelInfo (&t)[2][2][2]) {
+    t[0][0][0] = decode_info<DecodeTraits<64, 16, 8, false, 4>>();
+    t[0][0][1] = decode_info<DecodeTraits<64, 16, 16, false, 4>>();
+    t[0][1][0] = decode_info<DecodeTraits<64, 32, 8, false, 4>>();
+    t[0][1][1] = decode_info<DecodeTraits<64, 32, 16, false, 4>>();
+    t[1][0][0] = decode_info<DecodeTraits<64, 16, 8, false, 5>>();
+    t[1][0][1] = decode_info<DecodeTraits<64, 16, 16, false, 5>>();
+    t[1][1][0] = decode_info<DecodeTraits<64, 32, 8, false, 5>>();
+    t[1][1][1] = decode_info<DecodeTraits<64, 32, 16, false, 5>>();
+}
+
+}  // namespace pa

@@ -269,8 +269,8 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 }
 
 // Q fragments for the 8-bit path with the head dims in the order the K bytes
-// are read: k-step kk, fragment column 2 t4 + e -> dim 32 t4 + 4 kk + e,
-// column 2 t4 + 8 + e -> dim 32 t4 + 4 kk + 2 + e.  Loaded as stored (q's
+// are read: k-step kk, fragment column 2 t4 + e -> dim D / 4 t4 + 4 kk + e,
+// column 2 t4 + 8 + e -> dim D / 4 t4 + 4 kk + 2 + e.  Loaded as stored (q's
 // 16-bit type); q_frags8_to_f16 then turns bf16 pairs into fp16 pairs.
 template <int D>
 __device__ __forceinline__ void load_q_frags8(uint32_t (&qa)[D / 16][4], const uint16_t* row0,
@@ -278,7 +278,7 @@ __device__ __forceinline__ void load_q_frags8(uint32_t (&qa)[D / 16][4], const u
     auto ld = [](const uint16_t* p) -> uint32_t { return __ldg(reinterpret_cast<const uint32_t*>(p)); };
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        const int c = 32 * t4 + 4 * kk;
+        const int c = D / 4 * t4 + 4 * kk;
         qa[kk][0] = row0 ? ld(row0 + c) : 0u;
         qa[kk][2] = row0 ? ld(row0 + c + 2) : 0u;
         qa[kk][1] = row1 ? ld(row1 + c) : 0u;

@@ -54,6 +54,7 @@
 
 #include "decode_common.cuh"
 #include "decode_tok.cuh"
+#include "decode_bs8.cuh"
 
 namespace pa {
 
@@ -92,27 +93,32 @@ constexpr int stage_data_bytes() {
 }
 
 // KVF: 0 = the cache holds q's 16-bit type; 1 = FP8 E4M3 codes; 2 = FP8 E5M2;
-// 3 = 4-bit integer codes with per-row scales.  KV8: any quantized cache (one
-// contiguous piece per (block, head), fetched by bulk copies).
+// 3 = 4-bit integer codes with per-row scales; 4 = FP8 E4M3 codes with a scale
+// per block and head, 5 = FP8 E5M2 so.  KV8: any quantized cache (one
+// contiguous piece per (block, head), fetched by bulk copies).  For 4 and 5 (B8) G_
+// is the most query heads of a group, 8 or 16; the launch's own count is Hq / Hkv.
 template <int D_, int BS_, int G_, bool BF16_, int KVF_ = 0>
 struct DecodeTraits {
     static constexpr bool KV8 = KVF_ != 0;
     static constexpr bool I4 = KVF_ == 3;
-    using Gm = std::conditional_t<I4, Geom4<BS_>, std::conditional_t<KV8, Geom8<BS_>, Geom<D_, BS_>>>;
+    static constexpr bool B8 = KVF_ >= 4;
+    using Gm = std::conditional_t<B8, GeomB8<D_, BS_>,
+                                  std::conditional_t<I4, Geom4<BS_>, std::conditional_t<KV8, Geom8<BS_>, Geom<D_, BS_>>>>;
     static constexpr int D = D_;
     static constexpr int BS = BS_;
     static constexpr int UB = Gm::UB;                       // blocks per stage
     static constexpr int G = G_;
     static constexpr bool BF16 = BF16_;
-    static constexpr bool E5M2 = KVF_ == 2;
+    static constexpr bool E5M2 = KVF_ == 2 || KVF_ == 5;
     // About 192 KiB of stages per SM (200 KiB for the quantized caches, whose
     // two-piece stages carry 64 bytes of bank padding): stages of up to 8 KiB
     // of data, two CTAs of four warps; 16 KiB stages, one CTA of six warps.
+    // The 8-bit cache with scales in its pieces: as the 8-bit one (8.1 KiB, 4.1 KiB at D 64).
     // The 4-bit cache: 64-token stages (8.6 KiB), two CTAs of four warps with
     // three stages each (212 KB of copies in flight per SM).
     static constexpr int RING_PER_SM = (KV8 ? 200 : 192) * 1024;
     static constexpr int DATA_BYTES = stage_data_bytes<Gm, KV8>();
-    static constexpr int MIN_CTAS = I4 ? 2 : DATA_BYTES <= 8192 ? 2 : 1;
+    static constexpr int MIN_CTAS = I4 || B8 ? 2 : DATA_BYTES <= 8192 ? 2 : 1;
     static constexpr int NW = MIN_CTAS == 1 ? 6 : 4;       // warps (workers) per CTA
     static constexpr int R_FIT = RING_PER_SM / (MIN_CTAS * NW * Gm::STAGE_BYTES);
     // stages per warp (the 4-bit cache: see above)
@@ -121,7 +127,7 @@ struct DecodeTraits {
     static constexpr int NR = G > 8 ? 2 : 1;                // 8-row groups of query heads in use
     // quantized caches: the stage's tokens are the MMA rows (decode_tok.cuh)
     static constexpr bool TR = KV8;
-    using Acc = std::conditional_t<TR, WarpAccT<D_, NR>, WarpAcc<D_, NR>>;
+    using Acc = std::conditional_t<B8, WarpAccB8<D_, NR>, std::conditional_t<TR, WarpAccT<D_, NR>, WarpAcc<D_, NR>>>;
     static constexpr int PSTRIDE = D_ + 4;                  // partial row: o[D], m, l, 2 pad (16-byte rows)
     static constexpr int CSTRIDE = D_ + 2;                  // carry row (prefix pass): o[D], m, l
     static constexpr int CUM_SMEM = I4 ? 256 : 512;         // sequences whose tables fit in smem
@@ -254,7 +260,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_CTAS)
 pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const DecodeParams p) {
     using Gm = typename Tr::Gm;
-    constexpr int D = Tr::D, BS = Tr::BS, G = Tr::G, NW = Tr::NW, R = Tr::R, UB = Tr::UB;
+    constexpr int D = Tr::D, BS = Tr::BS, NW = Tr::NW, R = Tr::R, UB = Tr::UB;
+    const int G = Tr::B8 ? p.Hq / p.Hkv : Tr::G;              // query heads of a group
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + (Tr::ALIGN - 1)) &
                                                ~uintptr_t(Tr::ALIGN - 1));
@@ -495,7 +502,7 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     auto load_q = [&](uint32_t (&qa)[Gm::KD][4], const SegIter& sg) {
         const uint16_t* qrow = p.q + ((size_t)sg.s * p.Hq + (size_t)sg.kvh * G) * D;
         const uint16_t* r0 = g < G ? qrow + g * D : nullptr;
-        const uint16_t* r1 = (G > 8) ? qrow + (g + 8) * D : nullptr;
+        const uint16_t* r1 = (Tr::G > 8) ? qrow + (g + 8) * D : nullptr;
         if constexpr (Tr::KV8) {
             load_q_frags8<D>(qa, r0, r1, t4);
         } else {
@@ -525,8 +532,11 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     uint32_t qa[Gm::KD][4];
     load_q(qa, it);
     float qc[Tr::NR][2];   // 4-bit cache: the code offset per head (prepare_q4)
+    float qf[Tr::NR][2];   // B8: the score factor of each of the lane's heads
     auto q_to_f16 = [&]() {
-        if constexpr (Tr::KV8) {
+        if constexpr (Tr::B8) {
+            normalise_q<Tr::BF16, Gm::KD, Tr::NR>(qa, qf, p.scale_log2, lane);
+        } else if constexpr (Tr::KV8) {
             if (__any_sync(0xffffffffu, q_frags8_to_f16<D, Tr::BF16>(qa)) && lane == 0)
                 set_err(p.err, PA_DEVERR_Q_RANGE);
         }
@@ -625,7 +635,12 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const int valid = min(nblk * BS, ctx - (it.first + it.b0 + b) * BS);
             const uint32_t kb = ring + st * Gm::STAGE_BYTES;
             bool zeroed = false;
-            if constexpr (Tr::I4) {
+            if constexpr (Tr::B8) {
+                if (!consume_stage_b8<Gm, Tr::NR, Tr::E5M2>(kb, valid, qa, qf, acc, lane)) {
+                    poisoned = 1;
+                    if (lane == 0) set_err(p.err, PA_DEVERR_SCALE);
+                }
+            } else if constexpr (Tr::I4) {
                 consume_stage4t<Gm, Tr::NR>(kb, valid, qa, qc, acc, p.scale_log2, lane);
             } else if constexpr (Tr::KV8) {
                 consume_stage8t<Gm, Tr::NR, Tr::E5M2>(kb, valid, qa, acc, p.scale_log2, lane);
@@ -669,7 +684,10 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         const long long clast = sc.of(P0 + it.nb - 1);
         const bool complete = cfirst == clast;
         uint16_t* orow = p.out + ((size_t)it.s * p.Hq + (size_t)it.kvh * G) * D;
-        if (complete) {
+        if constexpr (Tr::B8) {
+            float* prow = p.partials + ((size_t)cid * 2 + (it.gi == clo ? 0 : 1)) * G * Tr::PSTRIDE;
+            store_b8<D, Tr::NR, Tr::BF16>(acc, complete, poisoned, G, orow, prow, lane);
+        } else if (complete) {
 #pragma unroll
             for (int r = 0; r < Tr::NR; ++r) {
                 // this lane's o columns are heads 8 r + 2 t4 and 8 r + 2 t4 + 1
@@ -898,6 +916,11 @@ void decode8_table_fp16(DecodeKernelInfo (&t)[2][2][5]);
 // 4-bit cache: [bs == 32][log2(g)]
 void decode4_table_bf16(DecodeKernelInfo (&t)[2][5]);
 void decode4_table_fp16(DecodeKernelInfo (&t)[2][5]);
+// the 8-bit cache with a scale per block and head: [e5m2][bs == 32][more than 8 heads a group]
+void decode_bs8_table_bf16_d128(DecodeKernelInfo (&t)[2][2][2]);
+void decode_bs8_table_bf16_d64(DecodeKernelInfo (&t)[2][2][2]);
+void decode_bs8_table_fp16_d128(DecodeKernelInfo (&t)[2][2][2]);
+void decode_bs8_table_fp16_d64(DecodeKernelInfo (&t)[2][2][2]);
 void decode_table_bf16_d128(DecodeKernelInfo (&t)[2][5]);
 void decode_table_bf16_d64(DecodeKernelInfo (&t)[2][5]);
 void decode_table_fp16_d128(DecodeKernelInfo (&t)[2][5]);

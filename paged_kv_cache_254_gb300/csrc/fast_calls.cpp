@@ -1,4 +1,4 @@
-// The host side of the tree-speculation calls, compiled: argument checks, output
+// The host side of the tree-speculation calls and of those on the block-scaled 8-bit cache, compiled: argument checks, output
 // allocation and the call into libpa for arguments that are all in order.
 //
 // These kernels run for 2 to 20 microseconds, and the same steps take 10 to 20 in
@@ -98,6 +98,22 @@ at::Tensor part(const at::Tensor& whole, at::ScalarType t, at::IntArrayRef sizes
     impl->set_storage_offset(at);
     impl->set_sizes_contiguous(sizes);
     return at::Tensor(std::move(impl));
+}
+
+// The workspace of a call: the one given, or the one kept for the stream in the dict `kept` if
+// need() bytes fit into it; else null.  From here to the end of the call the interpreter lock
+// stays held, so no other thread takes the stream's workspace or queues a call that uses it;
+// while one that runs without the lock uses it, it is not in the dict.
+template <class F>
+const at::Tensor* workspace(PyObject* kept, PyObject* given, int dev, void* stream, F need) {
+    if (given != Py_None)
+        return THPVariable_Check(given) ? tensor(given, THPVariable_Unpack(given).scalar_type(), dev) : nullptr;
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return nullptr;
+    PyObject* key = Py_BuildValue("(iK)", dev, (unsigned long long)(uintptr_t)stream);
+    PyObject* found = key ? PyDict_GetItem(kept, key) : nullptr;             // borrowed
+    Py_XDECREF(key);
+    const at::Tensor* ws = found ? tensor(found, at::kByte, dev) : nullptr;
+    return ws && ws->nbytes() >= need() ? ws : nullptr;
 }
 
 // Runs `f` and turns a C++ exception (an allocation that failed) into NotImplemented.
@@ -207,20 +223,8 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
         s.max_blocks_per_seq = (int32_t)table->size(1);
         void* stream = stream_of(dev);
         const at::Tensor out = given ? *given : at::empty_like(*q);
-        // From here to the end of the call the interpreter lock stays held, so no other thread
-        // takes the stream's workspace or queues a call that uses it; while one that runs
-        // without the lock uses it, it is not in the dict.
-        const at::Tensor* ws = nullptr;
-        if (a[11] != Py_None) {
-            if (!THPVariable_Check(a[11])) return declined();
-            ws = tensor(a[11], THPVariable_Unpack(a[11]).scalar_type(), dev);
-        } else if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) {
-            PyObject* key = Py_BuildValue("(iK)", dev, (unsigned long long)(uintptr_t)stream);
-            PyObject* kept = key ? PyDict_GetItem(a[0], key) : nullptr;      // borrowed
-            Py_XDECREF(key);
-            if (kept) ws = tensor(kept, at::kByte, dev);
-            if (ws && ws->nbytes() < pa_decode_tree_workspace_bytes(&s, (int32_t)P)) ws = nullptr;
-        }
+        const at::Tensor* ws =
+            workspace(a[0], a[11], dev, stream, [&] { return pa_decode_tree_workspace_bytes(&s, (int32_t)P); });
         if (!ws) return declined();
         const pa_status st =
             pa_decode_tree(&s, (int32_t)P, (int32_t)T, data<void>(q), data<int32_t>(start), data<uint64_t>(masks),
@@ -284,8 +288,130 @@ PyObject* rope_append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------------------- block-scaled 8-bit cache
+constexpr int64_t BS8_HEAD = 32;
+
+// A pool uint8 [NB, Hkv, 32 + 2 * B * d] for values [.., d] of type t, as a shape; null if it is not that.
+const at::Tensor* bs8_shape(PyObject* o, at::ScalarType t, int64_t d, int dev, pa_shape& s) {
+    const at::Tensor* pool = tensor(o, at::kByte, dev);
+    if (!pool || pool->dim() != 3 || (t != at::kHalf && t != at::kBFloat16) || d < 1) return nullptr;
+    const int64_t NB = pool->size(0), Hkv = pool->size(1), n = pool->size(2) - BS8_HEAD;
+    if (!fits_int(NB) || !fits_int(Hkv) || !fits_int(n) || !fits_int(d) || n % (2 * d)) return nullptr;
+    s = pa_shape{0, (int32_t)Hkv, (int32_t)Hkv, (int32_t)d, (int32_t)(n / (2 * d)), (int32_t)NB, 1,
+                 t == at::kBFloat16 ? PA_BF16 : PA_FP16};
+    return pool;
+}
+
+// Tables int32 [N, MB] and lengths int32 [N], into the shape; false if they are not that.
+bool sequences(PyObject* tables, PyObject* lens, int dev, const at::Tensor*& table, const at::Tensor*& ctx, pa_shape& s) {
+    table = tensor(tables, at::kInt, dev);
+    ctx = tensor(lens, at::kInt, dev);
+    if (!table || !ctx || table->dim() != 2 || !fits_int(table->size(0)) || !fits_int(table->size(1)) ||
+        !is_shape(*ctx, {table->size(0)}))
+        return false;
+    s.num_seqs = (int32_t)table->size(0);
+    s.max_blocks_per_seq = (int32_t)table->size(1);
+    return true;
+}
+
+// An int that fits 32 bits and is not negative; -1 if it is not that.
+int32_t small_int(PyObject* o) {
+    if (!PyLong_Check(o)) return -1;
+    const long v = PyLong_AsLong(o);
+    if (v < 0 || v > 0x7fffffff) {
+        PyErr_Clear();
+        return -1;
+    }
+    return (int32_t)v;
+}
+
+// (k_new, v_new, block_tables, context_lens, q_start, kv_pool, format, max_new, err)
+PyObject* append_kv_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 9 || !THPVariable_Check(a[0])) return declined();
+        const int dev = device_of(a[5]);
+        const at::Tensor& k_any = THPVariable_Unpack(a[0]);
+        const int32_t fmt = small_int(a[6]), max_new = small_int(a[7]);
+        if (dev < 0 || fmt < 0 || max_new < 1 || k_any.dim() != 3) return declined();
+        const at::ScalarType t = k_any.scalar_type();
+        const int64_t T = k_any.size(0), Hkv = k_any.size(1), d = k_any.size(2);
+        pa_shape s;
+        const at::Tensor *pool = bs8_shape(a[5], t, d, dev, s), *k, *v, *table, *ctx, *err;
+        if (!pool || s.num_kv_heads != Hkv || !fits_int(T)) return declined();
+        const int64_t ks = token_stride(a[0], t, dev, T, Hkv, d, k), vs = token_stride(a[1], t, dev, T, Hkv, d, v);
+        const at::Tensor* start = tensor(a[4], at::kInt, dev);
+        if (ks < 0 || vs < 0 || !sequences(a[2], a[3], dev, table, ctx, s) || !start ||
+            !is_shape(*start, {(int64_t)s.num_seqs + 1}) || !optional(a[8], at::kInt, dev, err))
+            return declined();
+        const pa_status st =
+            pa_append_kv_bs8(&s, fmt, max_new, (int32_t)T, data<void>(k), ks, data<void>(v), vs, data<int32_t>(start),
+                             data<int32_t>(table), data<int32_t>(ctx), data<void>(pool), data<uint32_t>(err), stream_of(dev));
+        if (st != PA_OK) return refused(st, "pa_append_kv_bs8");
+        Py_RETURN_NONE;
+    });
+}
+
+// (workspaces, q, kv_pool, block_tables, context_lens, scale, format, out, workspace, err)
+PyObject* decode_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 10 || !THPVariable_Check(a[1]) || !PyFloat_Check(a[5])) return declined();
+        const int dev = device_of(a[1]);
+        const at::Tensor& q_any = THPVariable_Unpack(a[1]);
+        const int32_t fmt = small_int(a[6]);
+        if (dev < 0 || fmt < 0 || q_any.dim() != 3) return declined();
+        const at::ScalarType t = q_any.scalar_type();
+        pa_shape s;
+        const at::Tensor *q = tensor(a[1], t, dev), *pool = bs8_shape(a[2], t, q_any.size(2), dev, s), *table, *ctx, *given, *err;
+        if (!q || !pool || !sequences(a[3], a[4], dev, table, ctx, s) || q->size(0) != s.num_seqs || !fits_int(q->size(1)) ||
+            !optional(a[7], t, dev, given) || (given && given->sizes() != q->sizes()) || !optional(a[9], at::kInt, dev, err))
+            return declined();
+        s.num_q_heads = (int32_t)q->size(1);
+        void* stream = stream_of(dev);
+        const at::Tensor out = given ? *given : at::empty_like(*q);
+        const at::Tensor* ws = workspace(a[0], a[8], dev, stream, [&] { return pa_decode_bs8_workspace_bytes(&s, fmt); });
+        if (!ws) return declined();
+        const pa_status st = pa_decode_bs8(&s, fmt, data<void>(q), data<void>(pool), data<int32_t>(table), data<int32_t>(ctx),
+                                           (float)PyFloat_AS_DOUBLE(a[5]), data<void>(&out), data<void>(ws), ws->nbytes(),
+                                           data<uint32_t>(err), stream);
+        if (st != PA_OK) return refused(st, "pa_decode_bs8");
+        return given ? Py_NewRef(a[7]) : THPVariable_Wrap(out);
+    });
+}
+
+// (workspaces, q, kv_pool, block_tables, context_lens, q_start, scale, format, max_q_len, out, workspace, err)
+PyObject* decode_multi_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 12 || !THPVariable_Check(a[1]) || !PyFloat_Check(a[6])) return declined();
+        const int dev = device_of(a[1]);
+        const at::Tensor& q_any = THPVariable_Unpack(a[1]);
+        const int32_t fmt = small_int(a[7]), most = small_int(a[8]);
+        if (dev < 0 || fmt < 0 || most < 1 || q_any.dim() != 3) return declined();
+        const at::ScalarType t = q_any.scalar_type();
+        pa_shape s;
+        const at::Tensor *q = tensor(a[1], t, dev), *pool = bs8_shape(a[2], t, q_any.size(2), dev, s), *table, *ctx, *given, *err;
+        const at::Tensor* start = tensor(a[5], at::kInt, dev);
+        if (!q || !pool || !sequences(a[3], a[4], dev, table, ctx, s) || !fits_int(q->size(0)) || !fits_int(q->size(1)) ||
+            !start || !is_shape(*start, {(int64_t)s.num_seqs + 1}) || !optional(a[9], t, dev, given) ||
+            (given && given->sizes() != q->sizes()) || !optional(a[11], at::kInt, dev, err))
+            return declined();
+        s.num_q_heads = (int32_t)q->size(1);
+        void* stream = stream_of(dev);
+        const at::Tensor out = given ? *given : at::empty_like(*q);
+        const at::Tensor* ws =
+            workspace(a[0], a[10], dev, stream, [&] { return pa_decode_multi_bs8_workspace_bytes(&s, fmt, most); });
+        if (!ws) return declined();
+        const pa_status st =
+            pa_decode_multi_bs8(&s, fmt, most, (int32_t)q->size(0), data<void>(q), data<int32_t>(start), data<void>(pool),
+                                data<int32_t>(table), data<int32_t>(ctx), (float)PyFloat_AS_DOUBLE(a[6]), data<void>(&out),
+                                data<void>(ws), ws->nbytes(), data<uint32_t>(err), stream);
+        if (st != PA_OK) return refused(st, "pa_decode_multi_bs8");
+        return given ? Py_NewRef(a[9]) : THPVariable_Wrap(out);
+    });
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(keep_kv), METHOD(tree_verify), METHOD(decode_tree), METHOD(rope_append_kv),
+                         METHOD(append_kv_bs8), METHOD(decode_bs8), METHOD(decode_multi_bs8),
                          METHOD(on_failure), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

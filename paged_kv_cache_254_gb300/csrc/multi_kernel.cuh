@@ -263,8 +263,8 @@ __device__ __forceinline__ Sched tree_sched(long long W, int ctas, int min_block
 // whose run the chunk begins in walks it.  (A pre-pass kernel that writes prefix
 // sums for all, and a search in them, cost three dependent loads more and 3 us.)
 // wsum: THREADS / 32 words, box: one TreeStart, both in shared memory.
-template <int THREADS>
-__device__ __forceinline__ void tree_start(const TreeTab& tab, int Hkv, int min_blocks, long long* wsum,
+template <int THREADS, class Tab>
+__device__ __forceinline__ void tree_start(const Tab& tab, int Hkv, int min_blocks, long long* wsum,
                                            TreeStart* box) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = tab.N * tab.groups, per = (n + THREADS - 1) / THREADS;

@@ -10,6 +10,9 @@
 #include <cstring>
 
 #include "../../include/pa.h"
+#include "bs8.cuh"
+#include "bs8_ops.cuh"
+#include "chunk_bs8_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "kv_ops.cuh"
 #include "launch.cuh"
@@ -351,6 +354,51 @@ pa_status check_fp8(const pa_shape* s, int kv_format, float k_scale, float v_sca
     return PA_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit cache with scales per block and head
+// Shapes of every call on it: 16-bit values of head_dim 64 or 128 in blocks of 16 or 32.
+pa_status check_bs8(const pa_shape* s, int kv_format) {
+    const pa_status st = check_common(s);
+    if (st != PA_OK) return st;
+    if (s->dtype != PA_FP16 && s->dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+    if (kv_format != PA_FP8_E4M3 && kv_format != PA_FP8_E5M2) return PA_ERR_INVALID_ARG;
+    if (s->head_dim != 64 && s->head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (s->block_size != 16 && s->block_size != 32) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+Bs8Kind bs8_kind(const pa_shape* s, int kv_format) {
+    return Bs8Kind{s->dtype == PA_BF16, kv_format == PA_FP8_E5M2, s->block_size == 32, s->head_dim == 128};
+}
+
+// The decode's rules on top: groups of 1, 2, 4, 8 or 16 query heads.
+pa_status pick_decode_bs8(const pa_shape* s, int kv_format, const DecodeKernelInfo** out) {
+    const DecodeKernelInfo* k16 = nullptr;
+    pa_status st = pick_decode(s, &k16);
+    if (st == PA_OK) st = check_bs8(s, kv_format);
+    if (st != PA_OK) return st;
+    static const auto tab = [] {
+        struct T { DecodeKernelInfo t[2][2][2][2][2]; } x;      // [bf16][d == 128][e5m2][bs == 32][g > 8]
+        decode_bs8_table_fp16_d64(x.t[0][0]);
+        decode_bs8_table_fp16_d128(x.t[0][1]);
+        decode_bs8_table_bf16_d64(x.t[1][0]);
+        decode_bs8_table_bf16_d128(x.t[1][1]);
+        return x;
+    }();
+    const Bs8Kind k = bs8_kind(s, kv_format);
+    *out = &tab.t[k.bf16][k.d128][k.e5m2][k.bs32][s->num_q_heads / s->num_kv_heads > 8];
+    return PA_OK;
+}
+
+uint64_t bs8_pool_bytes(const pa_shape* s) {
+    return (uint64_t)s->num_blocks * s->num_kv_heads * bs8_piece_bytes(s->block_size, s->head_dim);
+}
+
+// Warps of a launch over (pair or block, KV head, keys or values): a grid of eight-warp
+// blocks has to hold them.
+bool bs8_grid_fits(const pa_shape* s, long long units) {
+    return units <= ((1ll << 31) - 1) * 8 / (2ll * s->num_kv_heads);
+}
+
 const PrefixKernelInfo& pick_prefix(const pa_shape* s) {
     static const auto tab = [] {
         struct T { PrefixKernelInfo t[2][2][2]; } x;
@@ -465,6 +513,61 @@ size_t tree_starts_bytes(int ctas) { return align256((size_t)ctas * sizeof(TreeS
 // per tile row per CTA.
 size_t tree_region_bytes(const pa_shape* s, const TreePlan& plan, int ctas) {
     return tree_starts_bytes(ctas) + (size_t)ctas * 2 * plan.k->rows * (s->head_dim + 4) * sizeof(float);
+}
+
+// The post-pass of a tree or chunk launch L: one CTA per chunk boundary, for the pairs cut there.
+bool merge_trees(const pa_shape* shape, const TreePlan& plan, const MultiLaunch& L, int max_nodes, int ctas) {
+    if (ctas <= 1) return true;
+    const int g = shape->num_q_heads / shape->num_kv_heads;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(1, TREE_MERGE_THREADS, 0, L.stream, attr);
+    // A pair is cut into at most about this many pieces.  Many of them are worth a
+    // search for the few pairs and several groups of lanes a row (one sequence of
+    // 4000 tokens, 62 pieces: 27 -> 19 us for the call), up to 16 are not (8
+    // sequences, 16 pieces: 29 against 31 us).
+    const long long pairs = (long long)shape->num_seqs * shape->num_kv_heads * plan.groups;
+    const long long pieces = std::min(ctas / pairs, (long long)shape->max_blocks_per_seq / plan.min_blocks + 1);
+    const bool few = pieces > 16 && ctas <= 32 * TREE_MERGE_THREADS;
+    int splits = 1;
+    while (few && splits < TREE_MERGE_SPLITS && 4 * splits <= pieces) splits *= 2;
+    cfg.gridDim.x = (unsigned)(few ? pairs : ctas - 1);
+    const int rows = std::min(plan.k->rows, max_nodes * g);
+    const int per = TREE_MERGE_THREADS / (shape->head_dim / 4) / splits;   // rows of a block
+    cfg.gridDim.y = (rows + per - 1) / per;
+    const DecodeParams& d = L.p.d;
+    const float* parts = d.partials;
+    const TreeStart* starts = L.p.starts;
+    const auto merge = shape->head_dim == 128 ? (few ? pa_tree_merge<128, true> : pa_tree_merge<128, false>)
+                                              : (few ? pa_tree_merge<64, true> : pa_tree_merge<64, false>);
+    return cudaLaunchKernelEx(&cfg, merge, L.p.q_start, starts, parts, d.out, d.N, d.Hkv, g, plan.k->rows, ctas,
+                              plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes, splits) == cudaSuccess;
+}
+
+// Chunks over the block-scaled 8-bit cache, as a tree launch: up to 128 query rows per
+// (sequence, KV head) pair in the arrangement that splits a pair's stages over both
+// tiles, more in groups of 256 rows.
+pa_status plan_chunk(const pa_shape* s, int kv_format, int max_q, TreePlan* out) {
+    const DecodeKernelInfo* k8 = nullptr;
+    const pa_status st = pick_decode_bs8(s, kv_format, &k8);
+    if (st != PA_OK) return st;
+    if (max_q < 1) return PA_ERR_INVALID_ARG;
+    static const auto tab = [] {
+        struct T { MultiKernelInfo t[2][2][2][2][2]; } x;       // [bf16][d == 128][e5m2][bs == 32][rows > 128]
+        chunk_bs8_table_fp16_d64(x.t[0][0]);
+        chunk_bs8_table_fp16_d128(x.t[0][1]);
+        chunk_bs8_table_bf16_d64(x.t[1][0]);
+        chunk_bs8_table_bf16_d128(x.t[1][1]);
+        return x;
+    }();
+    const int g = s->num_q_heads / s->num_kv_heads;
+    const Bs8Kind k = bs8_kind(s, kv_format);
+    out->tc = true;
+    out->k = &tab.t[k.bf16][k.d128][k.e5m2][k.bs32][max_q > 128 / g];
+    out->group_nodes = out->k->rows / g;
+    out->groups = (max_q - 1) / out->group_nodes + 1;
+    out->tile_nodes = 128 / g;
+    out->min_blocks = 128 / s->block_size;
+    return (long long)s->num_seqs * out->groups < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 // Workspace of prefix-aware decode (offsets in off[]): [0] prefix counters,
@@ -1021,32 +1124,7 @@ pa_status pa_decode_tree(const pa_shape* shape, int32_t max_nodes, int32_t total
     L.stream = static_cast<cudaStream_t>(stream);
     L.grid = ctas;
     if (plan.k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
-    if (ctas > 1) {   // one CTA per chunk boundary: the pairs cut there
-        const int g = shape->num_q_heads / shape->num_kv_heads;
-        cudaLaunchAttribute attr[1];
-        cudaLaunchConfig_t cfg = pdl_config(1, TREE_MERGE_THREADS, 0, L.stream, attr);
-        // A pair is cut into at most about this many pieces.  Many of them are worth a
-        // search for the few pairs and several groups of lanes a row (one sequence of
-        // 4000 tokens, 62 pieces: 27 -> 19 us for the call), up to 16 are not (8
-        // sequences, 16 pieces: 29 against 31 us).
-        const long long pairs = (long long)shape->num_seqs * shape->num_kv_heads * plan.groups;
-        const long long pieces = std::min(ctas / pairs, (long long)shape->max_blocks_per_seq / plan.min_blocks + 1);
-        const bool few = pieces > 16 && ctas <= 32 * TREE_MERGE_THREADS;
-        int splits = 1;
-        while (few && splits < TREE_MERGE_SPLITS && 4 * splits <= pieces) splits *= 2;
-        cfg.gridDim.x = (unsigned)(few ? pairs : ctas - 1);
-        const int rows = std::min(plan.k->rows, max_nodes * g);
-        const int per = TREE_MERGE_THREADS / (shape->head_dim / 4) / splits;   // rows of a block
-        cfg.gridDim.y = (rows + per - 1) / per;
-        const float* parts = d.partials;
-        const TreeStart* starts = L.p.starts;
-        const auto merge = shape->head_dim == 128 ? (few ? pa_tree_merge<128, true> : pa_tree_merge<128, false>)
-                                                  : (few ? pa_tree_merge<64, true> : pa_tree_merge<64, false>);
-        if (cudaLaunchKernelEx(&cfg, merge, q_start, starts, parts, d.out, d.N, d.Hkv, g, plan.k->rows, ctas,
-                               plan.min_blocks, (int)(shape->dtype == PA_BF16), plan.group_nodes, splits) != cudaSuccess)
-            return PA_ERR_CUDA;
-    }
-    return PA_OK;
+    return merge_trees(shape, plan, L, max_nodes, ctas) ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_tree_verify(int32_t num_seqs, int32_t max_nodes, int32_t total_q, const int32_t* q_start,
@@ -1179,6 +1257,231 @@ pa_status pa_rope_append_kv(const pa_shape* shape, const pa_rope* rope, int32_t 
     return rope_append_launch(a, shape->dtype == PA_BF16, static_cast<cudaStream_t>(stream), sms) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+pa_status pa_append_kv_bs8(const pa_shape* shape, int32_t kv_format, int32_t max_new, int32_t total_new,
+                           const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                           const int32_t* q_start, const int32_t* block_tables, const int32_t* context_lens,
+                           void* kv_pool, uint32_t* err_word, void* stream) {
+    const pa_status st = check_bs8(shape, kv_format);
+    if (st != PA_OK) return st;
+    if (shape->num_seqs < 0 || shape->max_blocks_per_seq <= 0 || max_new < 1 || total_new < 0) return PA_ERR_INVALID_ARG;
+    if ((long long)shape->max_blocks_per_seq * shape->block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if (shape->num_seqs == 0) return PA_OK;
+    if (!q_start || !block_tables || !context_lens || !kv_pool) return PA_ERR_INVALID_ARG;
+    if (total_new > 0 && (!k_new || !v_new)) return PA_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(kv_pool, 32) || !aligned(q_start, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)shape->num_kv_heads * shape->head_dim;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return PA_ERR_INVALID_ARG;
+    if (total_new > 0 && (overlap(k_new, 2 * ((total_new - 1) * k_stride + row), kv_pool, bs8_pool_bytes(shape)) ||
+                          overlap(v_new, 2 * ((total_new - 1) * v_stride + row), kv_pool, bs8_pool_bytes(shape))))
+        return PA_ERR_INVALID_ARG;
+    AppendBs8Args a{};
+    a.k = static_cast<const uint16_t*>(k_new);
+    a.v = static_cast<const uint16_t*>(v_new);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_start = q_start;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.pool = static_cast<uint8_t*>(kv_pool);
+    a.err = err_word;
+    a.N = shape->num_seqs;
+    a.T = total_new;
+    a.max_new = max_new;
+    // a sequence has no more new tokens than the call has, nor than its table holds
+    const long long most = std::min({(long long)max_new, std::max(1ll, (long long)total_new),
+                                     (long long)shape->max_blocks_per_seq * shape->block_size});
+    a.span = (int32_t)std::min((most + shape->block_size - 2) / shape->block_size + 1, (long long)shape->max_blocks_per_seq);
+    a.Hkv = shape->num_kv_heads;
+    a.NB = shape->num_blocks;
+    a.MB = shape->max_blocks_per_seq;
+    if (!bs8_grid_fits(shape, (long long)a.N * a.span)) return PA_ERR_UNSUPPORTED;
+    return append_bs8_launch(a, bs8_kind(shape, kv_format), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                              : PA_ERR_CUDA;
+}
+
+size_t pa_decode_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format) {
+    const DecodeKernelInfo* k = nullptr;
+    if (pick_decode_bs8(shape, kv_format, &k) != PA_OK) return 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int ctas = k->max_ctas(dev);
+    if (ctas <= 0) return 0;
+    const long long workers = (long long)ctas * k->workers;
+    return decode_region_bytes(shape, workers, kDynPerWorker * workers);
+}
+
+pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q, const void* kv_pool,
+                        const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                        void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream) {
+    const DecodeKernelInfo* k = nullptr;
+    const pa_status st = pick_decode_bs8(shape, kv_format, &k);
+    if (st != PA_OK) return st;
+    if (!q || !kv_pool || !block_tables || !context_lens || !out) return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv_pool, 32) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;
+    const uint64_t out_bytes = (uint64_t)shape->num_seqs * shape->num_q_heads * shape->head_dim * 2;
+    if (overlap(q, out_bytes, out, out_bytes)) return PA_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    const int ctas = k->max_ctas(dev);
+    if (ctas <= 0) return PA_ERR_CUDA;
+    if (!workspace || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+    CUtensorMap unused{};   // every (block, head) piece is bulk-copied from p.kv8
+    DecodeLaunch L{};
+    L.tmap_k = &unused;
+    L.tmap_v = &unused;
+    L.p.q = static_cast<const uint16_t*>(q);
+    L.p.block_tables = block_tables;
+    L.p.context_lens = context_lens;
+    L.p.out = static_cast<uint16_t*>(out);
+    L.p.err = err_word;
+    L.p.kv8 = static_cast<const uint8_t*>(kv_pool);
+    L.p.v_scale = 1.0f;                              // the pieces' scales are applied inside
+    L.p.N = shape->num_seqs;
+    L.p.Hq = shape->num_q_heads;
+    L.p.Hkv = shape->num_kv_heads;
+    L.p.NB = shape->num_blocks;
+    L.p.MB = shape->max_blocks_per_seq;
+    L.p.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
+    L.p.timeout_ns = kTimeoutNs;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return run_decode(k, ctas, L, shape, workspace, workspace_bytes, nullptr);
+}
+
+size_t pa_decode_multi_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format, int32_t max_q_len) {
+    TreePlan plan;
+    if (plan_chunk(shape, kv_format, max_q_len, &plan) != PA_OK) return 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int ctas = plan.k->max_ctas(dev);
+    return ctas > 0 ? tree_region_bytes(shape, plan, ctas) : 0;
+}
+
+pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t max_q_len, int32_t total_q,
+                              const void* q, const int32_t* q_start, const void* kv_pool,
+                              const int32_t* block_tables, const int32_t* context_lens, float scale, void* out,
+                              void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream) {
+    TreePlan plan;
+    const pa_status st = plan_chunk(shape, kv_format, max_q_len, &plan);
+    if (st != PA_OK) return st;
+    if (total_q < 0) return PA_ERR_INVALID_ARG;
+    if (!q_start || !kv_pool || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    if (total_q > 0 && (!q || !out)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv_pool, 32) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4) || !aligned(q_start, 4))
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    const uint64_t bytes = (uint64_t)total_q * shape->num_q_heads * shape->head_dim * 2;
+    if (total_q > 0 && overlap(q, bytes, out, bytes)) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;
+    // no chunk is longer than the call's rows, or than a table holds
+    const int most = (int)std::min({(long long)max_q_len, std::max(1ll, (long long)total_q),
+                                    (long long)shape->max_blocks_per_seq * shape->block_size});
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    const int ctas = plan.k->max_ctas(dev);
+    if (ctas <= 0) return PA_ERR_CUDA;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < tree_region_bytes(shape, plan, ctas))
+        return PA_ERR_WORKSPACE;
+    if (plan_chunk(shape, kv_format, most, &plan) != PA_OK) return PA_ERR_UNSUPPORTED;
+
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    MultiLaunch L{};
+    DecodeParams& d = L.p.d;
+    d.q = static_cast<const uint16_t*>(q);
+    d.block_tables = block_tables;
+    d.context_lens = context_lens;
+    d.out = static_cast<uint16_t*>(out);
+    d.err = err_word;
+    d.kv8 = static_cast<const uint8_t*>(kv_pool);
+    L.p.starts = reinterpret_cast<TreeStart*>(base);
+    d.partials = reinterpret_cast<float*>(base + tree_starts_bytes(ctas));
+    d.N = shape->num_seqs;
+    d.Hq = shape->num_q_heads;
+    d.Hkv = shape->num_kv_heads;
+    d.NB = shape->num_blocks;
+    d.MB = shape->max_blocks_per_seq;
+    d.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
+    d.timeout_ns = kTimeoutNs;
+    d.v_scale = 1.0f;
+    L.p.q_start = q_start;
+    L.p.max_q = max_q_len;
+    L.p.total_q = total_q;
+    L.p.groups = plan.groups;
+    L.p.group_nodes = plan.group_nodes;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.grid = ctas;
+    if (plan.k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
+    return merge_trees(shape, plan, L, most, ctas) ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_copy_blocks_bs8(const pa_shape* shape, const int32_t* src_dst_pairs, int32_t num_pairs, void* kv_pool,
+                             uint32_t* err_word, void* stream) {
+    const pa_status st = check_bs8(shape, PA_FP8_E4M3);   // either format: bytes are moved
+    if (st != PA_OK) return st;
+    if (num_pairs < 0) return PA_ERR_INVALID_ARG;
+    if (num_pairs == 0) return PA_OK;
+    if (!src_dst_pairs || !kv_pool || !aligned(kv_pool, 32) || !aligned(src_dst_pairs, 4)) return PA_ERR_INVALID_ARG;
+    const int sms = current_sms();
+    if (sms <= 0) return PA_ERR_CUDA;
+    CopyArgs a;
+    a.n = num_pairs;
+    a.vec_per_block = (long long)shape->num_kv_heads * bs8_piece_bytes(shape->block_size, shape->head_dim) / 16;
+    a.NB = shape->num_blocks;
+    a.err = err_word;
+    return copy_launch(src_dst_pairs, kv_pool, nullptr, a, static_cast<cudaStream_t>(stream), sms) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+// pa_pack_blocks_bs8 and pa_unpack_blocks_bs8.
+static pa_status convert_bs8(bool pack, const pa_shape* shape, int32_t kv_format, int32_t num_blocks16,
+                             const int32_t* pairs, int32_t num_pairs, void* k_pool, void* v_pool, void* kv_pool,
+                             uint32_t* err_word, void* stream) {
+    pa_status st = check_bs8(shape, kv_format);
+    if (st != PA_OK) return st;
+    if (num_pairs < 0 || num_blocks16 <= 0) return PA_ERR_INVALID_ARG;
+    if (num_pairs == 0) return PA_OK;
+    if (!pairs || !k_pool || !v_pool || !kv_pool || k_pool == v_pool) return PA_ERR_INVALID_ARG;
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(kv_pool, 32) || !aligned(pairs, 4))
+        return PA_ERR_INVALID_ARG;
+    const uint64_t bytes16 = (uint64_t)num_blocks16 * shape->num_kv_heads * shape->block_size * shape->head_dim * 2;
+    if (overlap(k_pool, bytes16, kv_pool, bs8_pool_bytes(shape)) || overlap(v_pool, bytes16, kv_pool, bs8_pool_bytes(shape)))
+        return PA_ERR_INVALID_ARG;
+    if (!bs8_grid_fits(shape, num_pairs)) return PA_ERR_UNSUPPORTED;
+    ConvertBs8Args a{};
+    a.pairs = pairs;
+    a.k = static_cast<uint16_t*>(k_pool);
+    a.v = static_cast<uint16_t*>(v_pool);
+    a.pool = static_cast<uint8_t*>(kv_pool);
+    a.err = err_word;
+    a.n = num_pairs;
+    a.Hkv = shape->num_kv_heads;
+    a.NB8 = shape->num_blocks;
+    a.NB16 = num_blocks16;
+    const auto launch_it = pack ? pack_bs8_launch : unpack_bs8_launch;
+    return launch_it(a, bs8_kind(shape, kv_format), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_pack_blocks_bs8(const pa_shape* shape, int32_t kv_format, int32_t num_blocks16,
+                             const int32_t* src_dst_pairs, int32_t num_pairs, const void* k_pool, const void* v_pool,
+                             void* kv_pool, uint32_t* err_word, void* stream) {
+    return convert_bs8(true, shape, kv_format, num_blocks16, src_dst_pairs, num_pairs, const_cast<void*>(k_pool),
+                       const_cast<void*>(v_pool), kv_pool, err_word, stream);
+}
+
+pa_status pa_unpack_blocks_bs8(const pa_shape* shape, int32_t kv_format, int32_t num_blocks16,
+                               const int32_t* src_dst_pairs, int32_t num_pairs, const void* kv_pool, void* k_pool,
+                               void* v_pool, uint32_t* err_word, void* stream) {
+    return convert_bs8(false, shape, kv_format, num_blocks16, src_dst_pairs, num_pairs, k_pool, v_pool,
+                       const_cast<void*>(kv_pool), err_word, stream);
 }
 
 size_t pa_decode_int4_workspace_bytes(const pa_shape* shape) {

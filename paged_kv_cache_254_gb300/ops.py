@@ -759,3 +759,253 @@ def pa_copy_blocks_int4(src_dst_pairs, kv_pool, dtype=torch.bfloat16, err=None, 
                                              ctypes.c_int32(src_dst_pairs.shape[0]), _ptr(kv_pool), _ptr(err),
                                              _stream(kv_pool.device, stream))
     _lib.check(st, "pa_copy_blocks_int4")
+
+
+# --------------------------------------------------------------------------- 8-bit cache, a scale per block and head
+BS8_HEAD = 32
+
+
+def bs8_pool(num_blocks, num_kv_heads, block_size, head_dim=128, device="cuda"):
+    """An empty block-scaled 8-bit pool: zeros, uint8 [NB, Hkv, 32 + 2 * B * d]
+    (two scales, then the codes of B keys and B values; see include/pa.h)."""
+    return torch.zeros((num_blocks, num_kv_heads, BS8_HEAD + 2 * block_size * head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def bs8_scales(kv_pool):
+    """The pool's scales as a view, fp32 [NB, Hkv, 2]: keys', values'."""
+    return kv_pool[..., :8].view(torch.float32)
+
+
+def _bs8_format(kv_format) -> int:
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}, got {kv_format!r}")
+    return KV_FORMATS[kv_format]
+
+
+def _bs8_shape(kv_pool, head_dim, dtype, dev) -> _lib.PaShape:
+    """Shape of a pool of pieces for head_dim; the block size follows from their bytes."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"queries and values must be float16 or bfloat16, got {dtype}")
+    _arg("kv_pool", kv_pool, torch.uint8, dev)
+    if kv_pool.dim() != 3 or head_dim < 1 or (kv_pool.shape[2] - BS8_HEAD) % (2 * head_dim):
+        raise ValueError("kv_pool must be uint8 [NB, Hkv, 32 + 2 * B * d] (see bs8_pool)")
+    NB, Hkv, P = kv_pool.shape
+    return _lib.PaShape(0, Hkv, Hkv, head_dim, (P - BS8_HEAD) // (2 * head_dim), NB, 1, _DTYPES[dtype])
+
+
+def pa_append_kv_bs8(k_new, v_new, block_tables, context_lens, q_start, kv_pool, kv_format="e4m3", max_new=None,
+                     err=None, stream=None):
+    """Quantise new tokens into the block-scaled pool (see include/pa.h): rows
+    q_start[b] .. q_start[b + 1] - 1 of k_new and v_new [T, Hkv, d] are sequence
+    b's last cached tokens, counted in context_lens.  k_new, v_new may be views
+    of one projection's output.  max_new defaults to the largest number of new
+    tokens (read from q_start on the host)."""
+    if stream is not None:
+        return _on_stream(stream, pa_append_kv_bs8, k_new, v_new, block_tables, context_lens, q_start, kv_pool,
+                          kv_format, max_new, err)
+    if max_new is None and isinstance(q_start, torch.Tensor):
+        max_new = _largest_chunk(q_start)
+    args = (k_new, v_new, block_tables, context_lens, q_start, kv_pool, _bs8_format(kv_format), max_new, err)
+    if (_fast or _load_fast()).append_kv_bs8(*args) is NotImplemented:
+        _append_kv_bs8(*args)
+
+
+def _append_kv_bs8(k_new, v_new, block_tables, context_lens, q_start, kv_pool, fmt, max_new, err):
+    """pa_append_kv_bs8 by way of every check."""
+    dev = _index("kv_pool", kv_pool)
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+        raise ValueError("k_new must be a tensor [T, Hkv, d]")
+    T, Hkv, d = k_new.shape
+    shape = _bs8_shape(kv_pool, d, k_new.dtype, dev)
+    if shape.num_kv_heads != Hkv:
+        raise ValueError(f"k_new has {Hkv} heads, kv_pool {shape.num_kv_heads}")
+    ks = _token_rows("k_new", k_new, k_new.dtype, (T, Hkv, d), dev)
+    vs = _token_rows("v_new", v_new, k_new.dtype, (T, Hkv, d), dev)
+    _arg("block_tables", block_tables, torch.int32, dev)
+    _arg("context_lens", context_lens, torch.int32, dev)
+    _arg("q_start", q_start, torch.int32, dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [N, MB]")
+    N, MB = block_tables.shape
+    if q_start.shape != (N + 1,) or context_lens.shape != (N,):
+        raise ValueError("q_start must have N + 1 entries, context_lens N")
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    shape.num_seqs, shape.max_blocks_per_seq = N, MB
+    st = _call(_lib.load().pa_append_kv_bs8, dev, shape, fmt, max_new, T, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+               q_start.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), kv_pool.data_ptr(), _addr(err),
+               _raw_stream(dev))
+    if st:
+        _lib.check(st, "pa_append_kv_bs8")
+
+
+_bs8_bytes = {}
+
+
+def _bs8_workspace_bytes(dev, shape, fmt, max_q):
+    # (max_q 0: pa_decode_bs8) the size of a valid shape's workspace depends on these and the device's SM count alone
+    key = (dev, fmt, max_q, shape.num_seqs, shape.num_q_heads, shape.num_kv_heads, shape.head_dim, shape.block_size,
+           shape.dtype)
+    need = _bs8_bytes.get(key)
+    if need is None:
+        lib = _lib.load()
+        need = int(_call(lib.pa_decode_multi_bs8_workspace_bytes, dev, shape, fmt, max_q) if max_q else
+                   _call(lib.pa_decode_bs8_workspace_bytes, dev, shape, fmt))
+        if need:                         # 0: something about the shape is invalid, which the call reports
+            _bs8_bytes[key] = need
+    return need
+
+
+def _bs8_attention(call, q, kv_pool, block_tables, context_lens, fmt, out, workspace, err, max_q, run):
+    """The checks and the workspace that both attention calls share;
+    run(lib, shape, out, ws, err, handle) makes the call."""
+    dev = _index("q", q)
+    dt = q.dtype
+    _arg("q", q, dt, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, d]")
+    shape = _bs8_shape(kv_pool, q.shape[2], dt, dev)
+    _arg("block_tables", block_tables, torch.int32, dev)
+    _arg("context_lens", context_lens, torch.int32, dev)
+    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],):
+        raise ValueError("block_tables must be [N, MB], context_lens [N]")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _arg("out", out, dt, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    shape.num_q_heads = q.shape[1]
+    shape.num_seqs, shape.max_blocks_per_seq = block_tables.shape
+    need = 0
+    if workspace is not None:
+        _arg("workspace", workspace, workspace.dtype, dev)
+    else:
+        need = _bs8_workspace_bytes(dev, shape, fmt, max_q)
+        if need == 0:
+            workspace = torch.empty(0, dtype=torch.uint8, device=q.device)
+    handle = _raw_stream(dev)
+    st = _lend(workspace, dev, handle, need, lambda ws: run(_lib.load(), dev, shape, out, ws, handle))
+    if st:
+        _lib.check(st, call)
+    return out
+
+
+def pa_decode_bs8(q, kv_pool, block_tables, context_lens, scale, kv_format="e4m3", out=None, workspace=None, err=None,
+                  stream=None):
+    """Decode over the block-scaled 8-bit cache (see include/pa.h): out [N, Hq, d]
+    in q's type, for q [N, Hq, d]."""
+    if stream is not None:
+        return _on_stream(stream, pa_decode_bs8, q, kv_pool, block_tables, context_lens, scale, kv_format, out,
+                          workspace, err)
+    args = (q, kv_pool, block_tables, context_lens, scale, _bs8_format(kv_format), out, workspace, err)
+    done = (_fast or _load_fast()).decode_bs8(_sp_cache, *args)
+    return _decode_bs8(*args) if done is NotImplemented else done
+
+
+def _decode_bs8(q, kv_pool, block_tables, context_lens, scale, fmt, out, workspace, err):
+    """pa_decode_bs8 by way of every check."""
+    def run(lib, dev, shape, out, ws, handle):
+        if q.shape[0] != shape.num_seqs:
+            raise ValueError("q and block_tables must have N rows")
+        return _call(lib.pa_decode_bs8, dev, shape, fmt, q.data_ptr(), kv_pool.data_ptr(), block_tables.data_ptr(),
+                     context_lens.data_ptr(), scale, out.data_ptr(), ws.data_ptr(), ws.nbytes, _addr(err), handle)
+    return _bs8_attention("pa_decode_bs8", q, kv_pool, block_tables, context_lens, fmt, out, workspace, err, 0, run)
+
+
+def pa_decode_multi_bs8(q, kv_pool, block_tables, context_lens, q_start, scale, kv_format="e4m3", max_q_len=None,
+                        out=None, workspace=None, err=None, stream=None):
+    """Causal attention of a chunk of new tokens per sequence over the
+    block-scaled 8-bit cache (see include/pa.h): q [T, Hq, d] holds each
+    sequence's last cached tokens at rows q_start[b] .. q_start[b + 1] - 1
+    (q_start: int32 [N + 1]), few or thousands.  max_q_len defaults to the
+    largest chunk (read from q_start on the host)."""
+    if stream is not None:
+        return _on_stream(stream, pa_decode_multi_bs8, q, kv_pool, block_tables, context_lens, q_start, scale,
+                          kv_format, max_q_len, out, workspace, err)
+    if max_q_len is None and isinstance(q_start, torch.Tensor):
+        max_q_len = _largest_chunk(q_start)
+    args = (q, kv_pool, block_tables, context_lens, q_start, scale, _bs8_format(kv_format), max_q_len, out, workspace,
+            err)
+    done = (_fast or _load_fast()).decode_multi_bs8(_sp_cache, *args)
+    return _decode_multi_bs8(*args) if done is NotImplemented else done
+
+
+def _decode_multi_bs8(q, kv_pool, block_tables, context_lens, q_start, scale, fmt, max_q_len, out, workspace, err):
+    """pa_decode_multi_bs8 by way of every check."""
+    if max_q_len < 1:
+        raise ValueError("max_q_len must be at least 1")
+    _arg("q_start", q_start, torch.int32, _index("q", q))
+
+    def run(lib, dev, shape, out, ws, handle):
+        if q_start.shape != (shape.num_seqs + 1,):
+            raise ValueError("q_start must have N + 1 entries")
+        return _call(lib.pa_decode_multi_bs8, dev, shape, fmt, max_q_len, q.shape[0], q.data_ptr(), q_start.data_ptr(),
+                     kv_pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale, out.data_ptr(),
+                     ws.data_ptr(), ws.nbytes, _addr(err), handle)
+    return _bs8_attention("pa_decode_multi_bs8", q, kv_pool, block_tables, context_lens, fmt, out, workspace, err,
+                          max_q_len, run)
+
+
+def pa_copy_blocks_bs8(src_dst_pairs, kv_pool, err=None, stream=None):
+    """Copy-on-write copies of whole blocks, scales included, of the
+    block-scaled pool."""
+    if stream is not None:
+        return _on_stream(stream, pa_copy_blocks_bs8, src_dst_pairs, kv_pool, err)
+    dev = _index("kv_pool", kv_pool)
+    n = kv_pool.shape[-1] - BS8_HEAD
+    # blocks of 16 or 32 tokens: the bytes are the same for either, and for either head_dim
+    d = n // 32 if n // 32 in (64, 128) else n // 64
+    shape = _bs8_shape(kv_pool, max(d, 1), torch.bfloat16, dev)
+    _arg("src_dst_pairs", src_dst_pairs, torch.int32, dev)
+    if src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be [n, 2]")
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    st = _call(_lib.load().pa_copy_blocks_bs8, dev, shape, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0],
+               kv_pool.data_ptr(), _addr(err), _raw_stream(dev))
+    if st:
+        _lib.check(st, "pa_copy_blocks_bs8")
+
+
+def _convert_bs8(call, src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err):
+    dev = _index("kv_pool", kv_pool)
+    fmt = _bs8_format(kv_format)
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("k_pool must be a tensor [NB, Hkv, B, d]")
+    _arg("k_pool", k_pool, k_pool.dtype, dev)
+    _arg("v_pool", v_pool, k_pool.dtype, dev)
+    NB, Hkv, B, d = k_pool.shape
+    shape = _bs8_shape(kv_pool, d, k_pool.dtype, dev)
+    if v_pool.shape != k_pool.shape or (shape.num_kv_heads, shape.block_size) != (Hkv, B):
+        raise ValueError("k_pool, v_pool [NB, Hkv, B, d] and kv_pool [NB, Hkv, 32 + 2 * B * d] disagree")
+    _arg("src_dst_pairs", src_dst_pairs, torch.int32, dev)
+    if src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be [n, 2]")
+    if err is not None:
+        _arg("err", err, torch.int32, dev)
+    pools = (k_pool, v_pool, kv_pool) if call == "pa_pack_blocks_bs8" else (kv_pool, k_pool, v_pool)
+    st = _call(getattr(_lib.load(), call), dev, shape, fmt, NB, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0],
+               *(p.data_ptr() for p in pools), _addr(err), _raw_stream(dev))
+    if st:
+        _lib.check(st, call)
+
+
+def pa_pack_blocks_bs8(src_dst_pairs, k_pool, v_pool, kv_pool, kv_format="e4m3", err=None, stream=None):
+    """Quantise whole blocks src of a 16-bit cache (k_pool, v_pool [NB, Hkv, B, d])
+    into blocks dst of the block-scaled pool, for each row of src_dst_pairs [n, 2]
+    (int32)."""
+    if stream is not None:
+        return _on_stream(stream, pa_pack_blocks_bs8, src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
+    _convert_bs8("pa_pack_blocks_bs8", src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
+
+
+def pa_unpack_blocks_bs8(src_dst_pairs, kv_pool, k_pool, v_pool, kv_format="e4m3", err=None, stream=None):
+    """Blocks src of the block-scaled pool back into blocks dst of a 16-bit cache,
+    for each row of src_dst_pairs [n, 2] (int32)."""
+    if stream is not None:
+        return _on_stream(stream, pa_unpack_blocks_bs8, src_dst_pairs, kv_pool, k_pool, v_pool, kv_format, err)
+    _convert_bs8("pa_unpack_blocks_bs8", src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
