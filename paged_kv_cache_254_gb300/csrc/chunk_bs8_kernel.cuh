@@ -20,19 +20,33 @@
 //    segment's end, where the threads of tile 0 read both outputs from tensor memory.
 //
 // Tensor memory (512 columns): S_0, S_1 at 0 and 128, O_0, O_1 at 256 and 384; P_t overwrites
-// S_t, 16 columns at the start of each 32 that held its scores.  A row's reference moves
+// S_t, 32 columns at the start of each 64 that held its scores.  A row's reference moves
 // only when its maximum rises by more than 8 (O is rescaled then), so weights are at most
 // 2^8.
 //
-// Roles (512 threads, one CTA per SM):
-//   warps 0-3, 4-7   softmax of tile 0, 1: thread = row = TMEM lane
-//   warps 8-11       per segment the queries, as fp16 under the swizzle that the products
-//                    read; per stage the block scales, the keys, then the values: codes
-//                    from shared memory, fp16 back.  Value rows past the context become
-//                    zeros, and so do rows of the chunk that hold NaN or infinities
-//                    (rows that see them become NaN at the softmax)
-//   warps 12, 13     products of tile 0, 1 (one thread each)
-//   warp 14          copies: a bulk copy per block for scales and keys, one for values
+// Roles (one CTA per SM; 640 threads for SPLIT, else 512):
+//   warps 0-3, 4-7   softmax of tile 0, 1: thread = row = TMEM lane, half of a stage at a time, so that the
+//                    products of the first half run beside the softmax of the second
+//   8 or 4 warps     per segment the queries, as fp16 under the swizzle that the products read; per
+//                    stage the keys, then the values: codes from shared memory, fp16 back.
+//                    Value rows past the context become zeros, and so do rows of the chunk that hold
+//                    NaN or infinities (rows that see them become NaN at the softmax)
+//   2 warps          products of tile 0, 1 (one thread each)
+//   1 warp           the plan: each stage's place, blocks and scales, as a record for the others
+//   1 warp           copies: a bulk copy per block for its keys, one for its values
+//
+// Bound by the chain of a stage within a tile, not by a unit: at 256 rows and head_dim 128 a stage
+// takes 6,000 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
+// scores (700), their way to the softmax (300), two halves (1,200 to 1,600 each, the loads
+// 300 of it), the last products and their way back (700) follow one another, and the tiles'
+// warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
+// Measured on GB300: 1,050 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (785 TFLOP/s of 1,905); 640 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// to 8192 (1.9 TB/s).  Also measured: 64-key products ahead of the softmax (1,470 us), scores of one
+// stage in one piece (1,175), two softmax warps to a row (1,250), codes loaded into
+// registers from L2 (1,160), the conversion unrolled over both kinds (1,190: the roles' loops then
+// fall out of the SM's instruction cache), polling loops in place of held waits (no
+// difference).
 //
 // The work list and the partial states of split rows are those of the tree kernels: each CTA
 // takes an equal run of (row group, KV head, block) units; a group's keys end at its
@@ -90,66 +104,98 @@ struct ChunkTraits {
     static constexpr int KEYS = 128;                         // keys per stage
     static constexpr int SB = KEYS / BS;                     // blocks per stage
     static constexpr int HALVES = D / 64;
+    // SPLIT is the arrangement that HBM feeds: twice the converting warps
+    static constexpr int CONVERT_WARPS = SPLIT ? 8 : 4;
+    static constexpr int THREADS = 32 * (8 + CONVERT_WARPS + 4);
+    // registers after the roles part, in all no more than the launch's: 640 x 96 or 512 x 128
+    static constexpr int SOFT_REGS = SPLIT ? 144 : 168, CONVERT_REGS = SPLIT ? 64 : 104, OTHER_REGS = 64;
+    static_assert(256 * SOFT_REGS + 32 * CONVERT_WARPS * CONVERT_REGS + 128 * OTHER_REGS <= THREADS * (SPLIT ? 96 : 128), "registers");
     static constexpr int SLOT_BYTES = KEYS * D * 2;          // a stage's keys, or its values, in fp16
     static constexpr int HALF_STRIDE = KEYS * 128;           // between the column halves of a slot
-    static constexpr int R = 3;                              // such slots; K and V alternate
-    static constexpr int K8_BYTES = BS8_HEAD + BS * D;       // a block's scales and key codes
-    static constexpr int V8_BYTES = BS * D;
-    static constexpr int SLOT8_BYTES = (SB * K8_BYTES + 127) / 128 * 128;
     static constexpr int SMEM_BYTES = 227 * 1024;
     static constexpr int Q_HALF = TILE * 128;
     static constexpr int Q_BYTES = (SPLIT ? 1 : 2) * HALVES * Q_HALF;
     static constexpr int NREC = 8;
+    static constexpr int R_CAP = 6;
     static constexpr int N8_CAP = 8;
-    // full8, empty8; empty, ready; s_full, p_part[4], pv_done per tile; q_full, q_empty; fin;
-    // described; lead, follow; joined, o1_free
-    static constexpr int NBAR = 2 * N8_CAP + 2 * R + 2 * 6 + 2 + 2 + NREC + 2 + 2;
+    // empty, ready; empty8, full8; s_full, p_half[2], pv_half[2] per tile; q_full, q_empty; fin; described, forgotten;
+    // listed; joined, o1_free
+    static constexpr int NBAR = 2 * R_CAP + 2 * N8_CAP + 2 * 6 + 2 + 2 + 3 * NREC + 2;
     static constexpr int REC_OFF = (8 * NBAR + 15) / 16 * 16;
-    static constexpr int REC_BYTES = 48 + 4 * SB * 4;
+    static constexpr int REC_BYTES = 48 + 5 * SB * 4;
+    static constexpr int SLOT8_BYTES = KEYS * D;             // a stage's key or value codes
     static constexpr int ROWF_OFF = REC_OFF + NREC * REC_BYTES;   // score factors of the rows, two segments
     static constexpr int XCH_OFF = ROWF_OFF + 2 * 2 * TILE * 4;   // SPLIT: tile 1's (m, l) of a row
     static constexpr int MISC_OFF = XCH_OFF + (SPLIT ? TILE * 8 : 0);   // TMEM base, abort flag
     static constexpr int SPOILT_OFF = MISC_OFF + 16;         // per segment: first position of a value that is not finite
-    static constexpr int START_OFF = SPOILT_OFF + NREC * 4;  // a TreeStart, a word per warp
-    static constexpr int THREADS = 512;
+    static constexpr int NSEG = 2 * NREC;
+    static constexpr int START_OFF = SPOILT_OFF + NSEG * 4;  // a TreeStart, a word per warp
     static constexpr int Q_OFF = (START_OFF + 32 + 8 * THREADS / 32 + 1023) / 1024 * 1024;
-    static constexpr int OUT_OFF = Q_OFF + Q_BYTES;          // per softmax warp: 32 rows of 64 bytes on their way out
-    static constexpr int OUT_BYTES = 32 * 64;
-    static constexpr int RING_OFF = OUT_OFF + 8 * OUT_BYTES;
+    static constexpr int RING_OFF = Q_OFF + Q_BYTES;
+    static constexpr int R = 3;                              // fp16 slots; K and V alternate
+    // slots of codes on their way, a ring for keys and one for values
     static constexpr int RING8_OFF = RING_OFF + R * SLOT_BYTES;
-    static constexpr int N8_FIT = (SMEM_BYTES - 1024 - RING8_OFF) / SLOT8_BYTES / 2 * 2;
-    static constexpr int N8 = N8_FIT > N8_CAP ? N8_CAP : N8_FIT;   // slots of codes; keys in the even ones
-    static constexpr int CONVERT_WARP = 8, MMA_WARP = 12, COPY_WARP = 14;
+    static constexpr int N8_FIT = (SMEM_BYTES - 1024 - RING8_OFF) / SLOT8_BYTES;
+    static constexpr int N8 = N8_FIT > N8_CAP ? N8_CAP : N8_FIT;
+    static constexpr int NK8 = (N8 + 1) / 2, NV8 = N8 / 2;
+    static constexpr int CONVERT_WARP = 8, MMA_WARP = CONVERT_WARP + CONVERT_WARPS, PLAN_WARP = MMA_WARP + 2, COPY_WARP = MMA_WARP + 3;
     static constexpr int TMEM_COLS = 512;
     static constexpr int O_COL = 256;
     static constexpr int PSTRIDE = D + 4;
     static constexpr float TAU = 8.f;                        // lazy-rescale threshold (log2 units)
-    static_assert(N8 >= 2, "shared memory");
+    static_assert(N8 >= 2 && RING_OFF % 1024 == 0, "shared memory");
 };
 
-// One stage: what the copy warp says of it (first the 48 bytes), and its blocks' scales.
+// One stage as the planning warp describes it, and its blocks.
 template <int SB>
 struct alignas(16) ChunkStage {
     int base, kvh, t0, nkeys;     // position of the group's first token, KV head, first key, keys copied
     int n, ctx, q0, flags;        // tokens of the group, context, the group's first query row
-    int poison, seg, chunk, pad;  // bad block id or scale; segment number; the chunk's first position
+    int poison, seg, chunk, cuts; // bad block id or scale; segment number; the chunk's first position; any cut != 1
+    int ids[SB];
     float ks[SB], lb[SB], back[SB], cut[SB];   // key scale, lb, 2^-lb, f of decode_bs8.cuh
 };
 
-// 32 consecutive columns' worth of scores' maximum, 16 columns at a time.
+// Waits with a hint of how long the hardware may hold the warp before the test answers (20 us): a warp that
+// polls takes issue slots from the others.  In few instructions, because the roles' loops together
+// have to fit the instruction cache.
+__device__ __forceinline__ bool try_wait_held(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (!try_wait_held(bar, parity)) {
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) return false;
+    }
+    return true;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The maximum of 16 scores.
 __device__ __forceinline__ float max16(const uint32_t* u) {
-    float m[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m[i] = fmaxf(fmaxf(__uint_as_float(u[i]), __uint_as_float(u[i + 4])),
-                     fmaxf(__uint_as_float(u[i + 8]), __uint_as_float(u[i + 12])));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    auto f = [&](int i) -> float { return __uint_as_float(u[i]); };
+    const float a = max3(max3(f(0), f(1), f(2)), f(3), f(4)), b = max3(max3(f(5), f(6), f(7)), f(8), f(9));
+    const float c = max3(max3(f(10), f(11), f(12)), f(13), f(14));
+    return fmaxf(max3(a, b, c), f(15));
 }
 
 template <class Tr>
 __global__ void __launch_bounds__(Tr::THREADS, 1)
 pa_chunk_bs8_kernel(const MultiParams mp) {
-    constexpr int D = Tr::D, BS = Tr::BS, SB = Tr::SB, HALVES = Tr::HALVES, KEYS = Tr::KEYS, R = Tr::R, N8 = Tr::N8;
+    constexpr int D = Tr::D, BS = Tr::BS, SB = Tr::SB, HALVES = Tr::HALVES, KEYS = Tr::KEYS, R = Tr::R;
     constexpr bool SPLIT = Tr::SPLIT;
     constexpr uint32_t IDESC_S = idesc_f16<false>(128, KEYS, false, false);
     constexpr uint32_t IDESC_O = idesc_f16<false>(128, D, false, true);
@@ -163,50 +209,58 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
     const int lane = threadIdx.x & 31;
     const int G = p.Hq / p.Hkv, gs = 31 - __clz(G);           // a power of two
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t q_base = sbase + Tr::Q_OFF, ring = sbase + Tr::RING_OFF, ring8 = sbase + Tr::RING8_OFF;
-    auto full8 = [&](int st) -> uint32_t { return sbase + 8 * st; };
-    auto empty8 = [&](int st) -> uint32_t { return sbase + 8 * (Tr::N8_CAP + st); };
-    const uint32_t slot_bars = sbase + 8 * 2 * Tr::N8_CAP;
-    auto empty = [&](int st) -> uint32_t { return slot_bars + 8 * st; };
-    auto ready = [&](int st) -> uint32_t { return slot_bars + 8 * (R + st); };
-    const uint32_t tile_bars = slot_bars + 8 * 2 * R;
-    auto s_full = [&](int t) -> uint32_t { return tile_bars + 48 * t; };
-    auto p_part = [&](int t, int c) -> uint32_t { return tile_bars + 48 * t + 8 + 8 * c; };
-    auto pv_done = [&](int t) -> uint32_t { return tile_bars + 48 * t + 40; };
+    const uint32_t q_base = sbase + Tr::Q_OFF, ring = sbase + Tr::RING_OFF;
+    auto empty = [&](int st) -> uint32_t { return sbase + 8 * st; };
+    auto ready = [&](int st) -> uint32_t { return sbase + 8 * (Tr::R_CAP + st); };
+    auto empty8 = [&](int st) -> uint32_t { return sbase + 8 * (2 * Tr::R_CAP + st); };
+    auto full8 = [&](int st) -> uint32_t { return sbase + 8 * (2 * Tr::R_CAP + Tr::N8_CAP + st); };
+    // the slot of stage j's key codes (op 0) or value codes (1), and how often it has been used before
+    auto slot8 = [&](int op, int j) -> int { return op ? Tr::NK8 + j % Tr::NV8 : j % Tr::NK8; };
+    auto uses8 = [&](int op, int j) -> int { return op ? j / Tr::NV8 : j / Tr::NK8; };
+    const uint32_t ring8 = sbase + Tr::RING8_OFF;
+    const uint32_t tile_bars = sbase + 8 * (2 * Tr::R_CAP + 2 * Tr::N8_CAP);
+    auto s_full = [&](int t) -> uint32_t { return tile_bars + 48 * t; };                        // a stage's scores,
+    auto p_half = [&](int t, int h) -> uint32_t { return tile_bars + 48 * t + 16 + 8 * h; };    // half of its weights
+    auto pv_half = [&](int t, int h) -> uint32_t { return tile_bars + 48 * t + 32 + 8 * h; };   // and its products
     const uint32_t q_full = tile_bars + 96, q_empty = q_full + 8, fin = q_empty + 8;   // fin[2]
-    auto described = [&](int j) -> uint32_t { return fin + 16 + 8 * (j % Tr::NREC); };
-    // tile 1's scores of a stage come after tile 0's, tile 0's next ones after those have been issued
-    const uint32_t lead = fin + 16 + 8 * Tr::NREC, follow = lead + 8;
+    auto described = [&](int j) -> uint32_t { return fin + 16 + 8 * (j % Tr::NREC); };                // stage j's record stands
+    auto forgotten = [&](int j) -> uint32_t { return fin + 16 + 8 * (Tr::NREC + j % Tr::NREC); };      // no one reads it any more
+    auto listed = [&](int j) -> uint32_t { return fin + 16 + 8 * (2 * Tr::NREC + j % Tr::NREC); };     // its blocks do, without their scales
     // SPLIT: tile 1's state of a segment is there; tile 0 has read it
-    const uint32_t joined = follow + 8, o1_free = joined + 8;
+    const uint32_t joined = fin + 16 + 8 * 3 * Tr::NREC, o1_free = joined + 8;
     Stage* recs = reinterpret_cast<Stage*>(smem + Tr::REC_OFF);
     float* rowf = reinterpret_cast<float*>(smem + Tr::ROWF_OFF);
     float2* xch = reinterpret_cast<float2*>(smem + Tr::XCH_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Tr::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Tr::MISC_OFF + 4);
-    // (of segment s at s % NREC: no role is that many stages ahead of another)
+    // (of segment s at s % NSEG: no role is that many stages ahead of another)
     int* spoilt = reinterpret_cast<int*>(smem + Tr::SPOILT_OFF);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < N8; ++i) {
-            mbar_init(full8(i), 1);
-            mbar_init(empty8(i), 4);                // the converting warps are done with it
-        }
         for (int i = 0; i < R; ++i) {
-            mbar_init(empty(i), SPLIT ? 1 : 2);     // the products of its tile, or of both
-            mbar_init(ready(i), 4);
+            mbar_init(empty(i), SPLIT ? 1 : 2);     // its tile is done with it, or both are
+            mbar_init(ready(i), Tr::CONVERT_WARPS);
+        }
+        for (int i = 0; i < Tr::N8; ++i) {
+            mbar_init(empty8(i), Tr::CONVERT_WARPS);
+            mbar_init(full8(i), 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            for (int c = 0; c < 4; ++c) mbar_init(p_part(t, c), 4);
-            mbar_init(pv_done(t), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(p_half(t, h), 4);
+                mbar_init(pv_half(t, h), 1);
+            }
             mbar_init(fin + 8 * t, 1);
         }
-        mbar_init(q_full, 4);
+        mbar_init(q_full, Tr::CONVERT_WARPS);
         mbar_init(q_empty, 2);
-        for (int i = 0; i < Tr::NREC; ++i) mbar_init(described(i), 1);
-        mbar_init(lead, 1);
-        mbar_init(follow, 1);
+        for (int i = 0; i < Tr::NREC; ++i) {
+            mbar_init(described(i), 1);
+            mbar_init(listed(i), 1);
+            // converting warps, products, softmax warps, copies
+            mbar_init(forgotten(i), Tr::CONVERT_WARPS + 2 + 8 + 1);
+        }
         mbar_init(joined, 4);
         mbar_init(o1_free, 4);
         *abort_flag = 0;
@@ -262,193 +316,257 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
     // scores keep their order under a scale that is not negative; a sign goes into the queries
     const float scale_abs = fabsf(p.scale_log2);
 
-    // 256 x 168 + 128 x 104 + 128 x 64 registers: no more than the 512 x 128 of the launch
     if (warp >= Tr::MMA_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == Tr::COPY_WARP) {
-            // ============================================================ copies
-            // with one group the codes are read once per call; with more, other CTAs read them too
-            const uint64_t kv_pol = mp.groups == 1 ? l2_evict_first() : l2_evict_normal();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Tr::OTHER_REGS));
+        if (warp == Tr::PLAN_WARP) {
+            // ============================================================ the stages, and their blocks' scales
             if (lane == 0) mp.starts[blockIdx.x] = at;
-            int item = 0, st = 0, j = 0, nseg = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            auto claim = [&]() -> bool {             // lane 0: the slot's last use is over
-                return item < N8 || mbar_wait_bounded(empty8(st), ph ^ 1u, p.timeout_ns);
+            struct Next {                            // a stage whose blocks' scales are on their way
+                int base, kvh, t0, nbs, n, ctx, q0, flags, seg, chunk, id;
+                bool bad;
+                float2 scales;
             };
-            auto next_slot = [&]() {
-                ++item;
-                if (++st == N8) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            };
-            if (has_work) {
-                SegIter it{lo, at.s, at.kvh, at.b0, at.nb, 0};
-                while (ok && it.gi < hi) {
-                    const int len = seg_len(it, hi);
-                    const int s = it.s % seqs, skip = it.s / seqs * mp.group_nodes;
-                    const int size = chunk_size(s), n = min(mp.group_nodes, size - skip);   // > 0: it has blocks
-                    const int ctx = __ldg(p.context_lens + s), q0 = __ldg(qst + s) + skip;
-                    const long long P0 = it.gi - it.b0;
-                    const bool complete = sc.of(P0) == sc.of(P0 + it.nb - 1);
-                    const int seg_flags = (complete ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
-                    ++nseg;
-                    const int32_t* trow = p.block_tables + (size_t)s * p.MB + it.b0;
-                    auto batch = [&](int from) -> int { return lane < len - from ? __ldg(trow + from + lane) : 0; };
-                    int ids = batch(0), ids_next = batch(32);
-                    const int nst = (len + SB - 1) / SB;
-                    for (int k = 0; ok && k < nst; ++k, ++j) {
-                        const int bb = k * SB;
-                        if (bb > 0 && (bb & 31) == 0) {
-                            ids = ids_next;
-                            ids_next = batch(bb + 32);
-                        }
-                        const int nbs = min(SB, len - bb);
-                        int cid = __shfl_sync(0xffffffffu, ids, (bb + lane) & 31);
-                        const bool copies = lane < nbs;
-                        const bool bad = copies && (unsigned)cid >= (unsigned)p.NB;
-                        if (bad) cid = 0;
-                        const bool poison = __any_sync(0xffffffffu, bad);
-                        const uint8_t* piece = p.kv8 + ((size_t)cid * p.Hkv + it.kvh) * bs8_piece_bytes(BS, D);
-                        for (int op = 0; op < 2; ++op) {          // scales and keys, then values
-                            if (lane == 0) {
-                                if (!claim()) {
-                                    ok = false;
-                                } else {
-                                    if (op == 0) {
-                                        if (poison) set_err(p.err, PA_DEVERR_BLOCK_ID);
-                                        Stage& rc = recs[j % Tr::NREC];
-                                        rc.base = ctx - size + skip;
-                                        rc.kvh = it.kvh;
-                                        rc.t0 = (it.b0 + bb) * BS;
-                                        rc.nkeys = nbs * BS;
-                                        rc.n = n;
-                                        rc.ctx = ctx;
-                                        rc.q0 = q0;
-                                        rc.flags = seg_flags | (k == 0 ? TC_FIRST : 0) | (k == nst - 1 ? TC_LAST : 0);
-                                        rc.poison = poison;
-                                        rc.seg = nseg;
-                                        rc.chunk = ctx - size;
-                                    }
-                                    mbar_arrive_expect_tx(full8(st), (uint32_t)(nbs * (op ? Tr::V8_BYTES : Tr::K8_BYTES)));
-                                }
-                            }
-                            ok = __shfl_sync(0xffffffffu, ok, 0);
-                            __syncwarp();
-                            if (!ok) break;
-                            if (copies) {
-                                const uint32_t dst = ring8 + st * Tr::SLOT8_BYTES;
-                                if (op == 0)
-                                    bulk_load_hint(dst + lane * Tr::K8_BYTES, piece, Tr::K8_BYTES, full8(st), kv_pol);
-                                else
-                                    bulk_load_hint(dst + lane * Tr::V8_BYTES, piece + Tr::K8_BYTES, Tr::V8_BYTES, full8(st),
-                                                   kv_pol);
-                            }
-                            next_slot();
-                        }
-                    }
+            SegIter it{lo, at.s, at.kvh, at.b0, at.nb, 0};
+            const int32_t* trow = nullptr;
+            int len = 0, k = 0, nseg = 0, ids = 0, ids_next = 0, n = 0, ctx = 0, q0 = 0, size = 0, skip = 0, seg_flags = 0;
+            auto batch = [&](int from) -> int { return lane < len - from ? __ldg(trow + from + lane) : 0; };
+            auto advance = [&](Next& x) -> bool {
+                if (len > 0 && k * SB >= len) {      // the segment is done
                     seg_advance(it, len, p, tab);
+                    len = 0;
                 }
-            }
-            if (lane == 0) {
-                if (ok && claim()) {
-                    recs[j % Tr::NREC].flags = TC_END;
-                    mbar_arrive(full8(st));
-                    next_slot();
-                } else {
+                if (len == 0) {
+                    if (!has_work || it.gi >= hi) return false;
+                    len = seg_len(it, hi);
+                    k = 0;
+                    const int s = it.s % seqs;
+                    skip = it.s / seqs * mp.group_nodes;
+                    size = chunk_size(s);
+                    n = min(mp.group_nodes, size - skip);                      // > 0: it has blocks
+                    ctx = __ldg(p.context_lens + s);
+                    q0 = __ldg(qst + s) + skip;
+                    const long long P0 = it.gi - it.b0;
+                    seg_flags = (sc.of(P0) == sc.of(P0 + it.nb - 1) ? TC_COMPLETE : 0) | (it.gi == lo ? 0 : TC_SLOT1);
+                    ++nseg;
+                    trow = p.block_tables + (size_t)s * p.MB + it.b0;
+                    ids = batch(0);
+                    ids_next = batch(32);
+                }
+                const int bb = k * SB;
+                if (bb > 0 && (bb & 31) == 0) {
+                    ids = ids_next;
+                    ids_next = batch(bb + 32);
+                }
+                x.nbs = min(SB, len - bb);
+                x.id = __shfl_sync(0xffffffffu, ids, (bb + lane) & 31);
+                const bool held = lane < x.nbs;
+                x.bad = held && (unsigned)x.id >= (unsigned)p.NB;
+                if (!held || x.bad) x.id = 0;
+                x.scales = make_float2(0.f, 0.f);
+                if (held) x.scales = __ldg(reinterpret_cast<const float2*>(p.kv8 + ((size_t)x.id * p.Hkv + it.kvh) * bs8_piece_bytes(BS, D)));
+                x.base = ctx - size + skip;
+                x.kvh = it.kvh;
+                x.t0 = (it.b0 + bb) * BS;
+                x.n = n;
+                x.ctx = ctx;
+                x.q0 = q0;
+                x.flags = seg_flags | (k == 0 ? TC_FIRST : 0) | (bb + SB >= len ? TC_LAST : 0);
+                x.seg = nseg;
+                x.chunk = ctx - size;
+                ++k;
+                return true;
+            };
+            float top_lb = -INFINITY;                             // R of decode_bs8.cuh
+            bool ok = true;
+            Next x, y;
+            bool more = false;
+            for (int j = -1;; ++j) {
+                const bool then = (more || j < 0) && advance(y);
+                if (j < 0) {
+                    x = y;
+                    more = then;
+                    continue;
+                }
+                const bool stop = j >= Tr::NREC && (*abort_flag != 0 || !wait_bounded(forgotten(j), (uint32_t)((j / Tr::NREC - 1) & 1), p.timeout_ns));
+                if (__any_sync(0xffffffffu, stop)) {
                     ok = false;
+                    break;
                 }
-                if (!ok) {
+                Stage& rc = recs[j % Tr::NREC];
+                if (!more) {
+                    if (lane == 0) {
+                        rc.flags = TC_END;
+                        mbar_arrive(listed(j));
+                        mbar_arrive(described(j));
+                    }
+                    break;
+                }
+                if (x.flags & TC_FIRST) {
+                    top_lb = -INFINITY;
+                    if (lane == 0) spoilt[x.seg % Tr::NSEG] = INT_MAX;
+                }
+                // what the copies need goes ahead of what waits for the scales
+                if (lane < SB) rc.ids[lane] = x.id;
+                if (lane == 0) {
+                    rc.base = x.base;
+                    rc.kvh = x.kvh;
+                    rc.t0 = x.t0;
+                    rc.nkeys = x.nbs * BS;
+                    rc.n = x.n;
+                    rc.ctx = x.ctx;
+                    rc.q0 = x.q0;
+                    rc.flags = x.flags;
+                    rc.seg = x.seg;
+                    rc.chunk = x.chunk;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(listed(j));
+                const bool held_here = lane < x.nbs;
+                const bool bad_scale = held_here && (!bs8_is_scale(x.scales.x) || !bs8_is_scale(x.scales.y));
+                const float lb = held_here ? fmaxf(__log2f(x.scales.y), -126.f) : -INFINITY;
+                float top = lb;
+#pragma unroll
+                for (int o = 1; o < SB; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top_lb = fmaxf(top_lb, __shfl_sync(0xffffffffu, top, 0));
+                const float held = fmaxf(lb, fmaxf(top_lb - BS8_LB_RANGE, BS8_LB_FLOOR));
+                const float cut = held_here ? ex2(lb - held) : 1.f;
+                if (lane < SB) {
+                    rc.ks[lane] = x.scales.x;
+                    rc.lb[lane] = held;
+                    rc.back[lane] = ex2(-held);
+                    rc.cut[lane] = cut;
+                }
+                const bool any_id = __any_sync(0xffffffffu, x.bad), any_scale = __any_sync(0xffffffffu, bad_scale);
+                const bool any_cut = __any_sync(0xffffffffu, cut != 1.f);
+                if (lane == 0) {
+                    if (any_id) set_err(p.err, PA_DEVERR_BLOCK_ID);
+                    if (any_scale) set_err(p.err, PA_DEVERR_SCALE);
+                    rc.poison = any_id || any_scale;
+                    rc.cuts = any_cut;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(described(j));
+                x = y;
+                more = then;
+            }
+            if (!ok && lane == 0) {
+                set_err(p.err, PA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+        } else if (warp == Tr::COPY_WARP) {
+            // ============================================================ copies of the codes
+            {
+                // with one group the codes are read once per call; with more, other CTAs read them too
+                const uint64_t kv_pol = mp.groups == 1 ? l2_evict_first() : l2_evict_normal();
+                int copied[2] = {0, 0};
+                bool ok = true;
+                for (int j = 0; ok; ++j) {
+                    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+                        const bool good = *abort_flag == 0 && wait_bounded(bar, parity, p.timeout_ns);
+                        return __all_sync(0xffffffffu, good);
+                    };
+                    if (!wait(listed(j), (uint32_t)((j / Tr::NREC) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    const Stage& rc = recs[j % Tr::NREC];
+                    if (rc.flags & TC_END) break;
+                    const int nbs = rc.nkeys / BS;
+                    const uint8_t* codes = p.kv8 + ((size_t)rc.ids[lane < nbs ? lane : 0] * p.Hkv + rc.kvh) * bs8_piece_bytes(BS, D) + BS8_HEAD;
+                    for (int op = 0; op < 2; ++op) {              // keys, values
+                        const int st = slot8(op, j), n = uses8(op, j);
+                        if (n > 0 && !wait(empty8(st), (uint32_t)((n - 1) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(full8(st), (uint32_t)(nbs * BS * D));
+                        __syncwarp();
+                        if (lane < nbs)
+                            bulk_load_hint(ring8 + st * Tr::SLOT8_BYTES + lane * BS * D, codes + op * BS * D, BS * D, full8(st), kv_pol);
+                        ++copied[op];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(forgotten(j));
+                }
+                if (!ok && lane == 0) {
                     set_err(p.err, PA_DEVERR_TIMEOUT);
                     *abort_flag = 1;
                     // copies still in flight land before the CTA's shared memory is released
-                    for (int k = item - N8 > 0 ? item - N8 : 0; k < item; ++k)
-                        mbar_wait_bounded(full8(k % N8), (uint32_t)((k / N8) & 1), p.timeout_ns);
+                    for (int op = 0; op < 2; ++op)
+                        for (int k = max(0, copied[op] - (op ? Tr::NV8 : Tr::NK8)); k < copied[op]; ++k)
+                            wait_bounded(full8(slot8(op, k)), (uint32_t)(uses8(op, k) & 1), p.timeout_ns);
                 }
             }
-        } else if (warp < Tr::COPY_WARP && lane == 0) {
+        } else if (lane == 0) {
             // ============================================================ products of one tile
             const int t = warp - Tr::MMA_WARP;
             const uint32_t s_col = tmem + 128 * t, o_col = tmem + Tr::O_COL + 128 * t;
             const uint32_t q_tile = q_base + (SPLIT ? 0 : t * HALVES * Tr::Q_HALF);
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-                if (mbar_try_wait(bar, parity)) return true;
-                if (*abort_flag || !mbar_wait_bounded(bar, parity, p.timeout_ns)) ok = false;
+                if (__builtin_expect(try_wait_held(bar, parity), 1)) return true;
+                if (*abort_flag || !wait_bounded(bar, parity, p.timeout_ns)) ok = false;
                 return ok;
             };
-            int own = 0, nseg = 0;                                // stages of this tile, segments begun
-            bool fresh = true;                                    // O holds nothing of the segment
-            bool issued = false;                                  // a PV product of stage own - 1
+            int own = 0, nseg = 0;                 // stages of this tile; segments begun
+            bool fresh = true;                     // O holds nothing of the segment
+            bool active = true;
             for (int j = 0;; ++j) {
                 if (!wait(described(j), (uint32_t)((j / Tr::NREC) & 1))) break;
                 const Stage& rc = recs[j % Tr::NREC];
                 const int flags = rc.flags;
                 if (flags & TC_END) break;
-                const bool active = SPLIT || rc.n > t * tile_nodes;
                 if (flags & TC_FIRST) {
                     if (!wait(q_full, (uint32_t)(nseg & 1))) break;
                     ++nseg;
                     fresh = true;
+                    active = SPLIT || rc.n > t * tile_nodes;
                 }
+                mbar_arrive(forgotten(j));
                 if (SPLIT && (j & 1) != t) {                      // the other tile's stage
                     if (flags & TC_LAST) mma_commit(q_empty);
                     continue;
                 }
-                const int ik = 2 * j, iv = 2 * j + 1;
-                const int ks = ik % R, vs = iv % R;
+                const int ks = 2 * j % R, vs = (2 * j + 1) % R;
                 const uint32_t par = (uint32_t)(own & 1);
-                if (!wait(ready(ks), (uint32_t)((ik / R) & 1))) break;
-                // the scores overwrite the weights of the stage before
-                if (issued && !wait(pv_done(t), par ^ 1u)) break;
-                if (!SPLIT && (t == 1 ? !wait(lead, par) : j > 0 && !wait(follow, par ^ 1u))) break;
+                if (!wait(ready(ks), (uint32_t)((2 * j / R) & 1))) break;
                 if (active) {
                     tc_fence_after();
-                    const uint64_t qd = sdesc_sw128(q_tile, 16, 1024);
-                    const uint64_t kd = sdesc_sw128(ring + ks * Tr::SLOT_BYTES, 16, 1024);
-#pragma unroll
+                    const uint64_t qd = sdesc_sw128(q_tile, 16, 1024), kd = sdesc_sw128(ring + ks * Tr::SLOT_BYTES, 16, 1024);
+#pragma unroll (SPLIT ? 1 : D / 16)               // (256 rows: 70 us slower rolled; SPLIT: 50 us faster)
                     for (int k = 0; k < D / 16; ++k)
                         mma_f16(s_col, qd + (uint64_t)((k / 4) * (Tr::Q_HALF >> 4) + (k % 4) * 2),
                                 kd + (uint64_t)((k / 4) * (Tr::HALF_STRIDE >> 4) + (k % 4) * 2), IDESC_S, k > 0 ? 1u : 0u);
                     mma_commit(s_full(t));
-                    if (!SPLIT && t == 0) mma_commit(lead);
-                    mma_commit(empty(ks));
                     if (flags & TC_LAST) mma_commit(q_empty);
                 } else {
                     mbar_arrive(s_full(t));
-                    if (!SPLIT && t == 0) mbar_arrive(lead);
-                    mbar_arrive(empty(ks));
                     if (flags & TC_LAST) mbar_arrive(q_empty);
                 }
-                if (!SPLIT && t == 1) mbar_arrive(follow);
-                if (!wait(ready(vs), (uint32_t)((iv / R) & 1))) break;
-                const uint64_t vd = sdesc_sw128(ring + vs * Tr::SLOT_BYTES, Tr::HALF_STRIDE, 1024);
+                if (!wait(ready(vs), (uint32_t)(((2 * j + 1) / R) & 1))) break;
                 bool stop = false;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {                     // as each quarter of the weights is there
-                    if (!wait(p_part(t, h), par)) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {                     // as each half of the weights is there
+                    if (!wait(p_half(t, h), par)) {
                         stop = true;
                         break;
                     }
                     if (active) {
                         tc_fence_after();
-#pragma unroll
-                        for (int k = 2 * h; k < 2 * h + 2; ++k)
-                            mma_f16_ts(o_col, s_col + 32 * (k / 2) + 8 * (k % 2), vd + (uint64_t)(k * (2048 >> 4)), IDESC_O,
-                                       fresh && k == 0 ? 0u : 1u);
+                        const uint64_t vd = sdesc_sw128(ring + vs * Tr::SLOT_BYTES + h * 8192, Tr::HALF_STRIDE, 1024);
+#pragma unroll (SPLIT ? 1 : 4)
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_ts(o_col, s_col + 64 * h + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), IDESC_O,
+                                       fresh && h + k == 0 ? 0u : 1u);
+                        mma_commit(pv_half(t, h));
+                    } else {
+                        mbar_arrive(pv_half(t, h));
                     }
                 }
-                if (stop) break;
+                // the next scores overwrite the weights
+                if (stop || !wait(pv_half(t, 1), par)) break;
+                mbar_arrive(empty(vs));                           // the stage's values are used up
                 fresh = false;
-                issued = active;
-                if (active) {
-                    mma_commit(pv_done(t));
-                    mma_commit(empty(vs));
-                } else {
-                    mbar_arrive(pv_done(t));
-                    mbar_arrive(empty(vs));
-                }
                 ++own;
             }
             if (!ok) {
@@ -457,138 +575,101 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
             }
             // every MMA of this thread completes before tensor memory is released
             mma_commit(fin + 8 * t);
-            mbar_wait_bounded(fin + 8 * t, 0, p.timeout_ns);
+            wait_bounded(fin + 8 * t, 0, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp >= Tr::CONVERT_WARP) {
         // ================================================================ queries, keys and values to fp16
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Tr::CONVERT_REGS));
         const int cw = warp - Tr::CONVERT_WARP;
-        // A lane's share of a row: one 16-byte part of codes.  Eight neighbouring lanes hold
-        // four parts each of two neighbouring rows (D 128: of different halves), which are read
-        // from eight different 16-byte bank groups and, as fp16, written to eight.
+        // A lane's share of a row: one 16-byte part of codes.  Eight neighbouring lanes hold four
+        // parts each of two neighbouring rows, a warp 512 consecutive bytes of a piece; as fp16 the eight
+        // lanes' parts fall into eight different 16-byte bank groups.
         constexpr int RPW = D == 128 ? 4 : 8;                     // rows a warp takes at once
-        constexpr int NI = KEYS / (4 * RPW);                      // such rounds in a slot
+        constexpr int STEP = Tr::CONVERT_WARPS * RPW;             // rows of a round
+        constexpr int NI = KEYS / STEP;                           // rounds of a slot
         const int part = D == 128 ? (lane & 3) | (((lane >> 2) ^ (lane >> 3)) & 1) << 2 : lane & 3;
         const int row0 = cw * RPW + (D == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2);
-        int j = 0, st8 = 0, st = 0, nseg = 0;
-        uint32_t ph8 = 0, ph = 0;
+        int nseg = 0;
         bool ok = true;
-        float top_lb = -INFINITY;
         auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait_bounded(bar, parity, p.timeout_ns));
+            if (__builtin_expect(__all_sync(0xffffffffu, try_wait_held(bar, parity)), 1)) return true;
+            return __all_sync(0xffffffffu, *abort_flag == 0 && wait_bounded(bar, parity, p.timeout_ns));
         };
-        // codes -> fp16 at (row, part) of the slot
-        auto put = [&](uint32_t slot, int row, const uint4& c, uint32_t by, bool scaled) {
-            uint32_t h[8];
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        // sixteen codes -> sixteen values
+        auto widen = [&](const uint32_t (&c)[4], uint32_t (&h)[8]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                h[2 * i] = fp8x2_to_f16x2<Tr::E5M2>((uint16_t)(w[i] & 0xffffu));
-                h[2 * i + 1] = fp8x2_to_f16x2<Tr::E5M2>((uint16_t)(w[i] >> 16));
-            }
-            if (scaled) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(by));
-            }
-            const uint32_t a = slot + (part >> 2) * Tr::HALF_STRIDE + row * 128;
-            const int c0 = 2 * (part & 3), x = row & 7;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + ((c0 ^ x) << 4)), "r"(h[0]), "r"(h[1]),
-                         "r"(h[2]), "r"(h[3]) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + (((c0 + 1) ^ x) << 4)), "r"(h[4]), "r"(h[5]),
-                         "r"(h[6]), "r"(h[7]) : "memory");
-        };
-        auto next = [&](int& s, uint32_t& parity, int n) {
-            if (++s == n) {
-                s = 0;
-                parity ^= 1u;
+                fp8x4_to_f16x4<Tr::E5M2>(c[i], h[2 * i], h[2 * i + 1]);
             }
         };
-        for (;; ++j) {
-            if (!wait_all(full8(st8), ph8)) {
-                ok = false;
-                break;
-            }
+        // the lane's place in a slot: its two 16-byte parts of row row0; round i is i * STEP rows on
+        const uint32_t put0 = (part >> 2) * Tr::HALF_STRIDE + row0 * 128;
+        const uint32_t put_a = put0 + (((2 * (part & 3)) ^ (row0 & 7)) << 4), put_b = put0 + (((2 * (part & 3) + 1) ^ (row0 & 7)) << 4);
+        auto put = [&](uint32_t slot, int i, const uint32_t (&h)[8]) {
+            const uint32_t a = slot + i * (STEP * 128);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + put_a), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + put_b), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                         : "memory");
+        };
+        auto place = [&](int op, int row) -> uint32_t {           // of the lane's part in a slot of codes
+            return (row / BS) * BS * D +
+                   (op ? bs8_value<BS, D>(row % BS, part) - BS * D - BS8_HEAD : bs8_key<D>(row % BS, part) - BS8_HEAD);
+        };
+        // item 2 j (+ 1): keys (values) of stage j, into slot item % R once its last use is over
+        auto claim = [&](int item) -> bool { return item < R || wait_all(empty(item % R), (uint32_t)((item / R - 1) & 1)); };
+        auto done = [&](int item) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready(item % R));
+        };
+        bool end = !wait_all(described(0), 0);
+        ok = !end;
+        for (int j = 0; ok; ++j) {
             Stage& rc = recs[j % Tr::NREC];
             const int flags = rc.flags;
-            if (flags & TC_END) {
-                __syncwarp();
-                if (cw == 0 && lane == 0) mbar_arrive(described(j));
-                break;
-            }
-            const int nkeys = rc.nkeys, nbs = nkeys / BS;
-            uint8_t* k8 = smem + Tr::RING8_OFF + st8 * Tr::SLOT8_BYTES;
-            if (cw == 0) {                                        // the blocks' scales
-                if (flags & TC_FIRST) {
-                    top_lb = -INFINITY;
-                    if (lane == 0) spoilt[rc.seg % Tr::NREC] = INT_MAX;
-                }
-                float ks = 0.f, lb = -INFINITY;
-                bool bad = false;
-                if (lane < nbs) {
-                    const float2 sc2 = *reinterpret_cast<const float2*>(k8 + lane * Tr::K8_BYTES);
-                    bad = !bs8_is_scale(sc2.x) || !bs8_is_scale(sc2.y);
-                    ks = sc2.x;
-                    lb = fmaxf(__log2f(sc2.y), -126.f);
-                }
-                float top = lb;
-#pragma unroll
-                for (int o = 1; o < SB; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                top_lb = fmaxf(top_lb, __shfl_sync(0xffffffffu, top, 0));
-                if (lane < SB) {
-                    const float held = fmaxf(lb, fmaxf(top_lb - BS8_LB_RANGE, BS8_LB_FLOOR));
-                    rc.ks[lane] = ks;
-                    rc.lb[lane] = held;
-                    rc.back[lane] = ex2(-held);
-                    rc.cut[lane] = lane < nbs ? ex2(lb - held) : 0.f;
-                }
-                if (__any_sync(0xffffffffu, bad) && lane == 0) {
-                    set_err(p.err, PA_DEVERR_SCALE);
-                    rc.poison = 1;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(described(j));
-            }
+            if (flags & TC_END) break;
             if (flags & TC_FIRST) {                               // the segment's queries
                 if (nseg > 0 && !wait_all(q_empty, (uint32_t)((nseg - 1) & 1))) {
                     ok = false;
                     break;
                 }
-                const int rows = min(rc.n << gs, Tr::ROWS), r = 32 * cw + lane;
-                for (int t = 0; t < (SPLIT ? 1 : 2); ++t) {
-                    const int row = t * Tr::TILE + r;
-                    if (!__any_sync(0xffffffffu, row < rows)) {   // nothing but rows that no one reads
-                        if (t * Tr::TILE >= rows) break;
-                        // (a partly filled tile: they have to be finite)
-                    }
-                    uint4 x[D / 8];
-                    uint32_t top = 0;
-                    const uint16_t* src = p.q + ((size_t)(rc.q0 + (row >> gs)) * p.Hq + (size_t)rc.kvh * G + (row & (G - 1))) * D;
+                // four lanes hold a row; rows past the last one in a tile have to be finite: zeros
+                constexpr int NQ = D / 32;                        // 16-byte parts of a lane
+                const int rows = min(rc.n << gs, Tr::ROWS), end = (rows + Tr::TILE - 1) / Tr::TILE * Tr::TILE;
+#pragma unroll 1
+                for (int row = 8 * cw + lane / 4; row < end; row += 8 * Tr::CONVERT_WARPS) {
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        p.q + ((size_t)(rc.q0 + (row >> gs)) * p.Hq + (size_t)rc.kvh * G + (row & (G - 1))) * D);
+                    uint4 x[NQ];
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                    }
+                    for (int i = 0; i < NQ; ++i) x[i] = row < rows ? __ldg(src + (lane & 3) + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
                     float2 f = make_float2(1.f, 1.f);
                     if constexpr (Tr::BF16) {
+                        uint32_t top = 0;
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i)
+                        for (int i = 0; i < NQ; ++i)
                             top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
                                                          __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
                         top = max(top & 0xffffu, top >> 16);
                         f = row_factor((int)(top >> 7));
                     }
                     if (p.scale_log2 < 0.f) f.x = -f.x;
-                    rowf[(nseg & 1) * 2 * Tr::TILE + row] = f.y * scale_abs;
-                    const uint32_t a = q_base + t * HALVES * Tr::Q_HALF + r * 128;
+                    if ((lane & 3) == 0) rowf[(nseg & 1) * 2 * Tr::TILE + row] = f.y * scale_abs;
+                    const int r = row % Tr::TILE;
+                    const uint32_t a = q_base + row / Tr::TILE * (HALVES * Tr::Q_HALF) + r * 128;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
+                    for (int i = 0; i < NQ; ++i) {
+                        const int c = (lane & 3) + 4 * i;
                         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                         uint32_t h[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             h[e] = pack2<false>(lo_of<Tr::BF16>(w[e]) * f.x, hi_of<Tr::BF16>(w[e]) * f.x);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + (i / 8) * Tr::Q_HALF + (((i & 7) ^ (r & 7)) << 4)),
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + (c / 8) * Tr::Q_HALF + (((c & 7) ^ (r & 7)) << 4)),
                                      "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
                     }
                 }
@@ -597,74 +678,54 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
-            // keys
-            const int item = 2 * j;
-            if (item >= R && !wait_all(empty(st), ph ^ 1u)) {
-                ok = false;
-                break;
-            }
-            {
-                const uint32_t slot = ring + st * Tr::SLOT_BYTES;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int row = row0 + i * 4 * RPW, b = row / BS;
-                    const uint4 c = *reinterpret_cast<const uint4*>(k8 + b * Tr::K8_BYTES + bs8_key<D>(row % BS, part));
-                    put(slot, row, c, 0u, false);
+            const int t0 = rc.t0, held = min(rc.nkeys, rc.ctx - t0), from = rc.chunk - t0;   // rows with values; of the chunk
+            const bool cuts = rc.cuts;
+#pragma unroll 1
+            for (int op = 0; op < 2 && ok; ++op) {                // keys, values
+                const int st = slot8(op, j), item = 2 * j + op;
+                if (!wait_all(full8(st), (uint32_t)(uses8(op, j) & 1)) || !claim(item)) {
+                    ok = false;
+                    break;
                 }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(ready(st));
-                mbar_arrive(empty8(st8));
-            }
-            next(st, ph, R);
-            next(st8, ph8, N8);
-            // values (the scales are in the record: this warp's wait makes warp 8's stores visible)
-            if (!wait_all(described(j), (uint32_t)((j / Tr::NREC) & 1)) || !wait_all(full8(st8), ph8) ||
-                (item + 1 >= R && !wait_all(empty(st), ph ^ 1u))) {
-                ok = false;
-                break;
-            }
-            {
-                const uint32_t slot = ring + st * Tr::SLOT_BYTES;
-                const uint8_t* v8 = smem + Tr::RING8_OFF + st8 * Tr::SLOT8_BYTES - Tr::K8_BYTES;   // where the pieces' keys would be
-                const int t0 = rc.t0, held = min(nkeys, rc.ctx - t0), from = rc.chunk - t0;   // rows with values; of the chunk
-                const bool plain = held == KEYS && from >= KEYS;
-#pragma unroll
+                const uint32_t src = ring8 + st * Tr::SLOT8_BYTES, slot = ring + (item % R) * Tr::SLOT_BYTES;
+                const uint32_t in0 = place(op, row0), in1 = place(op, row0 + STEP);
+                const bool care = op && (held < KEYS || from < KEYS || cuts);
+#pragma unroll (SPLIT ? 1 : 2)                            // (SPLIT: unrolled it spills, 673 us to 635)
                 for (int i = 0; i < NI; ++i) {
-                    const int row = row0 + i * 4 * RPW, b = row / BS;
-                    uint4 c = *reinterpret_cast<const uint4*>(v8 + b * Tr::V8_BYTES + bs8_value<BS, D>(row % BS, part));
-                    const float cut = rc.cut[b];
-                    if (!plain) {
-                        if (row >= held) {
-                            c = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (row >= from) {
-                            // NaN and infinite codes: all but the sign set (E4M3), the exponent all ones (E5M2)
-                            auto odd = [](uint32_t w) -> uint32_t {
-                                return Tr::E5M2 ? ((w & 0x7f7f7f7fu) + 0x04040404u) & 0x80808080u
-                                                : ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            };
-                            if (odd(c.x) | odd(c.y) | odd(c.z) | odd(c.w)) {
-                                atomicMin(&spoilt[rc.seg % Tr::NREC], t0 + row);
-                                c.x &= ~(odd(c.x) / 128 * 255);
-                                c.y &= ~(odd(c.y) / 128 * 255);
-                                c.z &= ~(odd(c.z) / 128 * 255);
-                                c.w &= ~(odd(c.w) / 128 * 255);
+                    uint32_t c[4], h[8];
+                    const int row = row0 + i * STEP;
+                    lds128(src + (i / 2) * (2 * STEP * D) + (i & 1 ? in1 : in0), c);
+                    if (care) {
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t odd = ((c[e] & 0x7f7f7f7fu) + (Tr::E5M2 ? 0x04040404u : 0x01010101u)) & 0x80808080u;
+                            if (row >= from) {
+                                any |= odd;
+                                c[e] &= ~(odd / 128 * 255);
                             }
+                            if (row >= held) c[e] = 0u;
                         }
+                        if (any && row < held) atomicMin(&spoilt[rc.seg % Tr::NSEG], t0 + row);
                     }
-                    put(slot, row, c, pack2<false>(cut, cut), cut != 1.f);
+                    widen(c, h);
+                    if (care && cuts) {                           // blocks of next to nothing
+                        const float cut = rc.cut[row / BS];
+                        const uint32_t by = pack2<false>(cut, cut);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(by));
+                    }
+                    put(slot, i, h);
                 }
+                done(item);
+                if (lane == 0) mbar_arrive(empty8(st));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(ready(st));
-                mbar_arrive(empty8(st8));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(forgotten(j));
+            if (!wait_all(described(j + 1), (uint32_t)(((j + 1) / Tr::NREC) & 1))) {
+                ok = false;
+                break;
             }
-            next(st, ph, R);
-            next(st8, ph8, N8);
         }
         if (!ok && lane == 0) {
             set_err(p.err, PA_DEVERR_TIMEOUT);
@@ -672,18 +733,19 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         }
     } else {
         // ================================================================ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Tr::SOFT_REGS));
         const int t = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;                        // row of the tile = TMEM lane
         const int row_of_group = SPLIT ? r : t * Tr::TILE + r;
         const int token = row_of_group >> gs;                     // of the group
         auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.timeout_ns));
+            if (__builtin_expect(__all_sync(0xffffffffu, try_wait_held(bar, parity)), 1)) return true;
+            return __all_sync(0xffffffffu, wait_bounded(bar, parity, p.timeout_ns));
         };
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lane_addr + 128 * t, o_addr = lane_addr + Tr::O_COL + 128 * t;
         const float qnan = __int_as_float(0x7fc00000);
-        int own = 0, cur_seg = 0, pois = 0;
+        int own = 0, cur_seg = 0, pois = 0, seg_q0 = 0, seg_kvh = 0, last_seen = 0;
         float m = -INFINITY, l = 0.f, rf = 0.f;                   // reference (log2 units), sum, the row's score factor
         bool alive = false, active = false, fresh = true, ok = true;
         for (int j = 0;; ++j) {
@@ -697,6 +759,9 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
             if (flags & TC_END) break;
             if (flags & TC_FIRST) {
                 cur_seg = rc.seg;
+                seg_q0 = rc.q0;                                   // (a record may be written again before a segment's end is over)
+                seg_kvh = rc.kvh;
+                last_seen = rc.base + token;
                 m = -INFINITY;
                 l = 0.f;
                 pois = 0;
@@ -709,127 +774,133 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
             const bool busy = active && __any_sync(0xffffffffu, alive);
             if (mine) {
                 const uint32_t par = (uint32_t)(own & 1);
-                const int seen = rc.base + token - rc.t0 + 1;     // keys of the stage that the row sees
-                if (!wait_all(s_full(t), par)) {
-                    ok = false;
-                    break;
-                }
+                const int seen = last_seen - rc.t0 + 1;     // keys of the stage that the row sees
                 if (busy) {
+                    if (!wait_all(s_full(t), par)) {
+                        ok = false;
+                        break;
+                    }
+                    if (quarter == 0 && lane == 0) mbar_arrive(empty(2 * j % R));   // the stage's keys are used up
                     tc_fence_after();
                     if (fresh) rf = rowf[((cur_seg - 1) & 1) * 2 * Tr::TILE + row_of_group];
-                    uint32_t u[32];
-                    const int vis = alive ? min(seen, rc.nkeys) : KEYS;
-                    const bool masked = __any_sync(0xffffffffu, vis < KEYS);
-                    if (masked) {
-                        // the last stages of a row: scores become final here, -inf where the row does not
-                        // see the key, and the loops below, which every stage runs, stay short
-#pragma unroll 1
-                        for (int c = 0; c < KEYS / 32; ++c) {
-                            tmem_ld32(s_addr + 32 * c, u);
-                            tmem_ld_wait();
-                            after_wait(u);
-                            const float by0 = rc.ks[32 * c / BS] * rf, by1 = rc.ks[(32 * c + 16) / BS] * rf;
-                            const float lb0 = rc.lb[32 * c / BS], lb1 = rc.lb[(32 * c + 16) / BS];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float x = fmaf(__uint_as_float(u[k]), k < 16 ? by0 : by1, k < 16 ? lb0 : lb1);
-                                u[k] = 32 * c + k < vis ? __float_as_uint(x) : 0xff800000u;
-                            }
-                            tmem_st32(s_addr + 32 * c, u);
-                        }
-                        tmem_st_wait();
-                    }
-                    auto factor = [&](int key) -> float { return masked ? 1.f : rc.ks[key / BS] * rf; };
-                    auto offset = [&](int key) -> float { return masked ? 0.f : rc.lb[key / BS]; };
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        tmem_ld32(s_addr + 32 * c, u);
-                        tmem_ld_wait();
-                        after_wait(u);
-                        if constexpr (BS == 16) {
-                            mx = fmaxf(mx, fmaxf(fmaf(max16(u), factor(32 * c), offset(32 * c)),
-                                                 fmaf(max16(u + 16), factor(32 * c + 16), offset(32 * c + 16))));
-                        } else {
-                            mx = fmaxf(mx, fmaf(fmaxf(max16(u), max16(u + 16)), factor(32 * c), offset(32 * c)));
-                        }
-                    }
-                    const bool need = mx > m + Tr::TAU && alive;
-                    const float alpha = need ? ex2(m - mx) : 1.f;     // m = -inf: 0
-                    if (need) {
-                        m = mx;
-                        l *= alpha;
-                    }
-                    if (!fresh && __any_sync(0xffffffffu, need)) {
-                        // O holds the earlier stages: their products are done (the scores were issued after them)
-                        if (!wait_all(pv_done(t), par ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld32(o_addr + 32 * c, u);
-                            tmem_ld_wait();
-                            after_wait(u);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * alpha);
-                            tmem_st32(o_addr + 32 * c, u);
-                        }
-                        tmem_st_wait();
-                    }
                     if (SPLIT && t == 1 && fresh && cur_seg > 1) {    // tile 0 has read the last segment's O
                         if (!wait_all(o1_free, (uint32_t)((cur_seg - 2) & 1))) {
                             ok = false;
                             break;
                         }
                     }
-                    tmem_ld32(s_addr, u);
-                    const float mref = m == -INFINITY ? 0.f : m;      // no visible key yet: weights 0
-                    tmem_ld_wait();
-                    after_wait(u);
+                    const int vis = alive ? min(seen, rc.nkeys) : KEYS;
+                    const bool masked = __any_sync(0xffffffffu, vis < KEYS);
+                    if (masked) {
+                        // The last stages of a row: scores become final here, -inf where the row does not see the
+                        // key, in tensor memory, so that the loop below, which every stage runs, has one form.
 #pragma unroll 1
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        uint32_t w[16];
+                        for (int c = 0; c < KEYS / 16; ++c) {
+                            uint32_t x[16];
+                            tmem_ld16(s_addr + 16 * c, x);
+                            const float by = rc.ks[16 * c / BS] * rf, add = rc.lb[16 * c / BS];
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const float by = factor(32 * c + 16 * b), add = offset(32 * c + 16 * b) - mref;
-                            const f32x2 by2 = pair2(by, by), add2x = pair2(add, add);
-                            f32x2 sum[2] = {0ull, 0ull};
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(x[k]));
+                                x[k] = 16 * c + k < vis ? __float_as_uint(fmaf(__uint_as_float(x[k]), by, add)) : 0xff800000u;
+                            }
+                            tmem_st16(s_addr + 16 * c, x);
+                        }
+                        tmem_st_wait();
+                    }
+                    // Half of the scores at a time becomes weights in the first 32 of the 64 columns that held
+                    // them.  The row's reference is looked at once a half, so scores are read once; when it
+                    // moves, O is rescaled behind the products of the half before.
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t u[64];
+                        tmem_ld64_wait(s_addr + 64 * h, u);
+                        float by[4], add[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            by[b] = masked ? 1.f : rc.ks[(64 * h + 16 * b) / BS] * rf;
+                            add[b] = masked ? 0.f : rc.lb[(64 * h + 16 * b) / BS];
+                        }
+                        const float mx = fmaxf(fmaxf(fmaf(max16(u), by[0], add[0]), fmaf(max16(u + 16), by[1], add[1])),
+                                               fmaxf(fmaf(max16(u + 32), by[2], add[2]), fmaf(max16(u + 48), by[3], add[3])));
+                        const bool need = mx > m + Tr::TAU && alive;
+                        if (__any_sync(0xffffffffu, need)) {
+                            const float alpha = need ? ex2(m - mx) : 1.f;     // m = -inf: 0
+                            if (need) {
+                                m = mx;
+                                l *= alpha;
+                            }
+                            if (!fresh || h > 0) {
+                                if (!wait_all(pv_half(t, h ^ 1), h == 0 ? par ^ 1u : par)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int i = 0; i < D / 16; ++i) {
+                                    uint32_t x[16];
+                                    tmem_ld16(o_addr + 16 * i, x);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        asm volatile("" : "+r"(x[k]));
+                                        x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+                                    }
+                                    tmem_st16(o_addr + 16 * i, x);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                        const float mref = m == -INFINITY ? 0.f : m;          // no visible key yet: weights 0
+                        uint32_t w[32];
+                        float sum = 0.f;
+                        auto weigh = [&](const uint32_t* x, int b) {          // 16 scores -> 8 columns of weights
+                            const f32x2 by2 = pair2(by[b], by[b]), add2x = pair2(add[b] - mref, add[b] - mref);
+                            f32x2 s2[2] = {0ull, 0ull};
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const int i = 16 * b + 2 * e;
                                 float p0, p1;
-                                split2(fma2(pair2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), by2, add2x), p0, p1);
+                                split2(fma2(pair2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), by2, add2x), p0, p1);
                                 p0 = ex2(p0);
                                 p1 = ex2(p1);
-                                sum[e & 1] = add2(sum[e & 1], pair2(p0, p1));
+                                s2[e & 1] = add2(s2[e & 1], pair2(p0, p1));
                                 w[8 * b + e] = pack2<false>(p0, p1);
                             }
                             float sa, sb;
-                            split2(add2(sum[0], sum[1]), sa, sb);
-                            l = fmaf(sa + sb, rc.back[(32 * c + 16 * b) / BS], l);
-                        }
-                        if (c + 1 < KEYS / 32) tmem_ld32(s_addr + 32 * c + 32, u);
-                        tmem_st16(s_addr + 32 * c, w);
-                        tmem_st_wait();                               // a quarter of the weights is there
+                            split2(add2(s2[0], s2[1]), sa, sb);
+                            sum = fmaf(sa + sb, rc.back[(64 * h + 16 * b) / BS], sum);
+                        };
+                        weigh(u, 0);
+                        weigh(u + 16, 1);
+                        weigh(u + 32, 2);
+                        weigh(u + 48, 3);
+                        tmem_st32(s_addr + 64 * h, w);
+                        l += sum;
+                        tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(p_part(t, c));
-                        tmem_ld_wait();
-                        after_wait(u);
+                        if (lane == 0) mbar_arrive(p_half(t, h));
                     }
+                    if (!ok) break;
                 } else {
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int c = 0; c < 4; ++c) mbar_arrive(p_part(t, c));
+                    if (!wait_all(s_full(t), par)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (quarter == 0) mbar_arrive(empty(2 * j % R));
+                        for (int h = 0; h < 2; ++h) mbar_arrive(p_half(t, h));
+                    }
                 }
                 fresh = false;
                 ++own;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(forgotten(j));
             if (flags & TC_LAST) {
                 // the tile's last product of the segment, if it had a stage in it
-                if (!fresh && !wait_all(pv_done(t), (uint32_t)((own - 1) & 1))) {
+                if (!fresh && !wait_all(pv_half(t, 1), (uint32_t)((own - 1) & 1))) {
                     ok = false;
                     break;
                 }
@@ -863,20 +934,19 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     m = top;
                 }
                 // the segment's values have all been converted; a row that sees one that is not finite is NaN
-                if (*const_cast<const volatile int*>(&spoilt[cur_seg % Tr::NREC]) <= rc.base + token) l = qnan;
+                if (*const_cast<const volatile int*>(&spoilt[cur_seg % Tr::NSEG]) <= last_seen) l = qnan;
                 if (busy) {
                     tc_fence_after();
-                    // 64 bytes of each row at a time (32 finished values, or 16 of a partial state) go
-                    // through shared memory, so that 4 lanes write a row's piece
-                    uint8_t* out = smem + Tr::OUT_OFF + warp * Tr::OUT_BYTES;
                     const bool complete = flags & TC_COMPLETE;
                     const float inv = pois ? qnan : complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                     f0 *= inv;
                     f1 *= inv;
-                    const unsigned rows = __ballot_sync(0xffffffffu, alive);
-                    const int row0 = (SPLIT ? 0 : t * Tr::TILE) + quarter * 32;   // the warp's first row of the group
-                    float* part0 = p.partials + ((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS * Tr::PSTRIDE;
-                    const int q0 = rc.q0, kvh = rc.kvh;
+                    // Each lane writes its row, 32 columns at a time (rows of one token stand side by side in the output, so
+                    // the sectors fill up in L2; exchanging them through shared memory first took 3 us longer
+                    // for a short chunk, cold code included, and nothing less for long ones).
+                    const int row = (SPLIT ? 0 : t * Tr::TILE) + r;
+                    float* prow = p.partials + (((size_t)blockIdx.x * 2 + ((flags & TC_SLOT1) ? 1 : 0)) * Tr::ROWS + row) * Tr::PSTRIDE;
+                    uint16_t* orow = p.out + ((size_t)(seg_q0 + (row >> gs)) * p.Hq + (size_t)seg_kvh * G + (row & (G - 1))) * D;
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t u[32];
@@ -899,41 +969,21 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                             for (int k = 0; k < 32; ++k)
                                 u[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), f1, __uint_as_float(u[k])));
                         }
-                        const int pieces = complete ? 1 : 2;
-                        for (int hf = 0; hf < pieces; ++hf) {
+                        if (alive && complete) {
+                            auto two = [&](int i) -> uint32_t {
+                                return pack2<Tr::BF16>(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+                            };
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint4 v;
-                                if (complete) {
-                                    auto two = [&](int i) -> uint32_t {
-                                        return pack2<Tr::BF16>(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
-                                    };
-                                    v = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
-                                } else {
-                                    v = hf ? make_uint4(u[16 + 4 * k], u[17 + 4 * k], u[18 + 4 * k], u[19 + 4 * k])
-                                           : make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
-                                }
-                                *reinterpret_cast<uint4*>(out + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = v;
-                            }
-                            __syncwarp();
+                            for (int k = 0; k < 32; k += 8)
+                                *reinterpret_cast<uint4*>(orow + 32 * c + k) = make_uint4(two(k), two(k + 2), two(k + 4), two(k + 6));
+                        } else if (alive) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int rr = 8 * i + lane / 4, part = lane & 3;
-                                const uint4 v = *reinterpret_cast<const uint4*>(out + rr * 64 + ((part ^ ((rr >> 1) & 3)) << 4));
-                                if (!((rows >> rr) & 1)) continue;
-                                const int row = row0 + rr;
-                                if (complete) {
-                                    uint16_t* orow = p.out + ((size_t)(q0 + (row >> gs)) * p.Hq + (size_t)kvh * G + (row & (G - 1))) * D;
-                                    *reinterpret_cast<uint4*>(orow + 32 * c + 8 * part) = v;
-                                } else {
-                                    *reinterpret_cast<uint4*>(part0 + (size_t)row * Tr::PSTRIDE + 32 * c + 16 * hf + 4 * part) = v;
-                                }
-                            }
-                            __syncwarp();
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<uint4*>(prow + 32 * c + k) = make_uint4(u[k], u[k + 1], u[k + 2], u[k + 3]);
                         }
+                        __syncwarp();
                     }
                     if (alive && !complete) {
-                        float* prow = part0 + (size_t)(row0 + lane) * Tr::PSTRIDE;
                         prow[D] = m;
                         prow[D + 1] = l;
                     }

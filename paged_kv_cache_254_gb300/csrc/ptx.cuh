@@ -248,6 +248,18 @@ __device__ __forceinline__ float hi_of(uint32_t v) {
     }
 }
 
+// Four 8-bit float codes of one word -> two fp16 pairs, exact.
+template <bool E5M2>
+__device__ __forceinline__ void fp8x4_to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    if constexpr (E5M2) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, a;\n\tcvt.rn.f16x2.e5m2x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(v));
+    } else {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(v));
+    }
+}
+
 // Two 8-bit float codes (low byte = first element) -> two fp16 values, exact.
 template <bool E5M2>
 __device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint16_t v) {
