@@ -36,6 +36,8 @@ struct Rows {
     static constexpr int RPI = 32 / LPR;         // rows a warp loads at once
     static constexpr int NL = BS / RPI;          // loads of a whole block
     static constexpr int TOP = E5M2 ? 15 : 8;    // F = 1.75 * 2^TOP
+    // blocks of threads that an SM holds at least: as many rows in flight as the registers allow
+    static constexpr int OCC = NL <= 4 ? 6 : NL <= 8 ? 4 : 2;
 
     // The exponent of the scale that values up to `top` need.
     static __device__ __forceinline__ int need(float top) {
@@ -103,7 +105,7 @@ struct Rows {
 };
 
 template <int D, int BS, bool BF16, bool E5M2>
-__global__ void __launch_bounds__(32 * WARPS) pa_append_bs8_kernel(const AppendBs8Args a) {
+__global__ void __launch_bounds__(32 * WARPS, Rows<D, BS, BF16, E5M2>::OCC) pa_append_bs8_kernel(const AppendBs8Args a) {
     using R = Rows<D, BS, BF16, E5M2>;
     const int lane = threadIdx.x & 31, sub = lane % R::LPR, rr = lane / R::LPR;
     // warps: (sequence, block of its span, KV head, keys or values), the last fastest, so
@@ -161,17 +163,22 @@ __global__ void __launch_bounds__(32 * WARPS) pa_append_bs8_kernel(const AppendB
     const uint32_t bits = __float_as_uint(now);
     const bool exact = (bits & 0x7fffffu) == 0 && bits < 0x7f000000u;
     const float inv = __uint_as_float(0x7f000000u - bits);
-#pragma unroll
-    for (int i = 0; i < R::NL; ++i) {
+    auto put = [&](int i, uint2 c) {
         const int r = i * R::RPI + rr;
-        if (r < hi - lo)
-            *reinterpret_cast<uint2*>(piece + R::place(op, lo + r, sub)) = exact ? R::codes(x[i], inv) : R::quotients(x[i], now);
+        if (r < hi - lo) *reinterpret_cast<uint2*>(piece + R::place(op, lo + r, sub)) = c;
+    };
+    if (exact) {
+#pragma unroll
+        for (int i = 0; i < R::NL; ++i) put(i, R::codes(x[i], inv));
+    } else {
+#pragma unroll
+        for (int i = 0; i < R::NL; ++i) put(i, R::quotients(x[i], now));
     }
 }
 
 // One warp per (pair, KV head, keys or values), as the append of a whole block.
 template <int D, int BS, bool BF16, bool E5M2>
-__global__ void __launch_bounds__(32 * WARPS) pa_pack_bs8_kernel(const ConvertBs8Args a) {
+__global__ void __launch_bounds__(32 * WARPS, Rows<D, BS, BF16, E5M2>::OCC) pa_pack_bs8_kernel(const ConvertBs8Args a) {
     using R = Rows<D, BS, BF16, E5M2>;
     const int lane = threadIdx.x & 31, sub = lane % R::LPR, rr = lane / R::LPR;
     const long long w = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
