@@ -877,6 +877,114 @@ pa_decode_merge(const long long* __restrict__ cum, const float* __restrict__ par
     *reinterpret_cast<uint2*>(out + ((size_t)s * Hq + (size_t)kvh * G + head) * D + d0) = make_uint2(w[0], w[1]);
 }
 
+// The post-pass of caches with a scale per block: as pa_decode_merge, with a block of threads to a pair
+// (blockIdx.x) and some of its heads (blockIdx.y), and `splits` of its 8 warps (1, 2, 4 or 8) to each row, which
+// take the row's pieces in turn and add up in shared memory in a fixed order.  Bound by latency: of the 64-bit
+// divisions that find the pieces (by one warp, a warp's lanes at once, because all of 16,384 warps
+// doing them took 8 us), then of two rounds of loads.
+template <int D>
+__global__ void __launch_bounds__(256, 6)
+pa_split_merge(const long long* __restrict__ cum, const float* __restrict__ partials, uint16_t* __restrict__ out,
+               int N, int Hkv, int G, long long nworkers, int nd, int splits, int bf16) {
+    constexpr int PSTRIDE = D + 4;
+    constexpr int LPH = D / 4;                     // lanes per head
+    constexpr int HPW = 32 / LPH;                  // heads per warp
+    constexpr int PB = 4;                          // pieces loaded beside their weights
+    __shared__ float4 part[256];
+    griddep_wait();   // the decode grid is complete and its writes visible
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = lane % LPH, sp = warp % splits;
+    const long long pair = blockIdx.x;
+    const int s = (int)(pair / Hkv), kvh = (int)(pair % Hkv);
+    __shared__ long long where[3];                 // the pair's first and last chunk; it starts inside the first
+    if (warp == 0) {
+        const long long c0 = cum[s];
+        const int nb = (int)(cum[s + 1] - c0);
+        const Sched sc = make_sched(cum[N] * Hkv, nworkers, nd);
+        const long long P0 = c0 * Hkv + (long long)kvh * nb;
+        const long long c = nb > 0 ? sc.of(P0 + (lane ? nb - 1 : 0)) : 0;
+        if (lane < 2) where[lane] = c;
+        if (lane == 0) where[2] = nb > 0 && sc.lo(c) < P0;
+    }
+    __syncthreads();
+    const long long cfirst = where[0];
+    const int np = (int)(where[1] - cfirst) + 1;
+    if (np <= 1) return;                           // no blocks, or written by the decode kernel
+    const int head0 = ((int)blockIdx.y * (8 / splits) + warp / splits) * HPW + lane / LPH;
+    const int head = head0 < G ? head0 : G - 1;
+    // piece i is chunk cfirst + i's; only the first can sit in slot 1 (when the pair starts inside that chunk)
+    const size_t cstride = (size_t)2 * G * PSTRIDE;
+    const float* base = partials + (size_t)cfirst * cstride + (size_t)head * PSTRIDE;
+    const size_t off0 = where[2] ? (size_t)G * PSTRIDE : 0;
+    auto piece = [&](int i) -> const float* { return base + (i == 0 ? off0 : (size_t)i * cstride); };
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    auto add = [&](const float4& v, float f) {
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+    };
+    float4 v[PB];
+#pragma unroll
+    for (int k = 0; k < PB; ++k)
+        if (sp + k * splits < np) v[k] = *reinterpret_cast<const float4*>(piece(sp + k * splits) + 4 * sub);
+    float M = -INFINITY, m = -INFINITY, l = 0.f;   // of the pieces; of this lane's last piece
+    for (int i = sub; i < np; i += LPH) {
+        m = piece(i)[D];
+        l = piece(i)[D + 1];
+        M = fmaxf(M, m);
+    }
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i0 = 0; i0 < np; i0 += LPH) {     // LPH is a multiple of splits
+        const int n = min(LPH, np - i0);
+        if (np > LPH) {                        // several rounds: this one's piece again
+            m = -INFINITY;
+            l = 0.f;
+            if (sub < n) {
+                m = piece(i0 + sub)[D];
+                l = piece(i0 + sub)[D + 1];
+            }
+        }
+        const float f = sub < n ? ex2(m - M) : 0.f;
+        L += f * l;
+        int k = 0;                             // piece i0 + sp + k * splits
+        if (i0 == 0) {
+#pragma unroll
+            for (; k < PB; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, (sp + k * splits) % LPH, LPH);
+                if (sp + k * splits < n) add(v[k], fk);
+            }
+        }
+        const int most = (n + splits - 1) / splits;
+#pragma unroll 4
+        for (; k < most; ++k) {
+            const int i = sp + k * splits;
+            const float fk = __shfl_sync(0xffffffffu, f, i % LPH, LPH);
+            if (i < n) add(*reinterpret_cast<const float4*>(piece(i0 + i) + 4 * sub), fk);
+        }
+    }
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (splits > 1) {
+        part[threadIdx.x] = acc;
+        __syncthreads();
+        if (sp != 0) return;
+        for (int k = 1; k < splits; ++k) add(part[threadIdx.x + 32 * k], 1.f);
+    }
+    if (head0 >= G) return;
+    const float inv = 1.f / L;                     // (a pair with blocks has a key that every row sees)
+    uint32_t w[2];
+    if (bf16) {
+        w[0] = pack2<true>(acc.x * inv, acc.y * inv);
+        w[1] = pack2<true>(acc.z * inv, acc.w * inv);
+    } else {
+        w[0] = pack2<false>(acc.x * inv, acc.y * inv);
+        w[1] = pack2<false>(acc.z * inv, acc.w * inv);
+    }
+    *reinterpret_cast<uint2*>(out + ((size_t)(s * (long long)Hkv + kvh) * G + head) * D + 4 * sub) = make_uint2(w[0], w[1]);
+}
+
 // ---------------------------------------------------------------- host side
 struct DecodeLaunch {
     const CUtensorMap* tmap_k;
@@ -885,6 +993,7 @@ struct DecodeLaunch {
     cudaStream_t stream;
     int grid;
     bool bf16;   // output type of the merge post-pass
+    bool split;  // pa_split_merge
 };
 
 struct DecodeKernelInfo {

@@ -179,6 +179,8 @@ pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __res
     }
 }
 
+constexpr long long kMergeWarps = 152 * 48;       // that the GPU holds of pa_split_merge
+
 template <int D>
 cudaError_t merge_launch(const DecodeLaunch& L, int g, long long nworkers, cudaStream_t st) {
     constexpr int HPW = 32 / (D / 4);
@@ -190,6 +192,21 @@ cudaError_t merge_launch(const DecodeLaunch& L, int g, long long nworkers, cudaS
     const cudaLaunchConfig_t cfg = pdl_config(blocks, 256, 0, st, attr);
     return cudaLaunchKernelEx(&cfg, pa_decode_merge<D>, L.p.cum, static_cast<const float*>(L.p.partials), L.p.out,
                               L.p.N, L.p.Hkv, g, nworkers, L.p.nd, L.p.v_scale, L.bf16 ? 1 : 0);
+}
+
+template <int D>
+cudaError_t split_merge_launch(const DecodeLaunch& L, int g, long long nworkers, cudaStream_t st) {
+    constexpr int HPW = 32 / (D / 4);
+    const int hgroups = (g + HPW - 1) / HPW;
+    const long long pairs = (long long)L.p.N * L.p.Hkv;
+    // as many warps to a row as leave the GPU with no more than it holds at once
+    int splits = 8;
+    while (splits > 1 && pairs * hgroups * splits > kMergeWarps) splits /= 2;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(pairs, 256, 0, st, attr);
+    cfg.gridDim.y = (unsigned)((hgroups * splits + 7) / 8);
+    return cudaLaunchKernelEx(&cfg, pa_split_merge<D>, L.p.cum, static_cast<const float*>(L.p.partials), L.p.out,
+                              L.p.N, L.p.Hkv, g, nworkers, L.p.nd, splits, L.bf16 ? 1 : 0);
 }
 
 // Lay out the decode region, run the pre-pass, fill L's scheduling fields,
@@ -217,8 +234,9 @@ pa_status run_decode(const DecodeKernelInfo* k, int ctas, DecodeLaunch& L, const
         return PA_ERR_CUDA;
     if (k->launch(L) != cudaSuccess) return PA_ERR_CUDA;
     const int g = s->num_q_heads / s->num_kv_heads;
-    const cudaError_t e = s->head_dim == 128 ? merge_launch<128>(L, g, workers, L.stream)
-                                             : merge_launch<64>(L, g, workers, L.stream);
+    const auto merge = L.split ? (s->head_dim == 128 ? split_merge_launch<128> : split_merge_launch<64>)
+                               : (s->head_dim == 128 ? merge_launch<128> : merge_launch<64>);
+    const cudaError_t e = merge(L, g, workers, L.stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1351,6 +1369,7 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
     L.p.MB = shape->max_blocks_per_seq;
     L.p.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
     L.p.timeout_ns = kTimeoutNs;
+    L.split = true;
     L.stream = static_cast<cudaStream_t>(stream);
     return run_decode(k, ctas, L, shape, workspace, workspace_bytes, nullptr);
 }
