@@ -179,7 +179,7 @@ class _Declining:
         return NotImplemented
 
     tree_verify = keep_kv = rope_append_kv = append_kv_bs8 = decode_bs8 = decode_tree
-    decode_multi_bs8 = decode_tree
+    decode_multi_bs8 = pack_blocks_bs8 = unpack_blocks_bs8 = decode_tree
 
 
 def load_fast():

@@ -409,9 +409,54 @@ PyObject* decode_multi_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The arguments that the two conversions share; false if anything is not plainly right.
+struct Convert {
+    pa_shape s;
+    int dev;
+    int32_t fmt;
+    const at::Tensor *pairs, *k, *v, *pool, *err;
+    bool read(PyObject* pr, PyObject* kp, PyObject* vp, PyObject* kv, PyObject* format, PyObject* er) {
+        dev = device_of(kv);
+        fmt = small_int(format);
+        pa_shape wide;
+        if (dev < 0 || fmt < 0 || !pool_shape(kp, vp, dev, k, v, wide)) return false;
+        pool = bs8_shape(kv, k->scalar_type(), wide.head_dim, dev, s);
+        pairs = tensor(pr, at::kInt, dev);
+        return pool && s.num_kv_heads == wide.num_kv_heads && s.block_size == wide.block_size && pairs && pairs->dim() == 2 &&
+               pairs->size(1) == 2 && fits_int(pairs->size(0)) && optional(er, at::kInt, dev, err);
+    }
+};
+
+// (src_dst_pairs, k_pool, v_pool, kv_pool, format, err)
+PyObject* pack_blocks_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Convert c;
+        if (n != 6 || !c.read(a[0], a[1], a[2], a[3], a[4], a[5])) return declined();
+        const pa_status st = pa_pack_blocks_bs8(&c.s, c.fmt, (int32_t)c.k->size(0), data<int32_t>(c.pairs), (int32_t)c.pairs->size(0),
+                                                data<void>(c.k), data<void>(c.v), data<void>(c.pool), data<uint32_t>(c.err),
+                                                stream_of(c.dev));
+        if (st != PA_OK) return refused(st, "pa_pack_blocks_bs8");
+        Py_RETURN_NONE;
+    });
+}
+
+// (src_dst_pairs, kv_pool, k_pool, v_pool, format, err)
+PyObject* unpack_blocks_bs8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Convert c;
+        if (n != 6 || !c.read(a[0], a[2], a[3], a[1], a[4], a[5])) return declined();
+        const pa_status st = pa_unpack_blocks_bs8(&c.s, c.fmt, (int32_t)c.k->size(0), data<int32_t>(c.pairs), (int32_t)c.pairs->size(0),
+                                                  data<void>(c.pool), data<void>(c.k), data<void>(c.v), data<uint32_t>(c.err),
+                                                  stream_of(c.dev));
+        if (st != PA_OK) return refused(st, "pa_unpack_blocks_bs8");
+        Py_RETURN_NONE;
+    });
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(keep_kv), METHOD(tree_verify), METHOD(decode_tree), METHOD(rope_append_kv),
                          METHOD(append_kv_bs8), METHOD(decode_bs8), METHOD(decode_multi_bs8),
+                         METHOD(pack_blocks_bs8), METHOD(unpack_blocks_bs8),
                          METHOD(on_failure), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

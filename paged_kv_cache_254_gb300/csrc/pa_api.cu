@@ -1338,12 +1338,12 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
     const DecodeKernelInfo* k = nullptr;
     const pa_status st = pick_decode_bs8(shape, kv_format, &k);
     if (st != PA_OK) return st;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;              // (its operands may be empty, without addresses)
     if (!q || !kv_pool || !block_tables || !context_lens || !out) return PA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv_pool, 32) || !aligned(out, 16) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4))
         return PA_ERR_INVALID_ARG;
-    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
-    if (shape->num_seqs == 0) return PA_OK;
     const uint64_t out_bytes = (uint64_t)shape->num_seqs * shape->num_q_heads * shape->head_dim * 2;
     if (overlap(q, out_bytes, out, out_bytes)) return PA_ERR_INVALID_ARG;
     int dev = 0;
@@ -1390,16 +1390,15 @@ pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t 
     TreePlan plan;
     const pa_status st = plan_chunk(shape, kv_format, max_q_len, &plan);
     if (st != PA_OK) return st;
-    if (total_q < 0) return PA_ERR_INVALID_ARG;
+    if (total_q < 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return PA_OK;
     if (!q_start || !kv_pool || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
     if (total_q > 0 && (!q || !out)) return PA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv_pool, 32) || !aligned(out, 16) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4) || !aligned(q_start, 4))
         return PA_ERR_INVALID_ARG;
-    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
     const uint64_t bytes = (uint64_t)total_q * shape->num_q_heads * shape->head_dim * 2;
     if (total_q > 0 && overlap(q, bytes, out, bytes)) return PA_ERR_INVALID_ARG;
-    if (shape->num_seqs == 0) return PA_OK;
     // no chunk is longer than the call's rows, or than a table holds
     const int most = (int)std::min({(long long)max_q_len, std::max(1ll, (long long)total_q),
                                     (long long)shape->max_blocks_per_seq * shape->block_size});
@@ -1468,11 +1467,12 @@ static pa_status convert_bs8(bool pack, const pa_shape* shape, int32_t kv_format
     if (st != PA_OK) return st;
     if (num_pairs < 0 || num_blocks16 <= 0) return PA_ERR_INVALID_ARG;
     if (num_pairs == 0) return PA_OK;
-    if (!pairs || !k_pool || !v_pool || !kv_pool || k_pool == v_pool) return PA_ERR_INVALID_ARG;
+    if (!pairs || !k_pool || !v_pool || !kv_pool) return PA_ERR_INVALID_ARG;
     if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(kv_pool, 32) || !aligned(pairs, 4))
         return PA_ERR_INVALID_ARG;
     const uint64_t bytes16 = (uint64_t)num_blocks16 * shape->num_kv_heads * shape->block_size * shape->head_dim * 2;
-    if (overlap(k_pool, bytes16, kv_pool, bs8_pool_bytes(shape)) || overlap(v_pool, bytes16, kv_pool, bs8_pool_bytes(shape)))
+    if (overlap(k_pool, bytes16, kv_pool, bs8_pool_bytes(shape)) || overlap(v_pool, bytes16, kv_pool, bs8_pool_bytes(shape)) ||
+        overlap(k_pool, bytes16, v_pool, bytes16))
         return PA_ERR_INVALID_ARG;
     if (!bs8_grid_fits(shape, num_pairs)) return PA_ERR_UNSUPPORTED;
     ConvertBs8Args a{};

@@ -936,9 +936,9 @@ def pa_decode_multi_bs8(q, kv_pool, block_tables, context_lens, q_start, scale, 
 
 def _decode_multi_bs8(q, kv_pool, block_tables, context_lens, q_start, scale, fmt, max_q_len, out, workspace, err):
     """pa_decode_multi_bs8 by way of every check."""
+    _arg("q_start", q_start, torch.int32, _index("q", q))
     if max_q_len < 1:
         raise ValueError("max_q_len must be at least 1")
-    _arg("q_start", q_start, torch.int32, _index("q", q))
 
     def run(lib, dev, shape, out, ws, handle):
         if q_start.shape != (shape.num_seqs + 1,):
@@ -971,9 +971,9 @@ def pa_copy_blocks_bs8(src_dst_pairs, kv_pool, err=None, stream=None):
         _lib.check(st, "pa_copy_blocks_bs8")
 
 
-def _convert_bs8(call, src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err):
+def _convert_bs8(call, src_dst_pairs, k_pool, v_pool, kv_pool, fmt, err):
+    """pa_pack_blocks_bs8 and pa_unpack_blocks_bs8 by way of every check."""
     dev = _index("kv_pool", kv_pool)
-    fmt = _bs8_format(kv_format)
     if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
         raise ValueError("k_pool must be a tensor [NB, Hkv, B, d]")
     _arg("k_pool", k_pool, k_pool.dtype, dev)
@@ -1000,7 +1000,9 @@ def pa_pack_blocks_bs8(src_dst_pairs, k_pool, v_pool, kv_pool, kv_format="e4m3",
     (int32)."""
     if stream is not None:
         return _on_stream(stream, pa_pack_blocks_bs8, src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
-    _convert_bs8("pa_pack_blocks_bs8", src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
+    args = (src_dst_pairs, k_pool, v_pool, kv_pool, _bs8_format(kv_format), err)
+    if (_fast or _load_fast()).pack_blocks_bs8(*args) is NotImplemented:
+        _convert_bs8("pa_pack_blocks_bs8", *args)
 
 
 def pa_unpack_blocks_bs8(src_dst_pairs, kv_pool, k_pool, v_pool, kv_format="e4m3", err=None, stream=None):
@@ -1008,4 +1010,6 @@ def pa_unpack_blocks_bs8(src_dst_pairs, kv_pool, k_pool, v_pool, kv_format="e4m3
     for each row of src_dst_pairs [n, 2] (int32)."""
     if stream is not None:
         return _on_stream(stream, pa_unpack_blocks_bs8, src_dst_pairs, kv_pool, k_pool, v_pool, kv_format, err)
-    _convert_bs8("pa_unpack_blocks_bs8", src_dst_pairs, k_pool, v_pool, kv_pool, kv_format, err)
+    args = (src_dst_pairs, kv_pool, k_pool, v_pool, _bs8_format(kv_format), err)
+    if (_fast or _load_fast()).unpack_blocks_bs8(*args) is NotImplemented:
+        _convert_bs8("pa_unpack_blocks_bs8", src_dst_pairs, k_pool, v_pool, kv_pool, *args[-2:])
