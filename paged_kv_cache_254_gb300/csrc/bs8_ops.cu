@@ -152,10 +152,16 @@ __global__ void __launch_bounds__(32 * WARPS, Rows<D, BS, BF16, E5M2>::OCC) pa_a
     const float now = rises ? need : old;
     if (rises) {
         const float ratio = __fdiv_rn(old, need);
-        for (int r = rr; r < lo; r += R::RPI) {          // older rows
-            uint2* at = reinterpret_cast<uint2*>(piece + R::place(op, r, sub));
-            const uint2 c = *at;
-            *at = make_uint2(R::scaled(c.x, ratio), R::scaled(c.y, ratio));
+        for (int r0 = rr; r0 < lo; r0 += 4 * R::RPI) {   // older rows, four loads in flight
+            uint2 c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * R::RPI < lo) c[k] = *reinterpret_cast<const uint2*>(piece + R::place(op, r0 + k * R::RPI, sub));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * R::RPI < lo)
+                    *reinterpret_cast<uint2*>(piece + R::place(op, r0 + k * R::RPI, sub)) =
+                        make_uint2(R::scaled(c[k].x, ratio), R::scaled(c[k].y, ratio));
         }
         if (lane == 0) *scale_at = now;
     }
