@@ -31,22 +31,22 @@
 //                    stage the keys, then the values: codes from shared memory, fp16 back.
 //                    Value rows past the context become zeros, and so do rows of the chunk that hold
 //                    NaN or infinities (rows that see them become NaN at the softmax)
-//   2 warps          products of tile 0, 1 (one thread each)
+//   2 warps          products of tile 0, 1
 //   1 warp           the plan: each stage's place, blocks and scales, as a record for the others
 //   1 warp           copies: a bulk copy per block for its keys, one for its values
 //
 // Bound by the chain of a stage within a tile, not by a unit: at 256 rows and head_dim 128 a stage
-// takes 6,000 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
-// scores (700), their way to the softmax (300), two halves (1,200 to 1,600 each, the loads
+// takes 5,700 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
+// scores (700), their way to the softmax (200), two halves (1,000 to 1,800 each, the loads
 // 300 of it), the last products and their way back (700) follow one another, and the tiles'
 // warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
-// Measured on GB300: 1,050 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
-// 128 (785 TFLOP/s of 1,905); 640 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
-// to 8192 (1.9 TB/s).  Also measured: 64-key products ahead of the softmax (1,470 us), scores of one
-// stage in one piece (1,175), two softmax warps to a row (1,250), codes loaded into
-// registers from L2 (1,160), the conversion unrolled over both kinds (1,190: the roles' loops then
-// fall out of the SM's instruction cache), polling loops in place of held waits (no
-// difference).
+// Measured on GB300: 972 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (850 TFLOP/s of 1,905); 567 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// to 8192 (2.2 TB/s).  Also measured, against 1,060 us and 636: 64-key products ahead of the
+// softmax (1,470 us for the long prompt), scores of one stage in one piece (1,175), two softmax
+// warps to a row (1,250), codes loaded into registers from L2 (1,160), the conversion unrolled over
+// both kinds (1,190: the roles' loops then fall out of the SM's instruction cache), polling loops
+// in place of held waits (no difference).
 //
 // The work list and the partial states of split rows are those of the tree kernels: each CTA
 // takes an equal run of (row group, KV head, block) units; a group's keys end at its
@@ -132,7 +132,8 @@ struct ChunkTraits {
     static constexpr int START_OFF = SPOILT_OFF + NSEG * 4;  // a TreeStart, a word per warp
     static constexpr int Q_OFF = (START_OFF + 32 + 8 * THREADS / 32 + 1023) / 1024 * 1024;
     static constexpr int RING_OFF = Q_OFF + Q_BYTES;
-    static constexpr int R = 3;                              // fp16 slots; K and V alternate
+    // fp16 slots; K and V alternate.  (SPLIT: with three, a tile's next keys wait for its values' slot, 586 us to 567.)
+    static constexpr int R = SPLIT ? 4 : 3;
     // slots of codes on their way, a ring for keys and one for values
     static constexpr int RING8_OFF = RING_OFF + R * SLOT_BYTES;
     static constexpr int N8_FIT = (SMEM_BYTES - 1024 - RING8_OFF) / SLOT8_BYTES;
@@ -190,6 +191,13 @@ __device__ __forceinline__ float max16(const uint32_t* u) {
     const float a = max3(max3(f(0), f(1), f(2)), f(3), f(4)), b = max3(max3(f(5), f(6), f(7)), f(8), f(9));
     const float c = max3(max3(f(10), f(11), f(12)), f(13), f(14));
     return fmaxf(max3(a, b, c), f(15));
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <class Tr>
@@ -497,16 +505,23 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                             wait_bounded(full8(slot8(op, k)), (uint32_t)(uses8(op, k) & 1), p.timeout_ns);
                 }
             }
-        } else if (lane == 0) {
+        } else {
             // ============================================================ products of one tile
-            const int t = warp - Tr::MMA_WARP;
+            // The whole warp runs the loop and one lane of it issues, so that descriptors and addresses are
+            // uniform to the compiler: a loop of one thread issued a product in 150 cycles, not 64 (636 to 596
+            // us and 1,061 to 996).  Commits give the slots back, and the next stage's record and keys are
+            // waited for before the last products are through (to 585 and 972).
+            const int t = __shfl_sync(0xffffffffu, warp, 0) - Tr::MMA_WARP;
             const uint32_t s_col = tmem + 128 * t, o_col = tmem + Tr::O_COL + 128 * t;
             const uint32_t q_tile = q_base + (SPLIT ? 0 : t * HALVES * Tr::Q_HALF);
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-                if (__builtin_expect(try_wait_held(bar, parity), 1)) return true;
-                if (*abort_flag || !wait_bounded(bar, parity, p.timeout_ns)) ok = false;
+                if (__builtin_expect(__all_sync(0xffffffffu, try_wait_held(bar, parity)), 1)) return true;
+                if (!__all_sync(0xffffffffu, *abort_flag == 0 && wait_bounded(bar, parity, p.timeout_ns))) ok = false;
                 return ok;
+            };
+            auto arrive = [&](uint32_t bar) {
+                if (lane == 0) mbar_arrive(bar);
             };
             int own = 0, nseg = 0;                 // stages of this tile; segments begun
             bool fresh = true;                     // O holds nothing of the segment
@@ -522,26 +537,33 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     fresh = true;
                     active = SPLIT || rc.n > t * tile_nodes;
                 }
-                mbar_arrive(forgotten(j));
+                arrive(forgotten(j));
                 if (SPLIT && (j & 1) != t) {                      // the other tile's stage
-                    if (flags & TC_LAST) mma_commit(q_empty);
+                    if ((flags & TC_LAST) && elect_one()) mma_commit(q_empty);
                     continue;
                 }
                 const int ks = 2 * j % R, vs = (2 * j + 1) % R;
                 const uint32_t par = (uint32_t)(own & 1);
                 if (!wait(ready(ks), (uint32_t)((2 * j / R) & 1))) break;
+                // the scores overwrite the last stage's weights
+                if (own > 0 && !wait(pv_half(t, 1), par ^ 1u)) break;
                 if (active) {
                     tc_fence_after();
                     const uint64_t qd = sdesc_sw128(q_tile, 16, 1024), kd = sdesc_sw128(ring + ks * Tr::SLOT_BYTES, 16, 1024);
-#pragma unroll (SPLIT ? 1 : D / 16)               // (256 rows: 70 us slower rolled; SPLIT: 50 us faster)
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_f16(s_col, qd + (uint64_t)((k / 4) * (Tr::Q_HALF >> 4) + (k % 4) * 2),
-                                kd + (uint64_t)((k / 4) * (Tr::HALF_STRIDE >> 4) + (k % 4) * 2), IDESC_S, k > 0 ? 1u : 0u);
-                    mma_commit(s_full(t));
-                    if (flags & TC_LAST) mma_commit(q_empty);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_f16(s_col, qd + (uint64_t)((k / 4) * (Tr::Q_HALF >> 4) + (k % 4) * 2),
+                                    kd + (uint64_t)((k / 4) * (Tr::HALF_STRIDE >> 4) + (k % 4) * 2), IDESC_S, k > 0 ? 1u : 0u);
+                        mma_commit(s_full(t));
+                        mma_commit(empty(ks));
+                        if (flags & TC_LAST) mma_commit(q_empty);
+                    }
+                    __syncwarp();
                 } else {
-                    mbar_arrive(s_full(t));
-                    if (flags & TC_LAST) mbar_arrive(q_empty);
+                    arrive(s_full(t));
+                    arrive(empty(ks));
+                    if (flags & TC_LAST) arrive(q_empty);
                 }
                 if (!wait(ready(vs), (uint32_t)(((2 * j + 1) / R) & 1))) break;
                 bool stop = false;
@@ -554,27 +576,31 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     if (active) {
                         tc_fence_after();
                         const uint64_t vd = sdesc_sw128(ring + vs * Tr::SLOT_BYTES + h * 8192, Tr::HALF_STRIDE, 1024);
-#pragma unroll (SPLIT ? 1 : 4)
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_ts(o_col, s_col + 64 * h + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), IDESC_O,
-                                       fresh && h + k == 0 ? 0u : 1u);
-                        mma_commit(pv_half(t, h));
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ts(o_col, s_col + 64 * h + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), IDESC_O,
+                                           fresh && h + k == 0 ? 0u : 1u);
+                            mma_commit(pv_half(t, h));
+                            if (h == 1) mma_commit(empty(vs));
+                        }
+                        __syncwarp();
                     } else {
-                        mbar_arrive(pv_half(t, h));
+                        arrive(pv_half(t, h));
+                        if (h == 1) arrive(empty(vs));
                     }
                 }
-                // the next scores overwrite the weights
-                if (stop || !wait(pv_half(t, 1), par)) break;
-                mbar_arrive(empty(vs));                           // the stage's values are used up
+                if (stop) break;
                 fresh = false;
                 ++own;
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 set_err(p.err, PA_DEVERR_TIMEOUT);
                 *abort_flag = 1;
             }
             // every MMA of this thread completes before tensor memory is released
-            mma_commit(fin + 8 * t);
+            if (elect_one()) mma_commit(fin + 8 * t);
+            __syncwarp();
             wait_bounded(fin + 8 * t, 0, p.timeout_ns);
         }
         __syncwarp();
@@ -690,7 +716,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 const uint32_t src = ring8 + st * Tr::SLOT8_BYTES, slot = ring + (item % R) * Tr::SLOT_BYTES;
                 const uint32_t in0 = place(op, row0), in1 = place(op, row0 + STEP);
                 const bool care = op && (held < KEYS || from < KEYS || cuts);
-#pragma unroll (SPLIT ? 1 : 2)                            // (SPLIT: unrolled it spills, 673 us to 635)
+#pragma unroll (SPLIT ? 1 : 2)                            // (SPLIT: by two 611 us, by four 677, by one 567)
                 for (int i = 0; i < NI; ++i) {
                     uint32_t c[4], h[8];
                     const int row = row0 + i * STEP;
@@ -780,7 +806,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                         ok = false;
                         break;
                     }
-                    if (quarter == 0 && lane == 0) mbar_arrive(empty(2 * j % R));   // the stage's keys are used up
+                    
                     tc_fence_after();
                     if (fresh) rf = rowf[((cur_seg - 1) & 1) * 2 * Tr::TILE + row_of_group];
                     if (SPLIT && t == 1 && fresh && cur_seg > 1) {    // tile 0 has read the last segment's O
@@ -889,7 +915,6 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                         break;
                     }
                     if (lane == 0) {
-                        if (quarter == 0) mbar_arrive(empty(2 * j % R));
                         for (int h = 0; h < 2; ++h) mbar_arrive(p_half(t, h));
                     }
                 }
