@@ -368,7 +368,8 @@ pa_status pa_copy_blocks_fp8(const pa_shape* shape, const int32_t* src_dst_pairs
  *                     need no copy; not inside the pool
  *   q_start           int32 [N + 1], non-decreasing
  * Uses shape->num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
- * max_blocks_per_seq, dtype.  One launch.
+ * max_blocks_per_seq, dtype.  One launch over N * Hkv * (blocks that max_new tokens, or the
+ * table, can lie in) pieces; 2^31 or more of them: PA_ERR_UNSUPPORTED.
  */
 pa_status pa_append_kv_bs8(const pa_shape* shape, int32_t kv_format, int32_t max_new, int32_t total_new,
                            const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,

@@ -110,11 +110,9 @@ __global__ void __launch_bounds__(32 * WARPS, Rows<D, BS, BF16, E5M2>::OCC) pa_a
     const int lane = threadIdx.x & 31, sub = lane % R::LPR, rr = lane / R::LPR;
     // warps: (sequence, block of its span, KV head, keys or values), the last fastest, so
     // that neighbours read one token's heads
-    const long long w = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    const int per = 2 * a.Hkv;
-    const long long unit = w / per;
-    if (unit >= (long long)a.N * a.span) return;
+    const uint32_t w = blockIdx.x * WARPS + (threadIdx.x >> 5), per = 2 * a.Hkv, unit = w / per;
     const int s = (int)(unit / a.span), j = (int)(unit % a.span), h = (int)(w % per) >> 1, op = (int)(w & 1);
+    if (s >= a.N) return;
     const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1), ctx = __ldg(a.context_lens + s);
     const long long n = (long long)q1 - q0;
     if (q0 < 0 || q1 > a.T || n < 0 || n > a.max_new || ctx < 0 || n > ctx || ctx > a.MB * BS) {
@@ -187,12 +185,10 @@ template <int D, int BS, bool BF16, bool E5M2>
 __global__ void __launch_bounds__(32 * WARPS, Rows<D, BS, BF16, E5M2>::OCC) pa_pack_bs8_kernel(const ConvertBs8Args a) {
     using R = Rows<D, BS, BF16, E5M2>;
     const int lane = threadIdx.x & 31, sub = lane % R::LPR, rr = lane / R::LPR;
-    const long long w = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    const int per = 2 * a.Hkv;
-    const long long i0 = w / per;
-    if (i0 >= a.n) return;
+    const uint32_t w = blockIdx.x * WARPS + (threadIdx.x >> 5), per = 2 * a.Hkv, i0 = w / per;
+    if (i0 >= (uint32_t)a.n) return;
     const int op = (int)(w % per) / a.Hkv, h = (int)(w % per) % a.Hkv;
-    const int from = __ldg(a.pairs + 2 * i0), to = __ldg(a.pairs + 2 * i0 + 1);
+    const int from = __ldg(a.pairs + 2 * (size_t)i0), to = __ldg(a.pairs + 2 * (size_t)i0 + 1);
     if ((unsigned)from >= (unsigned)a.NB16 || (unsigned)to >= (unsigned)a.NB8) {
         if (lane == 0) set_err(a.err, PA_DEVERR_COPY_PAIR);
         return;
@@ -214,12 +210,10 @@ template <int D, int BS, bool BF16, bool E5M2>
 __global__ void __launch_bounds__(32 * WARPS) pa_unpack_bs8_kernel(const ConvertBs8Args a) {
     using R = Rows<D, BS, BF16, E5M2>;
     const int lane = threadIdx.x & 31, sub = lane % R::LPR, rr = lane / R::LPR;
-    const long long w = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    const int per = 2 * a.Hkv;
-    const long long i0 = w / per;
-    if (i0 >= a.n) return;
+    const uint32_t w = blockIdx.x * WARPS + (threadIdx.x >> 5), per = 2 * a.Hkv, i0 = w / per;
+    if (i0 >= (uint32_t)a.n) return;
     const int op = (int)(w % per) / a.Hkv, h = (int)(w % per) % a.Hkv;
-    const int from = __ldg(a.pairs + 2 * i0), to = __ldg(a.pairs + 2 * i0 + 1);
+    const int from = __ldg(a.pairs + 2 * (size_t)i0), to = __ldg(a.pairs + 2 * (size_t)i0 + 1);
     if ((unsigned)from >= (unsigned)a.NB8 || (unsigned)to >= (unsigned)a.NB16) {
         if (lane == 0) set_err(a.err, PA_DEVERR_COPY_PAIR);
         return;

@@ -23,8 +23,7 @@ struct ConvertBs8Args {
     uint16_t *k, *v;                // the 16-bit pools
     uint8_t* pool;
     uint32_t* err;
-    int64_t n;
-    int32_t Hkv, NB8, NB16;         // blocks of the 8-bit pool, of the 16-bit pools
+    int32_t n, Hkv, NB8, NB16;         // blocks of the 8-bit pool, of the 16-bit pools
 };
 
 // Kernels by type: the values' 16-bit type, the codes' format, block size and head_dim.

@@ -411,10 +411,9 @@ uint64_t bs8_pool_bytes(const pa_shape* s) {
     return (uint64_t)s->num_blocks * s->num_kv_heads * bs8_piece_bytes(s->block_size, s->head_dim);
 }
 
-// Warps of a launch over (pair or block, KV head, keys or values): a grid of eight-warp
-// blocks has to hold them.
+// Warps of a launch over (pair or block, KV head, keys or values): the kernels count them in 32 bits.
 bool bs8_grid_fits(const pa_shape* s, long long units) {
-    return units <= ((1ll << 31) - 1) * 8 / (2ll * s->num_kv_heads);
+    return units <= ((1ll << 32) - 8) / (2ll * s->num_kv_heads);
 }
 
 const PrefixKernelInfo& pick_prefix(const pa_shape* s) {
