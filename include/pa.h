@@ -341,7 +341,8 @@ pa_status pa_copy_blocks_fp8(const pa_shape* shape, const int32_t* src_dst_pairs
  * mod 2) of row r XOR (r / 16 mod 2).  A pool of zeros is a valid empty one.
  *
  * kv_format: PA_FP8_E4M3 or PA_FP8_E5M2, F its largest value (448, 57344).  Codes are
- * rounded to nearest even; an infinity becomes the largest code, NaN stays NaN.
+ * rounded to nearest even; an infinity becomes the largest code, NaN stays NaN.  (E5M2's codes
+ * of infinities, which no call here writes, are not supported in a pool.)
  * Supported by every call: shape->dtype fp16 or bf16 (queries, outputs, new values, the
  * 16-bit pools), d in {64, 128}, B in {16, 32}.
  */
@@ -357,7 +358,7 @@ pa_status pa_copy_blocks_fp8(const pa_shape* shape, const int32_t* src_dst_pairs
  *     new codes are code(x / s')
  * A block's first slot starts it afresh, whatever it holds (a block off the free list).
  * Blocks that new tokens fall into belong to one sequence each (copy-on-write has run
- * before).  A malformed sequence (n_b < 0, n_b > max_new, n_b > its context, rows
+ * before) and stand in its table once.  A malformed sequence (n_b < 0, n_b > max_new, n_b > its context, rows
  * outside [0, total_new), a context past its table) sets PA_DEVERR_CONTEXT and appends
  * nothing; a bad block id (PA_DEVERR_BLOCK_ID) or scale (PA_DEVERR_SCALE) leaves that
  * piece as it was.

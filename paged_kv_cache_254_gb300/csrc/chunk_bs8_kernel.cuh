@@ -520,7 +520,8 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 if (!__all_sync(0xffffffffu, *abort_flag == 0 && wait_bounded(bar, parity, p.timeout_ns))) ok = false;
                 return ok;
             };
-            auto arrive = [&](uint32_t bar) {
+            auto arrive = [&](uint32_t bar) {                     // for what all lanes have done
+                __syncwarp();
                 if (lane == 0) mbar_arrive(bar);
             };
             int own = 0, nseg = 0;                 // stages of this tile; segments begun
@@ -616,6 +617,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         constexpr int NI = KEYS / STEP;                           // rounds of a slot
         const int part = D == 128 ? (lane & 3) | (((lane >> 2) ^ (lane >> 3)) & 1) << 2 : lane & 3;
         const int row0 = cw * RPW + (D == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2);
+        const float qnan = __int_as_float(0x7fc00000);
         int nseg = 0;
         bool ok = true;
         auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -671,20 +673,21 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     uint4 x[NQ];
 #pragma unroll
                     for (int i = 0; i < NQ; ++i) x[i] = row < rows ? __ldg(src + (lane & 3) + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
-                    float2 f = make_float2(1.f, 1.f);
-                    if constexpr (Tr::BF16) {
-                        uint32_t top = 0;
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int i = 0; i < NQ; ++i)
-                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        top = max(top & 0xffffu, top >> 16);
-                        f = row_factor((int)(top >> 7));
-                    }
+                    for (int i = 0; i < NQ; ++i)
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+                    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = max(top & 0xffffu, top >> 16);
+                    float2 f = make_float2(1.f, 1.f);
+                    if constexpr (Tr::BF16) f = row_factor((int)(top >> 7));
                     if (p.scale_log2 < 0.f) f.x = -f.x;
-                    if ((lane & 3) == 0) rowf[(nseg & 1) * 2 * Tr::TILE + row] = f.y * scale_abs;
+                    // an infinite query has infinite scores or NaN: no weights (all at -inf would look like a row that
+                    // sees nothing)
+                    const bool finite = top < (Tr::BF16 ? 0x7f80u : 0x7c00u);
+                    if ((lane & 3) == 0) rowf[(nseg & 1) * 2 * Tr::TILE + row] = finite ? f.y * scale_abs : qnan;
                     const int r = row % Tr::TILE;
                     const uint32_t a = q_base + row / Tr::TILE * (HALVES * Tr::Q_HALF) + r * 128;
 #pragma unroll

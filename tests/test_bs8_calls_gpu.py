@@ -188,6 +188,41 @@ def test_largest_chunks_are_found_on_the_host():
     assert torch.equal(c.chunk(), pa().pa_decode_multi_bs8(c.q, c.pool, c.table, c.lens, c.q_start, c.scale))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [4, 40])
+def test_infinite_queries_are_nan_whatever_their_scores(dtype, n):
+    # every key is negative in dimension 5: an infinity there gives no score but -inf
+    c = Call(30, [100, 300], [n, n], dtype=dtype)
+    c.k[..., 5] = -c.k[..., 5].abs() - 1
+    pa().bs8_scales(c.pool)[...] = 1.0
+    c.pool[..., 32:] = 0xB8                                    # -1 in every place
+    c.append()
+    c.one[0, 1, 5], c.one[1, 3, 5] = float("inf"), float("nan")
+    c.q[2, 1, 5], c.q[n, 7, 5], c.q[n + 1, 2, 5] = float("inf"), float("-inf"), float("nan")
+    one, q = c.decode(), c.chunk()
+    torch.cuda.synchronize()
+    assert one.isnan().all(-1).nonzero().tolist() == [[0, 1], [1, 3]] == one.isnan().any(-1).nonzero().tolist()
+    want = [[2, 1], [n, 7], [n + 1, 2]]
+    assert q.isnan().all(-1).nonzero().tolist() == want == q.isnan().any(-1).nonzero().tolist()
+
+
+def test_the_timeout_path():
+    # every worker's first stage waits, for 100 us at most, on a barrier that nothing completes
+    c = Call(31, [700, 2000, 33], [1, 1, 1], Hq=16)
+    c.append()
+    want = c.decode()
+    pa().pa_set_decode_stall_ns(100_000)
+    try:
+        err = pa().new_error_word("cuda")
+        out = c.decode(err=err)
+        assert pa().pa_read_error(err) == 5                    # PA_ERR_TIMEOUT
+        assert out.isnan().all()                               # cut rows too, through the merge
+    finally:
+        pa().pa_set_decode_stall_ns(0)
+    err = pa().new_error_word("cuda")
+    assert torch.equal(c.decode(err=err), want) and pa().pa_read_error(err) == 0
+
+
 # ---------------------------------------------------------------- streams, threads, graphs
 def test_calls_on_another_stream():
     c = Call(10, CTX, NEW)
