@@ -179,7 +179,11 @@ pa_decode_prepass(const int32_t* __restrict__ context_lens, const int32_t* __res
     }
 }
 
-constexpr long long kMergeWarps = 152 * 48;       // that the GPU holds of pa_split_merge
+// Warps of pa_split_merge that a launch may have by splitting rows.  Decode calls with 1, 2, 4, 8 warps to a row: 512
+// rows 42.3, 35.7, 32.6, 31.4 us; 2,048 rows 64.6, 63.3, 65.0, 68.2; 4,096 rows 145, 133, 130, 136 (contexts to
+// 8192) and 30.0, 31.4, 35.1, 42.5 (to 1000); 16,384 rows 390, 395, 407, 433: blocks that have nothing to do
+// cost as well.
+constexpr long long kMergeWarps = 8192;
 
 template <int D>
 cudaError_t merge_launch(const DecodeLaunch& L, int g, long long nworkers, cudaStream_t st) {
@@ -199,7 +203,6 @@ cudaError_t split_merge_launch(const DecodeLaunch& L, int g, long long nworkers,
     constexpr int HPW = 32 / (D / 4);
     const int hgroups = (g + HPW - 1) / HPW;
     const long long pairs = (long long)L.p.N * L.p.Hkv;
-    // as many warps to a row as leave the GPU with no more than it holds at once
     int splits = 8;
     while (splits > 1 && pairs * hgroups * splits > kMergeWarps) splits /= 2;
     cudaLaunchAttribute attr[1];
