@@ -20,9 +20,13 @@
 //    segment's end, where the threads of tile 0 read both outputs from tensor memory.
 //
 // Tensor memory (512 columns): S_0, S_1 at 0 and 128, O_0, O_1 at 256 and 384; P_t overwrites
-// S_t, 32 columns at the start of each 64 that held its scores.  A row's reference moves
-// only when its maximum rises by more than 8 (O is rescaled then), so weights are at most
-// 2^8.
+// S_t, 32 columns at the start of each 64 that held its scores.  Weights are
+// 2^(x - m) for a reference m that moves (to the maximum, with O rescaled) only when half a stage's
+// add up to more than 2^12: fp16 holds any of them, its relative precision is the same at every
+// size, and no stage has to know its maximum before its weights (978 us to 922).  A weight that is the
+// row's maximum has no rounding error, so a lower border is a little more precise: fp16
+// outputs are off by 2.15e-4 of their size for 2^6 (983 us), 2.31e-4 for 2^9 (939), 2.48e-4 for 2^12,
+// 2.62e-4 for 2^15 (920), of which 2.07e-4 are the outputs' own rounding.
 //
 // Roles (one CTA per SM; 640 threads for SPLIT, else 512):
 //   warps 0-3, 4-7   softmax of tile 0, 1: thread = row = TMEM lane, half of a stage at a time, so that the
@@ -36,12 +40,12 @@
 //   1 warp           copies: a bulk copy per block for its keys, one for its values
 //
 // Bound by the chain of a stage within a tile, not by a unit: at 256 rows and head_dim 128 a stage
-// takes 5,700 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
+// takes 5,400 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
 // scores (700), their way to the softmax (200), two halves (1,000 to 1,800 each, the loads
 // 300 of it), the last products and their way back (700) follow one another, and the tiles'
 // warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
-// Measured on GB300: 972 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
-// 128 (850 TFLOP/s of 1,905); 567 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// Measured on GB300: 920 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (900 TFLOP/s of 1,905); 562 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
 // to 8192 (2.2 TB/s).  Also measured, against 1,060 us and 636: 64-key products ahead of the
 // softmax (1,470 us for the long prompt), scores of one stage in one piece (1,175), two softmax
 // warps to a row (1,250), codes loaded into registers from L2 (1,160), the conversion unrolled over
@@ -143,7 +147,7 @@ struct ChunkTraits {
     static constexpr int TMEM_COLS = 512;
     static constexpr int O_COL = 256;
     static constexpr int PSTRIDE = D + 4;
-    static constexpr float TAU = 8.f;                        // lazy-rescale threshold (log2 units)
+    static constexpr float MOST = 4096.f;                 // that the weights of half a stage may add up to
     static_assert(N8 >= 2 && RING_OFF % 1024 == 0, "shared memory");
 };
 
@@ -839,71 +843,83 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                         tmem_st_wait();
                     }
                     // Half of the scores at a time becomes weights in the first 32 of the 64 columns that held
-                    // them.  The row's reference is looked at once a half, so scores are read once; when it
-                    // moves, O is rescaled behind the products of the half before.
+                    // them, by the row's reference as it stands; only where there is none yet, or the weights
+                    // add up to more than fp16 holds with room to spare, are the scores' maxima looked for and
+                    // the half done again (the scores are still there).  O is rescaled behind the products of the
+                    // half before.
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t u[64];
-                        tmem_ld64_wait(s_addr + 64 * h, u);
+                        bool redo = __any_sync(0xffffffffu, alive && m == -INFINITY);
                         float by[4], add[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             by[b] = masked ? 1.f : rc.ks[(64 * h + 16 * b) / BS] * rf;
                             add[b] = masked ? 0.f : rc.lb[(64 * h + 16 * b) / BS];
                         }
-                        const float mx = fmaxf(fmaxf(fmaf(max16(u), by[0], add[0]), fmaf(max16(u + 16), by[1], add[1])),
-                                               fmaxf(fmaf(max16(u + 32), by[2], add[2]), fmaf(max16(u + 48), by[3], add[3])));
-                        const bool need = mx > m + Tr::TAU && alive;
-                        if (__any_sync(0xffffffffu, need)) {
-                            const float alpha = need ? ex2(m - mx) : 1.f;     // m = -inf: 0
-                            if (need) {
-                                m = mx;
-                                l *= alpha;
-                            }
-                            if (!fresh || h > 0) {
-                                if (!wait_all(pv_half(t, h ^ 1), h == 0 ? par ^ 1u : par)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int i = 0; i < D / 16; ++i) {
-                                    uint32_t x[16];
-                                    tmem_ld16(o_addr + 16 * i, x);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        asm volatile("" : "+r"(x[k]));
-                                        x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
-                                    }
-                                    tmem_st16(o_addr + 16 * i, x);
-                                }
-                                tmem_st_wait();
-                            }
-                        }
-                        const float mref = m == -INFINITY ? 0.f : m;          // no visible key yet: weights 0
                         uint32_t w[32];
-                        float sum = 0.f;
-                        auto weigh = [&](const uint32_t* x, int b) {          // 16 scores -> 8 columns of weights
-                            const f32x2 by2 = pair2(by[b], by[b]), add2x = pair2(add[b] - mref, add[b] - mref);
-                            f32x2 s2[2] = {0ull, 0ull};
+                        float sum, plain;
+#pragma unroll 1
+                        for (;;) {
+                            uint32_t u[64];
+                            tmem_ld64_wait(s_addr + 64 * h, u);
+                            if (redo) {
+                                const float mx = fmaxf(fmaxf(fmaf(max16(u), by[0], add[0]), fmaf(max16(u + 16), by[1], add[1])),
+                                                       fmaxf(fmaf(max16(u + 32), by[2], add[2]), fmaf(max16(u + 48), by[3], add[3])));
+                                const bool need = mx > m && alive;
+                                const float alpha = need ? ex2(m - mx) : 1.f;     // m = -inf: 0
+                                if (need) {
+                                    m = mx;
+                                    l *= alpha;
+                                }
+                                if ((!fresh || h > 0) && __any_sync(0xffffffffu, need)) {
+                                    if (!wait_all(pv_half(t, h ^ 1), h == 0 ? par ^ 1u : par)) {
+                                        ok = false;
+                                        break;
+                                    }
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int i = 0; i < D / 16; ++i) {
+                                        uint32_t x[16];
+                                        tmem_ld16(o_addr + 16 * i, x);
+                                        tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float p0, p1;
-                                split2(fma2(pair2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), by2, add2x), p0, p1);
-                                p0 = ex2(p0);
-                                p1 = ex2(p1);
-                                s2[e & 1] = add2(s2[e & 1], pair2(p0, p1));
-                                w[8 * b + e] = pack2<false>(p0, p1);
+                                        for (int k = 0; k < 16; ++k) {
+                                            asm volatile("" : "+r"(x[k]));
+                                            x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+                                        }
+                                        tmem_st16(o_addr + 16 * i, x);
+                                    }
+                                    tmem_st_wait();
+                                }
                             }
-                            float sa, sb;
-                            split2(add2(s2[0], s2[1]), sa, sb);
-                            sum = fmaf(sa + sb, rc.back[(64 * h + 16 * b) / BS], sum);
-                        };
-                        weigh(u, 0);
-                        weigh(u + 16, 1);
-                        weigh(u + 32, 2);
-                        weigh(u + 48, 3);
+                            const float mref = m == -INFINITY ? 0.f : m;          // no visible key yet: weights 0
+                            sum = plain = 0.f;
+                            auto weigh = [&](const uint32_t* x, int b) {          // 16 scores -> 8 columns of weights
+                                const f32x2 by2 = pair2(by[b], by[b]), add2x = pair2(add[b] - mref, add[b] - mref);
+                                f32x2 s2[2] = {0ull, 0ull};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    float p0, p1;
+                                    split2(fma2(pair2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), by2, add2x), p0, p1);
+                                    p0 = ex2(p0);
+                                    p1 = ex2(p1);
+                                    s2[e & 1] = add2(s2[e & 1], pair2(p0, p1));
+                                    w[8 * b + e] = pack2<false>(p0, p1);
+                                }
+                                float sa, sb;
+                                split2(add2(s2[0], s2[1]), sa, sb);
+                                plain += sa + sb;
+                                sum = fmaf(sa + sb, rc.back[(64 * h + 16 * b) / BS], sum);
+                            };
+                            weigh(u, 0);
+                            weigh(u + 16, 1);
+                            weigh(u + 32, 2);
+                            weigh(u + 48, 3);
+                            if (redo) break;
+                            redo = __any_sync(0xffffffffu, alive && !(plain <= Tr::MOST));
+                            if (!redo) break;
+                        }
+                        if (!ok) break;
                         tmem_st32(s_addr + 64 * h, w);
                         l += sum;
                         tmem_st_wait();
