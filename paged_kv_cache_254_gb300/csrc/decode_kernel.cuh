@@ -204,8 +204,8 @@ struct Sched {
 
 // The schedule of W flattened blocks over `nworkers` warps with `nd` dynamic
 // chunks wanted: the last quarter goes dynamic when every chunk can hold a
-// few blocks, else the static split alone.
-__device__ __forceinline__ Sched make_sched(long long W, long long nworkers, int nd) {
+// few blocks, else the static split alone, with `least` blocks or more to a chunk.
+__device__ __forceinline__ Sched make_sched(long long W, long long nworkers, int nd, int least = 1) {
     Sched sc;
     sc.W = W;
     if (nd > 0 && W >= 64 * nworkers) {
@@ -214,7 +214,8 @@ __device__ __forceinline__ Sched make_sched(long long W, long long nworkers, int
         sc.ND = nd;
     } else {
         sc.Ws = W;
-        sc.NS = (int)(W < nworkers ? W : nworkers);
+        const long long most = (W + least - 1) / least;
+        sc.NS = (int)(most < nworkers ? most : nworkers);
         sc.ND = 0;
     }
     return sc;
@@ -337,7 +338,9 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     // ---- the chunk schedule ----
     const long long nworkers = (long long)gridDim.x * NW;
     const long long wid = (long long)blockIdx.x * NW + warp;
-    const Sched sc = make_sched(cum[p.N] * p.Hkv, nworkers, p.nd);
+    // (B8: a stage at least.  One sequence of 700 tokens, blocks of 16: 18.0 us in chunks of one block or more, 15.5 of
+    // two, 16.7 of four; more chunks are more pieces to merge)
+    const Sched sc = make_sched(cum[p.N] * p.Hkv, nworkers, p.nd, Tr::B8 ? UB : 1);
     const int nchunks = sc.NS + sc.ND;
     if (nchunks == 0) return;
     // next chunk for this warp: its static one first, then claims (lane 0's
@@ -885,7 +888,7 @@ pa_decode_merge(const long long* __restrict__ cum, const float* __restrict__ par
 template <int D>
 __global__ void __launch_bounds__(256, 6)
 pa_split_merge(const long long* __restrict__ cum, const float* __restrict__ partials, uint16_t* __restrict__ out,
-               int N, int Hkv, int G, long long nworkers, int nd, int splits, int bf16) {
+               int N, int Hkv, int G, long long nworkers, int nd, int least, int splits, int bf16) {
     constexpr int PSTRIDE = D + 4;
     constexpr int LPH = D / 4;                     // lanes per head
     constexpr int HPW = 32 / LPH;                  // heads per warp
@@ -899,7 +902,7 @@ pa_split_merge(const long long* __restrict__ cum, const float* __restrict__ part
     if (warp == 0) {
         const long long c0 = cum[s];
         const int nb = (int)(cum[s + 1] - c0);
-        const Sched sc = make_sched(cum[N] * Hkv, nworkers, nd);
+        const Sched sc = make_sched(cum[N] * Hkv, nworkers, nd, least);
         const long long P0 = c0 * Hkv + (long long)kvh * nb;
         const long long c = nb > 0 ? sc.of(P0 + (lane ? nb - 1 : 0)) : 0;
         if (lane < 2) where[lane] = c;
@@ -994,6 +997,7 @@ struct DecodeLaunch {
     int grid;
     bool bf16;   // output type of the merge post-pass
     bool split;  // pa_split_merge
+    int least;   // blocks of a chunk, for it
 };
 
 struct DecodeKernelInfo {

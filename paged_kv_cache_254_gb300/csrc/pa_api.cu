@@ -209,7 +209,7 @@ cudaError_t split_merge_launch(const DecodeLaunch& L, int g, long long nworkers,
     cudaLaunchConfig_t cfg = pdl_config(pairs, 256, 0, st, attr);
     cfg.gridDim.y = (unsigned)((hgroups * splits + 7) / 8);
     return cudaLaunchKernelEx(&cfg, pa_split_merge<D>, L.p.cum, static_cast<const float*>(L.p.partials), L.p.out,
-                              L.p.N, L.p.Hkv, g, nworkers, L.p.nd, splits, L.bf16 ? 1 : 0);
+                              L.p.N, L.p.Hkv, g, nworkers, L.p.nd, L.least, splits, L.bf16 ? 1 : 0);
 }
 
 // Lay out the decode region, run the pre-pass, fill L's scheduling fields,
@@ -1372,6 +1372,7 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
     L.p.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
     L.p.timeout_ns = kTimeoutNs;
     L.split = true;
+    L.least = 32 / shape->block_size;                // GeomB8's stages hold 32 tokens
     L.stream = static_cast<cudaStream_t>(stream);
     return run_decode(k, ctas, L, shape, workspace, workspace_bytes, nullptr);
 }
