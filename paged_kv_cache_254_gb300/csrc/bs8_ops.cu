@@ -23,6 +23,7 @@
 #include "bs8_ops.cuh"
 #include "decode_common.cuh"
 #include "launch.cuh"
+#include "packed.cuh"
 
 namespace pa {
 
@@ -75,10 +76,18 @@ struct Rows {
     // Eight 16-bit values times a power of two, as codes.
     static __device__ __forceinline__ uint2 codes(const uint4& x, float inv) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t c[4];
+        const f32x2 by = pair2(inv, inv);
+        uint16_t c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = f32x2_to_fp8x2<E5M2>(lo_of<BF16>(w[j]) * inv, hi_of<BF16>(w[j]) * inv);
-        return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split2(mul2(pair2(lo_of<BF16>(w[j]), hi_of<BF16>(w[j])), by), a, b);
+            c[j] = f32x2_to_fp8x2<E5M2>(a, b);
+        }
+        uint2 r;
+        asm("mov.b32 %0, {%1, %2};" : "=r"(r.x) : "h"(c[0]), "h"(c[1]));
+        asm("mov.b32 %0, {%1, %2};" : "=r"(r.y) : "h"(c[2]), "h"(c[3]));
+        return r;
     }
 
     // The same by a division, for scales that are no power of two.
@@ -100,7 +109,10 @@ struct Rows {
 
     // Where 8 codes from dimension 8 * sub of row r stand in the piece.
     static __device__ __forceinline__ int place(int op, int r, int sub) {
-        return (op ? bs8_value<BS, D>(r, sub >> 1) : bs8_key<D>(r, sub >> 1)) + 8 * (sub & 1);
+        // bs8_value and bs8_key in one form: which bits of r permute the parts is all that differs
+        const int sh = op ? 2 : 0, mask = D == 128 ? (op ? 6 : 7) : (op ? 2 : 0);
+        const int row = D == 64 && BS == 32 ? r ^ (op ? (r >> 4) & 1 : 0) : r;
+        return BS8_HEAD + (op ? BS * D : 0) + row * D + (((sub >> 1) ^ ((r >> sh) & mask)) << 4) + 8 * (sub & 1);
     }
 };
 
