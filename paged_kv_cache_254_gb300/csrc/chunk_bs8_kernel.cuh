@@ -23,10 +23,15 @@
 // S_t, 32 columns at the start of each 64 that held its scores.  Weights are
 // 2^(x - m) for a reference m that moves (to the maximum, with O rescaled) only when half a stage's
 // add up to more than 2^12: fp16 holds any of them, its relative precision is the same at every
-// size, and no stage has to know its maximum before its weights (978 us to 922).  A weight that is the
-// row's maximum has no rounding error, so a lower border is a little more precise: fp16
-// outputs are off by 2.15e-4 of their size for 2^6 (983 us), 2.31e-4 for 2^9 (939), 2.48e-4 for 2^12,
-// 2.62e-4 for 2^15 (920), of which 2.07e-4 are the outputs' own rounding.
+// size, and no stage has to know its maximum before its weights.  l adds up the weights with the 11 bits that
+// the products read (not with their fp16 underflow: a block of next to nothing counts in l), so that a weight's
+// rounding moves a row only by the distance of its value from the row's output, and not at all where one
+// key has the row.  Of outputs in fp16, relative to their size (2.07e-4 of it their own rounding):
+//                                drafts, 128 sequences     prompt of 4096 tokens
+//   l of weights of 24 bits      2.48e-4,  564 us          2.75e-4,  918 us
+//   l of weights of 11 bits      2.26e-4,  604 us          2.38e-4,  972 us    (this kernel)
+//   ... border 2^9               2.21e-4,  622 us          2.34e-4,  990 us
+//   ... border 2^6               2.13e-4,  667 us          2.26e-4, 1031 us
 //
 // Roles (one CTA per SM; 640 threads for SPLIT, else 512):
 //   warps 0-3, 4-7   softmax of tile 0, 1: thread = row = TMEM lane, half of a stage at a time, so that the
@@ -44,8 +49,8 @@
 // scores (700), their way to the softmax (200), two halves (1,000 to 1,800 each, the loads
 // 300 of it), the last products and their way back (700) follow one another, and the tiles'
 // warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
-// Measured on GB300: 920 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
-// 128 (900 TFLOP/s of 1,905); 562 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// Measured on GB300: 972 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (848 TFLOP/s of 1,905); 604 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
 // to 8192 (2.2 TB/s).  Also measured, against 1,060 us and 636: 64-key products ahead of the
 // softmax (1,470 us for the long prompt), scores of one stage in one piece (1,175), two softmax
 // warps to a row (1,250), codes loaded into registers from L2 (1,160), the conversion unrolled over
@@ -897,13 +902,18 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                             auto weigh = [&](const uint32_t* x, int b) {          // 16 scores -> 8 columns of weights
                                 const f32x2 by2 = pair2(by[b], by[b]), add2x = pair2(add[b] - mref, add[b] - mref);
                                 f32x2 s2[2] = {0ull, 0ull};
+                                // The weight with fp16's 11 bits: p - 2^13 p rounded to 24 bits, plus 2^13 p, which
+                                // stands on the places that were left.  (2^13 p + p - 2^13 p would round weights next below
+                                // a power of two to 10 bits, and a row's largest is often the one next below 1.)
+                                const f32x2 up2 = pair2(8192.f, 8192.f), down2 = pair2(-8192.f, -8192.f);
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
                                     float p0, p1;
                                     split2(fma2(pair2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), by2, add2x), p0, p1);
                                     p0 = ex2(p0);
                                     p1 = ex2(p1);
-                                    s2[e & 1] = add2(s2[e & 1], pair2(p0, p1));
+                                    const f32x2 p2 = pair2(p0, p1);
+                                    s2[e & 1] = add2(s2[e & 1], fma2(p2, up2, fma2(p2, down2, p2)));
                                     w[8 * b + e] = pack2<false>(p0, p1);
                                 }
                                 float sa, sb;
