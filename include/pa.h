@@ -400,7 +400,8 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
  * largest n_b of the call (>= 1); a longer chunk is malformed.  Arithmetic as
  * pa_decode_bs8.  NaN or an infinity in a value of the chunk's own tokens makes the rows
  * that see it NaN and no others.  Rows of out outside every chunk are left as they are.
- * out must not overlap q.  Two launches: attention, then the merge of split rows.
+ * out must not overlap q.  After PA_DEVERR_TIMEOUT the rows of the CTAs that gave up are NaN.
+ * Two launches: attention, then the merge of split rows.
  */
 size_t pa_decode_multi_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format, int32_t max_q_len);
 
@@ -578,13 +579,15 @@ pa_status pa_decode_noalloc(const pa_shape* shape, const void* q, const void* k_
 /*
  * Fault injection for tests of the wait limit (no counterpart on the pages).
  * With wait_ns > 0, every later launch of the decode attention kernel (by
- * pa_decode, pa_decode_noalloc, pa_decode_fp8, pa_decode_int4 and the second
- * pass of pa_decode_shared_prefix), in any thread of the process, makes each
- * worker warp's first stage wait on a shared-memory barrier that nothing
- * completes, for at most wait_ns.  When it gives up, the kernel takes its
- * timeout path: it sets PA_DEVERR_TIMEOUT, issues no further copies, writes
- * NaN to every output row and partial state of that worker, waits (at the
- * normal 2 s limit) for its copies still in flight and returns.  The call's
+ * pa_decode, pa_decode_noalloc, pa_decode_fp8, pa_decode_int4, pa_decode_bs8
+ * and the second pass of pa_decode_shared_prefix) and of the chunk kernel of
+ * pa_decode_multi_bs8, in any thread of the process, makes each worker (a warp
+ * of the decode, a CTA of the chunk kernel) make its first stage wait on a
+ * shared-memory barrier that nothing completes, for at most wait_ns.  When it
+ * gives up, the kernel takes its timeout path: it sets PA_DEVERR_TIMEOUT,
+ * issues no further copies, writes NaN to every output row and partial state
+ * of that worker, waits (at the normal 2 s limit) for its copies still in
+ * flight and returns.  The call's
  * outputs are then NaN (rows of zero-length contexts stay zero) and
  * pa_read_error returns PA_ERR_TIMEOUT.  wait_ns = 0 turns it off (the
  * default).  wait_ns above 1e9 (1 s): PA_ERR_INVALID_ARG.

@@ -49,17 +49,19 @@
 // scores (700), their way to the softmax (200), two halves (1,000 to 1,800 each, the loads
 // 300 of it), the last products and their way back (700) follow one another, and the tiles'
 // warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
-// Measured on GB300: 972 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
-// 128 (848 TFLOP/s of 1,905); 604 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// Measured on GB300: 987 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (836 TFLOP/s of 1,905); 589 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
 // to 8192 (2.2 TB/s).  Also measured, against 1,060 us and 636: 64-key products ahead of the
 // softmax (1,470 us for the long prompt), scores of one stage in one piece (1,175), two softmax
 // warps to a row (1,250), codes loaded into registers from L2 (1,160), the conversion unrolled over
 // both kinds (1,190: the roles' loops then fall out of the SM's instruction cache), polling loops
-// in place of held waits (no difference).
+// in place of held waits (no difference), waits that end when another role gives up (640 us against 589: code
+// around every wait; without it the CTA is gone within the limit of one wait, not at once).
 //
 // The work list and the partial states of split rows are those of the tree kernels: each CTA
 // takes an equal run of (row group, KV head, block) units; a group's keys end at its
-// last token's.  Every wait is bounded (PA_DEVERR_TIMEOUT).
+// last token's.  Every wait is bounded (PA_DEVERR_TIMEOUT); a CTA that gives up gives NaN for all that it
+// was to write, so that the merge finds nothing of an earlier call.
 #pragma once
 
 #include <climits>
@@ -128,8 +130,8 @@ struct ChunkTraits {
     static constexpr int R_CAP = 6;
     static constexpr int N8_CAP = 8;
     // empty, ready; empty8, full8; s_full, p_half[2], pv_half[2] per tile; q_full, q_empty; fin; described, forgotten;
-    // listed; joined, o1_free
-    static constexpr int NBAR = 2 * R_CAP + 2 * N8_CAP + 2 * 6 + 2 + 2 + 3 * NREC + 2;
+    // listed; joined, o1_free; stall
+    static constexpr int NBAR = 2 * R_CAP + 2 * N8_CAP + 2 * 6 + 2 + 2 + 3 * NREC + 3;
     static constexpr int REC_OFF = (8 * NBAR + 15) / 16 * 16;
     static constexpr int REC_BYTES = 48 + 5 * SB * 4;
     static constexpr int SLOT8_BYTES = KEYS * D;             // a stage's key or value codes
@@ -245,6 +247,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
     auto listed = [&](int j) -> uint32_t { return fin + 16 + 8 * (2 * Tr::NREC + j % Tr::NREC); };     // its blocks do, without their scales
     // SPLIT: tile 1's state of a segment is there; tile 0 has read it
     const uint32_t joined = fin + 16 + 8 * 3 * Tr::NREC, o1_free = joined + 8;
+    const uint32_t stall_bar = o1_free + 8;                    // nothing completes it (pa_set_decode_stall_ns)
     Stage* recs = reinterpret_cast<Stage*>(smem + Tr::REC_OFF);
     float* rowf = reinterpret_cast<float*>(smem + Tr::ROWF_OFF);
     float2* xch = reinterpret_cast<float2*>(smem + Tr::XCH_OFF);
@@ -280,6 +283,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         }
         mbar_init(joined, 4);
         mbar_init(o1_free, 4);
+        mbar_init(stall_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -508,7 +512,10 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 if (!ok && lane == 0) {
                     set_err(p.err, PA_DEVERR_TIMEOUT);
                     *abort_flag = 1;
-                    // copies still in flight land before the CTA's shared memory is released
+                }
+                // Copies still in flight land before the CTA's shared memory is released, whoever gave up (the converting
+                // warps may have left stages that were copied long before).
+                if (lane == 0) {
                     for (int op = 0; op < 2; ++op)
                         for (int k = max(0, copied[op] - (op ? Tr::NV8 : Tr::NK8)); k < copied[op]; ++k)
                             wait_bounded(full8(slot8(op, k)), (uint32_t)(uses8(op, k) & 1), p.timeout_ns);
@@ -661,8 +668,9 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
             __syncwarp();
             if (lane == 0) mbar_arrive(ready(item % R));
         };
-        bool end = !wait_all(described(0), 0);
-        ok = !end;
+        ok = wait_all(described(0), 0);
+        if (ok && p.stall_ns != 0 && !(recs[0].flags & TC_END))
+            ok = __all_sync(0xffffffffu, wait_bounded(stall_bar, 0, p.stall_ns));
         for (int j = 0; ok; ++j) {
             Stage& rc = recs[j % Tr::NREC];
             const int flags = rc.flags;
@@ -787,7 +795,6 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         float m = -INFINITY, l = 0.f, rf = 0.f;                   // reference (log2 units), sum, the row's score factor
         bool alive = false, active = false, fresh = true, ok = true;
         for (int j = 0;; ++j) {
-            if (*abort_flag) break;
             if (!wait_all(described(j), (uint32_t)((j / Tr::NREC) & 1))) {
                 ok = false;
                 break;
@@ -795,6 +802,10 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
             const Stage& rc = recs[j % Tr::NREC];
             const int flags = rc.flags;
             if (flags & TC_END) break;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+                ok = false;
+                break;
+            }
             if (flags & TC_FIRST) {
                 cur_seg = rc.seg;
                 seg_q0 = rc.q0;                                   // (a record may be written again before a segment's end is over)
@@ -1052,6 +1063,32 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         if (!ok) {
             if (lane == 0) set_err(p.err, PA_DEVERR_TIMEOUT);
             *abort_flag = 1;
+            // The rows and partial states of the CTA's whole run become NaN, each by the thread that it is written by (an
+            // l of NaN is NaN after the merge, whatever stands beside it).  Rows written before are among them.
+            // (the run is found again from shared memory: what is kept for it costs the loop registers)
+            const volatile TreeStart& from = *reinterpret_cast<TreeStart*>(smem + Tr::START_OFF);
+            const Sched sc = tree_sched(from.W, gridDim.x, SB);
+            const bool has_rows = (int)blockIdx.x < sc.NS && !(SPLIT && t == 1);
+            const long long lo = has_rows ? sc.lo(blockIdx.x) : 0, hi = has_rows ? sc.lo(blockIdx.x + 1) : 0;
+            SegIter it{lo, from.s, from.kvh, from.b0, from.nb, 0};
+            while (it.gi < hi) {
+                const int len = seg_len(it, hi), s = it.s % seqs, skip = it.s / seqs * mp.group_nodes;
+                if (token < min(mp.group_nodes, chunk_size(s) - skip)) {
+                    const long long P0 = it.gi - it.b0;
+                    if (sc.of(P0) == sc.of(P0 + it.nb - 1)) {
+                        uint4* orow = reinterpret_cast<uint4*>(
+                            p.out + ((size_t)(__ldg(qst + s) + skip + token) * p.Hq + (size_t)it.kvh * G + (row_of_group & (G - 1))) * D);
+                        const uint32_t two = qnan16<Tr::BF16>() * 0x10001u;
+#pragma unroll 1
+                        for (int i = 0; i < D / 8; ++i) orow[i] = make_uint4(two, two, two, two);
+                    } else {
+                        float* prow = p.partials + (((size_t)blockIdx.x * 2 + (it.gi == lo ? 0 : 1)) * Tr::ROWS + row_of_group) * Tr::PSTRIDE;
+                        prow[D] = 0.f;
+                        prow[D + 1] = qnan;
+                    }
+                }
+                seg_advance(it, len, p, tab);
+            }
         }
     }
 

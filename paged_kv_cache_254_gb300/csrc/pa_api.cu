@@ -31,7 +31,7 @@ using namespace pa;
 constexpr uint64_t kTimeoutNs = 2000000000ull;   // bound on any device-side wait
 constexpr uint64_t kMaxStallNs = 1000000000ull;  // longest injected stall (pa_set_decode_stall_ns)
 
-// Injected stall of the decode kernel's first stage wait (0: off).
+// Injected stall of the first stage wait of the decode kernel and of the block-scaled chunks' (0: off).
 std::atomic<uint64_t> g_stall_ns{0};
 
 struct DecodeTables {
@@ -1431,6 +1431,7 @@ pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t 
     d.MB = shape->max_blocks_per_seq;
     d.scale_log2 = (float)((double)scale * 1.4426950408889634);   // log2(e)
     d.timeout_ns = kTimeoutNs;
+    d.stall_ns = g_stall_ns.load(std::memory_order_relaxed);
     d.v_scale = 1.0f;
     L.p.q_start = q_start;
     L.p.max_q = max_q_len;

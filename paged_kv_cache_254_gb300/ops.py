@@ -194,8 +194,9 @@ def pa_copy_blocks(src_dst_pairs, k_pool, v_pool, err=None, stream=None):
 
 def pa_set_decode_stall_ns(wait_ns: int) -> None:
     """Fault injection for tests (see include/pa.h): with wait_ns > 0 every
-    later decode launch makes each worker's first stage wait on a barrier
-    that nothing completes, for at most wait_ns, so the kernel's timeout path
+    later decode launch, and every launch of pa_decode_multi_bs8's chunk
+    kernel, makes each worker's first stage wait on a barrier that nothing
+    completes, for at most wait_ns, so the kernel's timeout path
     runs; 0 turns it off."""
     _lib.check(_lib.load().pa_set_decode_stall_ns(ctypes.c_uint64(int(wait_ns))), "pa_set_decode_stall_ns")
 
