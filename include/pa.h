@@ -379,12 +379,15 @@ pa_status pa_append_kv_bs8(const pa_shape* shape, int32_t kv_format, int32_t max
 
 /*
  * pa_decode over the block-scaled pool: attention over K = scale * code, V = scale * code
- * of each piece, with any scales (not only appended ones).  Computed in fp16 on the
+ * of each piece, with any key scales (not only appended ones).  Computed in fp16 on the
  * tensor cores with fp32 sums: codes are exact in fp16, a bf16 query row is brought into
  * fp16's range by a power of two (values below 2^-29 of the row's largest lose bits),
  * softmax weights are rounded once to fp16 in proportion to their share of the output.  A
- * bad scale sets PA_DEVERR_SCALE, and the rows that read it are NaN.  A value scale below
- * 2^-126 counts as that.  out must not overlap q.  Other arguments, supported groups,
+ * bad scale sets PA_DEVERR_SCALE, and the rows that read it are NaN.  Value scales from
+ * 2^-100 to 2^26 and no more than 2^100 apart in a sequence stand for their values in full
+ * (appended and packed ones do for values from 2^-91 to 2^34 and zeros); the values of a
+ * block with a smaller one lose bits and become zero, its keys count in the softmax all the
+ * same, and outputs beside a larger one may be off.  out must not overlap q.  Other arguments, supported groups,
  * errors and launches as pa_decode.
  */
 size_t pa_decode_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format);

@@ -11,9 +11,14 @@
 // make up the output.  (Weights e^(s_t - max s) times b would lose their last bits in
 // fp16 wherever b is far below the row's largest.)
 // Blocks whose values are all but zero would leave their tokens no weight, though the
-// softmax counts them in l: lb is therefore held above R - 24 (R the largest lb of the
+// softmax counts them in l: lb is therefore held above R - 100 (R the largest lb of the
 // stream so far) and above -100, and what is cut off, f = 2^(log2 b - lb), multiplies
-// the weights that enter O (1 but for such blocks).
+// the weights that enter O (1 but for such blocks).  In 32 bits that is far enough: m is at most the
+// row's largest score plus R, so a token that has 2^-24 or more of the softmax keeps w_t of 2^-124 or more,
+// and l, no more than 2^100 a token, stays above 2^-R.  (A smaller range, 24, took a row's own values
+// to zero in fp16 wherever a block that the row all but ignores had a scale 2^40 times theirs.)
+// When R rises behind blocks that were held at -100, l is multiplied by 2^(m - m') of 2^-126 at least
+// as long as R is no more than 26.
 //
 // Queries enter as fp16.  A bf16 query row is multiplied by the power of two that brings
 // its largest value between 2^14 and 2^15, which no finite row overflows and which
@@ -50,7 +55,7 @@ struct GeomB8 {
     static_assert(UB == 1 || PIECE_PAD % 128 == 64, "bank spread of the second piece");
 };
 
-constexpr float BS8_LB_RANGE = 24.f, BS8_LB_FLOOR = -100.f;   // of lb, see above
+constexpr float BS8_LB_RANGE = 100.f, BS8_LB_FLOOR = -100.f;   // of lb, see above
 
 // Running state of one warp: as WarpAccT (m and l as above), and R.  Row e >> 1 of
 // m-tile mt is dimension D / 8 g + 2 mt + (e >> 1): a lane holds D / 8 consecutive ones.
