@@ -402,7 +402,7 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
  * prefill -- thewebvale "vLLM & High-Throughput Serving", section 4).  max_q_len: the
  * largest n_b of the call (>= 1); a longer chunk is malformed.  Arithmetic as
  * pa_decode_bs8.  NaN or an infinity in a value of the chunk's own tokens makes the rows
- * that see it NaN and no others.  Rows of out outside every chunk are left as they are.
+ * that see it NaN and no others, and so does a bad block id or scale.  Rows of out outside every chunk are left as they are.
  * out must not overlap q.  After PA_DEVERR_TIMEOUT the rows of the CTAs that gave up are NaN.
  * Two launches: attention, then the merge of split rows.
  */

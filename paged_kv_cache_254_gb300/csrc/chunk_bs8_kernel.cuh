@@ -138,7 +138,7 @@ struct ChunkTraits {
     static constexpr int ROWF_OFF = REC_OFF + NREC * REC_BYTES;   // score factors of the rows, two segments
     static constexpr int XCH_OFF = ROWF_OFF + 2 * 2 * TILE * 4;   // SPLIT: tile 1's (m, l) of a row
     static constexpr int MISC_OFF = XCH_OFF + (SPLIT ? TILE * 8 : 0);   // TMEM base, abort flag
-    static constexpr int SPOILT_OFF = MISC_OFF + 16;         // per segment: first position of a value that is not finite
+    static constexpr int SPOILT_OFF = MISC_OFF + 16;         // per segment: first position of a bad block or a value that is not finite
     static constexpr int NSEG = 2 * NREC;
     static constexpr int START_OFF = SPOILT_OFF + NSEG * 4;  // a TreeStart, a word per warp
     static constexpr int Q_OFF = (START_OFF + 32 + 8 * THREADS / 32 + 1023) / 1024 * 1024;
@@ -163,7 +163,7 @@ template <int SB>
 struct alignas(16) ChunkStage {
     int base, kvh, t0, nkeys;     // position of the group's first token, KV head, first key, keys copied
     int n, ctx, q0, flags;        // tokens of the group, context, the group's first query row
-    int poison, seg, chunk, cuts; // bad block id or scale; segment number; the chunk's first position; any cut != 1
+    int seg, chunk, cuts, spare;  // segment number; the chunk's first position; any cut != 1
     int ids[SB];
     float ks[SB], lb[SB], back[SB], cut[SB];   // key scale, lb, 2^-lb, f of decode_bs8.cuh
 };
@@ -444,6 +444,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 if (lane == 0) mbar_arrive(listed(j));
                 const bool held_here = lane < x.nbs;
                 const bool bad_scale = held_here && (!bs8_is_scale(x.scales.x) || !bs8_is_scale(x.scales.y));
+                if (bad_scale) x.scales = make_float2(0.f, 0.f);   // (rows that do not see the block keep their sums)
                 const float lb = held_here ? fmaxf(__log2f(x.scales.y), -126.f) : -INFINITY;
                 float top = lb;
 #pragma unroll
@@ -458,11 +459,12 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     rc.cut[lane] = cut;
                 }
                 const bool any_id = __any_sync(0xffffffffu, x.bad), any_scale = __any_sync(0xffffffffu, bad_scale);
+                const uint32_t bad = __ballot_sync(0xffffffffu, x.bad || bad_scale);
                 const bool any_cut = __any_sync(0xffffffffu, cut != 1.f);
                 if (lane == 0) {
                     if (any_id) set_err(p.err, PA_DEVERR_BLOCK_ID);
                     if (any_scale) set_err(p.err, PA_DEVERR_SCALE);
-                    rc.poison = any_id || any_scale;
+                    if (bad) atomicMin(&spoilt[x.seg % Tr::NSEG], x.t0 + (__ffs((int)bad) - 1) * BS);
                     rc.cuts = any_cut;
                 }
                 __syncwarp();
@@ -791,7 +793,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lane_addr + 128 * t, o_addr = lane_addr + Tr::O_COL + 128 * t;
         const float qnan = __int_as_float(0x7fc00000);
-        int own = 0, cur_seg = 0, pois = 0, seg_q0 = 0, seg_kvh = 0, last_seen = 0;
+        int own = 0, cur_seg = 0, seg_q0 = 0, seg_kvh = 0, last_seen = 0;
         float m = -INFINITY, l = 0.f, rf = 0.f;                   // reference (log2 units), sum, the row's score factor
         bool alive = false, active = false, fresh = true, ok = true;
         for (int j = 0;; ++j) {
@@ -813,12 +815,10 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 last_seen = rc.base + token;
                 m = -INFINITY;
                 l = 0.f;
-                pois = 0;
                 fresh = true;
                 alive = token < rc.n;
                 active = SPLIT || rc.n > t * tile_nodes;
             }
-            pois |= rc.poison;
             const bool mine = !SPLIT || (j & 1) == t;
             const bool busy = active && __any_sync(0xffffffffu, alive);
             if (mine) {
@@ -998,12 +998,13 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                     l = l * f0 + x.y * f1;
                     m = top;
                 }
-                // the segment's values have all been converted; a row that sees one that is not finite is NaN
+                // the segment's values have all been converted; a row that sees one that is not finite, or a block with a bad
+                // id or scale, is NaN
                 if (*const_cast<const volatile int*>(&spoilt[cur_seg % Tr::NSEG]) <= last_seen) l = qnan;
                 if (busy) {
                     tc_fence_after();
                     const bool complete = flags & TC_COMPLETE;
-                    const float inv = pois ? qnan : complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                    const float inv = l != l ? qnan : complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                     f0 *= inv;
                     f1 *= inv;
                     // Each lane writes its row, 32 columns at a time (rows of one token stand side by side in the output, so
@@ -1023,7 +1024,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                             for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f0);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(pois ? qnan : 0.f);
+                            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(l != l ? qnan : 0.f);
                         }
                         if (SPLIT && other) {
                             uint32_t v[32];
