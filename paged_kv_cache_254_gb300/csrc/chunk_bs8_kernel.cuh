@@ -384,7 +384,7 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                 x.bad = held && (unsigned)x.id >= (unsigned)p.NB;
                 if (!held || x.bad) x.id = 0;
                 x.scales = make_float2(0.f, 0.f);
-                if (held) x.scales = __ldg(reinterpret_cast<const float2*>(p.kv8 + ((size_t)x.id * p.Hkv + it.kvh) * bs8_piece_bytes(BS, D)));
+                if (held && !x.bad) x.scales = __ldg(reinterpret_cast<const float2*>(p.kv8 + ((size_t)x.id * p.Hkv + it.kvh) * bs8_piece_bytes(BS, D)));
                 x.base = ctx - size + skip;
                 x.kvh = it.kvh;
                 x.t0 = (it.b0 + bb) * BS;

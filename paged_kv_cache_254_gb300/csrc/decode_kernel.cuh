@@ -641,7 +641,8 @@ pa_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             if constexpr (Tr::B8) {
                 if (!consume_stage_b8<Gm, Tr::NR, Tr::E5M2>(kb, valid, qa, qf, acc, lane)) {
                     poisoned = 1;
-                    if (lane == 0) set_err(p.err, PA_DEVERR_SCALE);
+                    // (in place of a block that is not there another is read, whose scale nobody asked for)
+                    if (lane == 0 && !stage_poison[st]) set_err(p.err, PA_DEVERR_SCALE);
                 }
             } else if constexpr (Tr::I4) {
                 consume_stage4t<Gm, Tr::NR>(kb, valid, qa, qc, acc, p.scale_log2, lane);

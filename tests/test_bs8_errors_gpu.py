@@ -51,3 +51,25 @@ def test_rows_before_a_bad_block_are_untouched(B, d, dtype, ctx, n, block):
             p = pool.copy()
             scales_of(p)[table[0, block // B], 1, i] = s
             run(table, p, 256, slice(8, 16))
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_a_bad_id_says_nothing_of_other_blocks_scales(kind):
+    """A block that no table names holds no scale: it is not read in place of one that is out of range."""
+    r = np.random.default_rng(3)
+    table, NB = place(r, [100, 50], 16)
+    pool = random_pool(r, NB, 2, 16, 128, "e4m3")
+    free = (set(range(NB)) - set(table[table < NB].tolist())).pop()
+    table, pool = np.where(table == 0, free, np.where(table == free, 0, table)), pool.copy()   # block 0 is free now
+    pool[[0, free]] = pool[[free, 0]]
+    pool[0] = 0xFF
+    assert not (table == 0).any()
+    table[0, 2] = -1
+    args = (dev(pool), dev(table.astype(np.int32)), dev(np.array([100, 50], np.int32)))
+    q = torch.from_numpy(r.standard_normal((2, 8, 128))).bfloat16().cuda()
+    err = pa().new_error_word("cuda")
+    if kind == "decode":
+        out = pa().pa_decode_bs8(q, *args, 0.1, err=err)
+    else:
+        out = pa().pa_decode_multi_bs8(q, *args, dev(np.array([0, 1, 2], np.int32)), 0.1, err=err)
+    assert int(err.item()) == 1 and out[0].isnan().all() and not out[1].isnan().any()
