@@ -587,7 +587,7 @@ pa_status plan_chunk(const pa_shape* s, int kv_format, int max_q, TreePlan* out)
     out->groups = (max_q - 1) / out->group_nodes + 1;
     out->tile_nodes = 128 / g;
     out->min_blocks = 128 / s->block_size;
-    return (long long)s->num_seqs * out->groups < (1ll << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
+    return PA_OK;
 }
 
 // Workspace of prefix-aware decode (offsets in off[]): [0] prefix counters,
@@ -1402,16 +1402,20 @@ pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t 
         return PA_ERR_INVALID_ARG;
     const uint64_t bytes = (uint64_t)total_q * shape->num_q_heads * shape->head_dim * 2;
     if (total_q > 0 && overlap(q, bytes, out, bytes)) return PA_ERR_INVALID_ARG;
-    // no chunk is longer than the call's rows, or than a table holds
+    // no chunk is longer than the call's rows, or than a table holds, whatever max_q_len is: the list has the groups that
+    // this takes (max_q_len decides how the workspace is sized)
     const int most = (int)std::min({(long long)max_q_len, std::max(1ll, (long long)total_q),
                                     (long long)shape->max_blocks_per_seq * shape->block_size});
+    TreePlan fitting;
+    if (plan_chunk(shape, kv_format, most, &fitting) != PA_OK) return PA_ERR_INVALID_ARG;
+    if ((long long)shape->num_seqs * fitting.groups >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
     const int ctas = plan.k->max_ctas(dev);
     if (ctas <= 0) return PA_ERR_CUDA;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < tree_region_bytes(shape, plan, ctas))
         return PA_ERR_WORKSPACE;
-    if (plan_chunk(shape, kv_format, most, &plan) != PA_OK) return PA_ERR_UNSUPPORTED;
+    plan = fitting;
 
     uint8_t* base = static_cast<uint8_t*>(workspace);
     MultiLaunch L{};
