@@ -283,7 +283,7 @@ cudaError_t append_bs8_launch(const AppendBs8Args& a, Bs8Kind kind, cudaStream_t
 }
 
 cudaError_t pack_bs8_launch(const ConvertBs8Args& a, Bs8Kind kind, cudaStream_t stream) {
-    const long long warps = a.n * 2 * a.Hkv;
+    const long long warps = (long long)a.n * 2 * a.Hkv;
     return by_kind(kind, [&](auto d, auto bs, auto bf, auto e5) {
         return launch(pa_pack_bs8_kernel<d(), bs(), bf(), e5()>, (unsigned)((warps + WARPS - 1) / WARPS), 32 * WARPS, 0,
                       stream, a);
@@ -291,7 +291,7 @@ cudaError_t pack_bs8_launch(const ConvertBs8Args& a, Bs8Kind kind, cudaStream_t 
 }
 
 cudaError_t unpack_bs8_launch(const ConvertBs8Args& a, Bs8Kind kind, cudaStream_t stream) {
-    const long long warps = a.n * 2 * a.Hkv;
+    const long long warps = (long long)a.n * 2 * a.Hkv;
     return by_kind(kind, [&](auto d, auto bs, auto bf, auto e5) {
         return launch(pa_unpack_bs8_kernel<d(), bs(), bf(), e5()>, (unsigned)((warps + WARPS - 1) / WARPS), 32 * WARPS, 0,
                       stream, a);

@@ -30,3 +30,26 @@ def test_any_bound_for_many_sequences(most):
                                    max_q_len=most, err=err)
     assert int(err.item()) == 0
     check(out, *rows_of(q, pool, table, ctx, qs, 0.125, B, "e4m3"))
+
+
+@pytest.mark.parametrize("call", ["pack", "unpack"])
+def test_conversions_of_2_to_the_30_pieces(call):
+    """2^20 pairs of 1024 heads, keys and values, are 2^31 warps: all but the last pair are out of range."""
+    r = np.random.default_rng(2)
+    H, B, d, n = 1024, 16, 64, 1 << 20
+    pool = dev(random_pool(r, 1, H, B, d, "e4m3"))
+    pairs = torch.full((n, 2), 5, dtype=torch.int32, device="cuda")
+    pairs[-1] = 0
+    k, v = (torch.randn(1, H, B, d, device="cuda").half() for _ in range(2))
+    one = pairs[-1:].contiguous()
+    if call == "pack":
+        pa().pa_pack_blocks_bs8(pairs, k, v, pool)
+        want = pa().bs8_pool(1, H, B, d)
+        pa().pa_pack_blocks_bs8(one, k, v, want)
+        keep = [*range(8), *range(32, pool.shape[2])]          # without the spare bytes
+        assert torch.equal(pool[..., keep], want[..., keep])
+    else:
+        k2, v2 = torch.zeros_like(k), torch.zeros_like(v)
+        pa().pa_unpack_blocks_bs8(pairs, pool, k, v)
+        pa().pa_unpack_blocks_bs8(one, pool, k2, v2)
+        assert torch.equal(k, k2) and torch.equal(v, v2) and k2.any()
