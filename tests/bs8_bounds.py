@@ -3,7 +3,8 @@
 import numpy as np
 import torch
 
-from oracle.bs8 import dequantized_pools, scales_of
+from oracle.bs8 import dequantized_pools, positions, scales_of
+from tests.bs8_util import DTYPES, place, random_pool
 
 
 def rows_of(q, pool, table, ctx, q_start, scale, B, fmt, lost=()):
@@ -63,3 +64,40 @@ def rows_of(q, pool, table, ctx, q_start, scale, B, fmt, lost=()):
             for x, y in ((want, o), (bound, err * (1 + half) + half * np.abs(o) + tiny)):
                 x[a:e, h * g:(h + 1) * g] = y.reshape(e - a, g, d)
     return want, bound
+
+
+# contexts that are cut into many pieces: (contexts, new tokens (None: a decode), Hq, Hkv, B, d, type)
+LONG = [([20000], None, 8, 1, 16, 128, "bf16"), ([20000], None, 8, 1, 16, 128, "fp16"),
+        ([9000, 11, 12000, 5000], None, 4, 4, 32, 64, "bf16"), ([20000], [5], 8, 1, 16, 128, "bf16"),
+        ([9000, 40, 12000], [20, 3, 40], 8, 1, 16, 128, "fp16"), ([6000, 5000], [300, 17], 4, 4, 32, 64, "bf16")]
+
+
+def block_by_block(r, pool, table, ctx, B, d):
+    """Values by which every block shows: block i of a sequence has values in dimension i mod d alone, positive ones, so
+    that a lost block takes a part of one dimension that no rounding takes; keys are small, the softmax nearly flat."""
+    key, val = positions(B, d)
+    s = scales_of(pool)
+    s[..., 0] /= 64
+    codes = pool[..., val]                                     # [NB, Hkv, B, d]
+    codes &= 0x7F
+    shown = np.zeros((len(pool), d), bool)
+    for row, c in zip(table, ctx):
+        n = -(-int(c) // B)
+        shown[row[:n], np.arange(n) % d] = True
+    codes[~np.broadcast_to(shown[:, None, None], codes.shape)] = 0
+    # (rows past the context are not cached; small codes give way to 1.0, so that each block counts)
+    codes[np.broadcast_to(shown[:, None, None], codes.shape) & (codes < 0x38)] = 0x38
+    pool[..., val] = codes
+
+
+def long_case(i, values):
+    """Case LONG[i] with values "random" or "block by block": (q, pool, table, ctx, q_start, scale, B)."""
+    ctx, n, Hq, Hkv, B, d, dtype = LONG[i]
+    r = np.random.default_rng(100 + i)
+    table, NB = place(r, ctx, B)
+    pool = random_pool(r, NB, Hkv, B, d, "e4m3", spread=4.0 if values == "random" else 1.0)
+    if values != "random":
+        block_by_block(r, pool, table, ctx, B, d)
+    q_start = np.concatenate([[0], np.cumsum(n or [1] * len(ctx))]).astype(np.int32)
+    q = torch.from_numpy(r.standard_normal((int(q_start[-1]), Hq, d))).to(DTYPES[dtype])
+    return q, pool, table, ctx, q_start, 1 / np.sqrt(d), B
