@@ -784,6 +784,11 @@ def _bs8_format(kv_format) -> int:
     return KV_FORMATS[kv_format]
 
 
+def _bound(n):
+    # (no chunk reaches 2^31 tokens; ctypes would cut the number to its low 32 bits)
+    return n if n is None else min(n, 2 ** 31 - 1)
+
+
 def _bs8_shape(kv_pool, head_dim, dtype, dev) -> _lib.PaShape:
     """Shape of a pool of pieces for head_dim; the block size follows from their bytes."""
     if dtype not in _DTYPES:
@@ -807,6 +812,7 @@ def pa_append_kv_bs8(k_new, v_new, block_tables, context_lens, q_start, kv_pool,
                           kv_format, max_new, err)
     if max_new is None and isinstance(q_start, torch.Tensor):
         max_new = _largest_chunk(q_start)
+    max_new = _bound(max_new)
     args = (k_new, v_new, block_tables, context_lens, q_start, kv_pool, _bs8_format(kv_format), max_new, err)
     if (_fast or _load_fast()).append_kv_bs8(*args) is NotImplemented:
         _append_kv_bs8(*args)
@@ -929,6 +935,7 @@ def pa_decode_multi_bs8(q, kv_pool, block_tables, context_lens, q_start, scale, 
                           kv_format, max_q_len, out, workspace, err)
     if max_q_len is None and isinstance(q_start, torch.Tensor):
         max_q_len = _largest_chunk(q_start)
+    max_q_len = _bound(max_q_len)
     args = (q, kv_pool, block_tables, context_lens, q_start, scale, _bs8_format(kv_format), max_q_len, out, workspace,
             err)
     done = (_fast or _load_fast()).decode_multi_bs8(_sp_cache, *args)

@@ -53,3 +53,21 @@ def test_conversions_of_2_to_the_30_pieces(call):
         pa().pa_unpack_blocks_bs8(pairs, pool, k, v)
         pa().pa_unpack_blocks_bs8(one, pool, k2, v2)
         assert torch.equal(k, k2) and torch.equal(v, v2) and k2.any()
+
+
+@pytest.mark.parametrize("most", [2 ** 31, 2 ** 32 + 1, 2 ** 63])
+def test_bounds_past_32_bits(most):
+    r = np.random.default_rng(3)
+    ctx, n, B, d = [40, 200], [9, 30], 16, 64
+    table, NB = place(r, ctx, B)
+    qs = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    q, k, v = (torch.from_numpy(r.standard_normal((39, h, d))).half().cuda() for h in (4, 2, 2))
+    args, pools, outs = (dev(table), dev(np.array(ctx, np.int32)), dev(qs)), [], []
+    start = random_pool(r, NB, 2, B, d, "e4m3")
+    for m in (30, most):
+        pools.append(dev(start))
+        err = pa().new_error_word("cuda")
+        pa().pa_append_kv_bs8(k, v, *args, pools[-1], max_new=m, err=err)
+        outs.append(pa().pa_decode_multi_bs8(q, pools[-1], *args, 0.1, max_q_len=m, err=err))
+        assert int(err.item()) == 0
+    assert torch.equal(*pools) and torch.equal(*outs)
