@@ -1411,9 +1411,11 @@ pa_status pa_decode_multi_bs8(const pa_shape* shape, int32_t kv_format, int32_t 
     if ((long long)shape->num_seqs * fitting.groups >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-    const int ctas = plan.k->max_ctas(dev);
-    if (ctas <= 0) return PA_ERR_CUDA;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < tree_region_bytes(shape, plan, ctas))
+    // (max_ctas() also sets up the kernel that it is asked about, which the launched one may be for the first time)
+    const int sized = plan.k->max_ctas(dev), ctas = fitting.k->max_ctas(dev);
+    if (sized <= 0 || ctas <= 0) return PA_ERR_CUDA;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < std::max(tree_region_bytes(shape, plan, sized), tree_region_bytes(shape, fitting, ctas)))
         return PA_ERR_WORKSPACE;
     plan = fitting;
 
