@@ -937,7 +937,8 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                             weigh(u + 32, 2);
                             weigh(u + 48, 3);
                             if (redo) break;
-                            redo = __any_sync(0xffffffffu, alive && !(plain <= Tr::MOST));
+                            // (a weight above 2^114 is -inf or NaN with 11 bits)
+                            redo = __any_sync(0xffffffffu, alive && !(fabsf(plain) <= Tr::MOST));
                             if (!redo) break;
                         }
                         if (!ok) break;
