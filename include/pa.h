@@ -333,12 +333,13 @@ pa_status pa_copy_blocks_fp8(const pa_shape* shape, const int32_t* src_dst_pairs
  * group (letsbuildsolutions "How LLM Inference Engines Work", quantization).  The
  * scales follow the data: nothing has to be known of a model's keys and values.
  *
- * Layout: ONE pool of bytes [NB][Hkv][P], P = 32 + 2 * B * d, 32-byte aligned.  A piece
+ * Layout: ONE pool of bytes [NB][Hkv][P], P = 32 + 2 * B * d, 32-byte aligned. A piece
  * holds the keys' scale and the values' scale (fp32, finite and not negative), 24 spare
- * bytes, B key rows of d codes, B value rows of d codes.  A stored value is scale * code.  The 16-byte parts of a row are permuted: part c (dimensions 16 c .. 16 c + 15)
- * of key row r stands at part c XOR (r mod 8) for d = 128 and at c for d = 64; of value
- * row r at part c XOR 2 (r / 8 mod 4) for d = 128, and for d = 64 at part c XOR 2 (r / 8
- * mod 2) of row r XOR (r / 16 mod 2).  A pool of zeros is a valid empty one.
+ * bytes, B key rows of d codes, B value rows of d codes. A stored value is scale * code.
+ * The 16-byte parts of a row are permuted: part c (dimensions 16 c .. 16 c + 15) of key row
+ * r stands at part c XOR (r mod 8) for d = 128 and at c for d = 64; of value row r at part
+ * c XOR 2 (r / 8 mod 4) for d = 128, and for d = 64 at part c XOR 2 (r / 8 mod 2) of row r
+ * XOR (r / 16 mod 2). A pool of zeros is a valid empty one.
  *
  * kv_format: PA_FP8_E4M3 or PA_FP8_E5M2, F its largest value (448, 57344).  Codes are
  * rounded to nearest even; an infinity becomes the largest code, NaN stays NaN.  (E5M2's codes
@@ -379,16 +380,16 @@ pa_status pa_append_kv_bs8(const pa_shape* shape, int32_t kv_format, int32_t max
 
 /*
  * pa_decode over the block-scaled pool: attention over K = scale * code, V = scale * code
- * of each piece, with any key scales (not only appended ones).  Computed in fp16 on the
- * tensor cores with fp32 sums: codes are exact in fp16, a bf16 query row is brought into
- * fp16's range by a power of two (values below 2^-29 of the row's largest lose bits),
- * softmax weights are rounded once to fp16 in proportion to their share of the output.  A
- * bad scale sets PA_DEVERR_SCALE, and the rows that read it are NaN.  Value scales from
- * 2^-100 to 2^26 and no more than 2^100 apart in a sequence stand for their values in full
- * (appended and packed ones do for values from 2^-91 to 2^34 and zeros); the values of a
- * block with a smaller one lose bits and become zero, its keys count in the softmax all the
- * same, and outputs beside a larger one may be off.  out must not overlap q.  Other arguments, supported groups,
- * errors and launches as pa_decode.
+ * of each piece, with any key scales (not only appended ones) that leave the scores in
+ * fp32's range. Computed in fp16 on the tensor cores with fp32 sums: codes are exact in
+ * fp16, a bf16 query row is brought into fp16's range by a power of two (values below 2^-29
+ * of the row's largest lose bits), softmax weights are rounded once to fp16 in proportion
+ * to their share of the output. A bad scale sets PA_DEVERR_SCALE, and the rows that read it
+ * are NaN. Value scales from 2^-100 to 2^26 and no more than 2^100 apart in a sequence
+ * stand for their values in full (appended and packed ones do for values from 2^-84 to 2^34
+ * and zeros); the values of a block with a smaller one lose bits and become zero, its keys
+ * count in the softmax all the same, and outputs beside a larger one may be off. out must
+ * not overlap q. Other arguments, supported groups, errors and launches as pa_decode.
  */
 size_t pa_decode_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format);
 
@@ -398,13 +399,13 @@ pa_status pa_decode_bs8(const pa_shape* shape, int32_t kv_format, const void* q,
 
 /*
  * Chunks of new tokens over the block-scaled pool: pa_decode_multi (causal within the
- * chunk), with chunks of any length: drafted tokens to verify, or a prompt (chunked
- * prefill -- thewebvale "vLLM & High-Throughput Serving", section 4).  max_q_len: the
- * largest n_b of the call (>= 1); a longer chunk is malformed.  Arithmetic as
- * pa_decode_bs8.  NaN or an infinity in a value of the chunk's own tokens makes the rows
- * that see it NaN and no others, and so does a bad block id or scale.  Rows of out outside every chunk are left as they are.
- * out must not overlap q.  After PA_DEVERR_TIMEOUT the rows of the CTAs that gave up are NaN.
- * Two launches: attention, then the merge of split rows.
+ * chunk), with chunks of any length: drafted tokens to verify, or a prompt (chunked prefill
+ * -- thewebvale "vLLM & High-Throughput Serving", section 4). max_q_len: the largest n_b of
+ * the call (>= 1); a longer chunk is malformed. Arithmetic as pa_decode_bs8. NaN or an
+ * infinity in a value of the chunk's own tokens, a block id out of range or a bad scale
+ * makes the rows that see it NaN and no others. Rows of out outside every chunk are left as
+ * they are. out must not overlap q. After PA_DEVERR_TIMEOUT the rows of the CTAs that gave
+ * up are NaN. Two launches: attention, then the merge of split rows.
  */
 size_t pa_decode_multi_bs8_workspace_bytes(const pa_shape* shape, int32_t kv_format, int32_t max_q_len);
 

@@ -17,8 +17,8 @@
 // that no new token falls in are read only when the scale rises.
 //
 // Bound by HBM where there is enough to do.  Measured on GB300, heads of 128 in blocks of 16: packing 4096
-// blocks of 8 heads 58 us (6.9 TB/s); 16 prompts of up to 2047 tokens 21.5 us a call (4.7 TB/s: launch, one
-// wave of loads, and half the warps without a block because lengths differ); one token of 256
+// blocks of 8 heads 58 us (6.9 TB/s); 16 prompts of up to 2047 tokens 21.5 to 23.1 us a call (4.4 to 4.7 TB/s: launch,
+// one wave of loads, and half the warps without a block because lengths differ); one token of 256
 // sequences 7 us, four loads that wait on one another.  777 blocks of 32 tokens and 8 heads of 64 are
 // unpacked in 12 us.  Registers are held to four blocks of threads per SM: the prompts took 32 us at two,
 // with nothing spilled.

@@ -45,12 +45,12 @@
 //   1 warp           copies: a bulk copy per block for its keys, one for its values
 //
 // Bound by the chain of a stage within a tile, not by a unit: at 256 rows and head_dim 128 a stage
-// takes 5,400 cycles, of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
+// takes 5,800 cycles (5,400 before l added up rounded weights, when this was stamped), of which 2,700 are products of both tiles and 1,100 exponentials; a tile's
 // scores (700), their way to the softmax (200), two halves (1,000 to 1,800 each, the loads
 // 300 of it), the last products and their way back (700) follow one another, and the tiles'
 // warps share issue slots with the conversion (530 of 2,600 instructions of a stage).
-// Measured on GB300: 987 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
-// 128 (836 TFLOP/s of 1,905); 589 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
+// Measured on GB300: 981 to 987 us for 4096 new tokens of one sequence at context 8192, 64 query and 8 KV heads of
+// 128 (840 TFLOP/s of 1,905); 576 to 591 us for 128 sequences of 1 to 16 new tokens at contexts of 1024
 // to 8192 (2.2 TB/s).  Also measured, against 1,060 us and 636: 64-key products ahead of the
 // softmax (1,470 us for the long prompt), scores of one stage in one piece (1,175), two softmax
 // warps to a row (1,250), codes loaded into registers from L2 (1,160), the conversion unrolled over
@@ -829,7 +829,6 @@ pa_chunk_bs8_kernel(const MultiParams mp) {
                         ok = false;
                         break;
                     }
-                    
                     tc_fence_after();
                     if (fresh) rf = rowf[((cur_seg - 1) & 1) * 2 * Tr::TILE + row_of_group];
                     if (SPLIT && t == 1 && fresh && cur_seg > 1) {    // tile 0 has read the last segment's O

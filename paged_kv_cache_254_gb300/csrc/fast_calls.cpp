@@ -1,5 +1,6 @@
-// The host side of the tree-speculation calls and of those on the block-scaled 8-bit cache, compiled: argument checks, output
-// allocation and the call into libpa for arguments that are all in order.
+// The host side of the tree-speculation calls and of those on the block-scaled 8-bit cache,
+// compiled: argument checks, output allocation and the call into libpa for arguments that are
+// all in order.
 //
 // These kernels run for 2 to 20 microseconds, and the same steps take 10 to 20 in
 // Python.  Each function here takes its Python namesake's arguments in order and
