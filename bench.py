@@ -48,12 +48,12 @@ FALLBACK_HBM_GBS = 6800.0
 # workload or kernel instantiation) reports null.
 #   (hash, kv dtype, workload): (captured dram bytes, algorithmic bytes of the captured launch)
 TRAFFIC = {
-    ("f1214767ababa837", "bf16", "llama3_70b_b256"): (1_217_302_272 + 7_294_976, 1_216_111_324),
-    ("f1214767ababa837", "fp8_e4m3", "llama3_70b_b256"): (609_424_128 + 7_066_112, 609_141_468),
-    ("f1214767ababa837", "int4", "llama3_70b_b256"): (324_384_000 + 4_621_312, 324_624_348),
+    ("26441dd90e863f79", "bf16", "llama3_70b_b256"): (1_217_332_992 + 7_192_320, 1_216_111_324),
+    ("26441dd90e863f79", "fp8_e4m3", "llama3_70b_b256"): (609_409_280 + 7_089_664, 609_141_468),
+    ("26441dd90e863f79", "int4", "llama3_70b_b256"): (324_336_896 + 4_473_600, 324_624_348),
 }
 
-KERNEL_SOURCES = ("decode_kernel.cuh", "decode_common.cuh", "decode_tok.cuh", "ptx.cuh")
+KERNEL_SOURCES = ("decode_kernel.cuh", "decode_common.cuh", "decode_tok.cuh", "decode_bs8.cuh", "bs8.cuh", "ptx.cuh")
 
 
 def kernel_hash() -> str:
